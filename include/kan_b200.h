@@ -320,6 +320,42 @@ KAN_API kan_status kan_ukan_generate_backward(const kan_ukan_shape* s, const flo
 KAN_API kan_status kan_input_range(int64_t n, const void* x, int32_t dtype, float* minmax, void* workspace,
                                    size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Embedding lookup with scaling: the layer that turns token ids into the rows
+ * that KAN layers take.  No counterpart on the pages.
+ *   y[t, :]  = scale * W[ids[t], :]
+ *   dW[v, :] = scale * sum over the t with ids[t] = v of dY[t, :]
+ * The sum runs in one fixed order (tokens ordered by id, ascending t, joined
+ * at fixed borders), without atomic adds, in fp32, rounded once: bitwise
+ * reproducible.  Rows of dW without a token are 0, and so is the row
+ * padding_idx (its tokens give no gradient; the forward reads it like any
+ * other row).  Ids outside 0..rows-1 are found on the device: their rows of y
+ * are 0, they give no gradient, and KAN_ERR_DEVICE_CHECK is recorded for
+ * kan_sync_status().
+ *
+ * Layouts (row-major): ids [tokens] int32 or int64; W [rows, dim], y and dY
+ * [tokens, dim] in the operand dtype; dW [rows, dim] in grad_dtype,
+ * overwritten.  W, y, dY, dW and the workspace 16-byte aligned; any dim.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+    int64_t tokens;       /* >= 0 */
+    int64_t rows;         /* of the table, >= 1 */
+    int64_t dim;          /* >= 1 */
+    int64_t padding_idx;  /* a row without a gradient, or -1 */
+    float scale;          /* finite */
+    int32_t dtype;        /* kan_dtype of W, y, dY */
+    int32_t grad_dtype;   /* kan_dtype of dW */
+    int32_t id_bytes;     /* 4 or 8 */
+} kan_embed_shape;
+
+/* Bytes of workspace that kan_embed_backward needs. */
+KAN_API kan_status kan_embed_workspace_size(const kan_embed_shape* s, size_t* bytes);
+
+KAN_API kan_status kan_embed_forward(const kan_embed_shape* s, const void* ids, const void* W, void* y, void* stream);
+
+KAN_API kan_status kan_embed_backward(const kan_embed_shape* s, const void* ids, const void* dY, void* dW,
+                                      void* workspace, size_t ws_bytes, void* stream);
+
 /* Static description of a status code. */
 KAN_API const char* kan_status_string(kan_status st);
 

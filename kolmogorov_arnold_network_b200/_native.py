@@ -23,6 +23,7 @@ EXPORTS = ("kan_abi_version", "kan_workspace_size", "kan_forward", "kan_backward
            "kan_grkan_workspace_size", "kan_grkan_forward", "kan_grkan_backward",
            "kan_ukan_layer_shape", "kan_ukan_generate", "kan_ukan_workspace_size", "kan_ukan_generate_backward",
            "kan_input_range",
+           "kan_embed_workspace_size", "kan_embed_forward", "kan_embed_backward",
            "kan_selftest_wait_timeout", "kan_status_string", "kan_last_error")
 
 
@@ -42,6 +43,12 @@ class kan_ukan_shape(ctypes.Structure):
     _fields_ = [("in_", ctypes.c_int64), ("out", ctypes.c_int64), ("group", ctypes.c_int32),
                 ("pe_dim", ctypes.c_int32), ("hidden", ctypes.c_int32), ("q0", ctypes.c_int32), ("nq", ctypes.c_int32),
                 ("dtype", ctypes.c_int32)]
+
+
+class kan_embed_shape(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("rows", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("padding_idx", ctypes.c_int64), ("scale", ctypes.c_float), ("dtype", ctypes.c_int32),
+                ("grad_dtype", ctypes.c_int32), ("id_bytes", ctypes.c_int32)]
 
 
 class KanError(RuntimeError):
@@ -108,6 +115,13 @@ def load(path: str | None = None):
     lib.kan_set_timing_marks.argtypes = [_vp, _vp]
     lib.kan_ffma_probe.restype = ctypes.c_int
     lib.kan_ffma_probe.argtypes = [ctypes.c_int32, ctypes.c_int64, _vp, ctypes.POINTER(ctypes.c_double), _vp]
+    ep = ctypes.POINTER(kan_embed_shape)
+    lib.kan_embed_workspace_size.restype = ctypes.c_int
+    lib.kan_embed_workspace_size.argtypes = [ep, ctypes.POINTER(ctypes.c_size_t)]
+    lib.kan_embed_forward.restype = ctypes.c_int
+    lib.kan_embed_forward.argtypes = [ep, _vp, _vp, _vp, _vp]
+    lib.kan_embed_backward.restype = ctypes.c_int
+    lib.kan_embed_backward.argtypes = [ep, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
     if path is None:
         _lib = lib
     return lib
@@ -200,6 +214,26 @@ def kan_ukan_generate_backward(shape, W1, W2, pre, dcoef, dW1, db1, dW2, db2, wo
 
 def kan_input_range(n, x, dtype, minmax, workspace, ws_bytes, stream):
     check(load().kan_input_range(int(n), x, int(dtype), minmax, workspace, ws_bytes, stream), "kan_input_range")
+
+
+def make_embed_shape(tokens, rows, dim, padding_idx, scale, dtype, grad_dtype, id_bytes) -> kan_embed_shape:
+    return kan_embed_shape(int(tokens), int(rows), int(dim), int(padding_idx), float(scale), int(dtype),
+                           int(grad_dtype), int(id_bytes))
+
+
+def kan_embed_workspace_size(shape: kan_embed_shape) -> int:
+    n = ctypes.c_size_t(0)
+    check(load().kan_embed_workspace_size(ctypes.byref(shape), ctypes.byref(n)), "kan_embed_workspace_size")
+    return n.value
+
+
+def kan_embed_forward(shape, ids, W, y, stream):
+    check(load().kan_embed_forward(ctypes.byref(shape), ids, W, y, stream), "kan_embed_forward")
+
+
+def kan_embed_backward(shape, ids, dY, dW, workspace, ws_bytes, stream):
+    check(load().kan_embed_backward(ctypes.byref(shape), ids, dY, dW, workspace, ws_bytes, stream),
+          "kan_embed_backward")
 
 
 def kan_set_timing_marks(after_prep, after_dcoef):

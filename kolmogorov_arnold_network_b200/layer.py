@@ -377,6 +377,98 @@ class UKANLayer(torch.nn.Module):
         return y.reshape(*lead, self.out_features)
 
 
+# ---------------------------------------------------------------------------
+# Sequence operators around the layers: embedding, gated linear recurrence, distillation loss
+def _same_device(ref, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != ref.device:
+            raise ValueError(f"{name} is on {t.device}, expected {ref.device}")
+
+
+def _id_bytes(ids, name="ids"):
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"{name} has dtype {ids.dtype}, expected int32 or int64")
+    return 4 if ids.dtype == torch.int32 else 8
+
+
+def embed_forward(ids, weight, scale=1.0, y=None):
+    """y[..., :] = scale * weight[ids[...], :]; ids int32 or int64 of any shape, weight [rows, dim].  An id outside the
+    table gives a row of zeros and is reported by the device status (``_native.kan_sync_status``)."""
+    _check(weight, "weight")
+    _check(ids, "ids")
+    if weight.dim() != 2:
+        raise ValueError("weight must be [rows, dim]")
+    rows, dim = weight.shape
+    code = _code(weight)
+    s = N.make_embed_shape(ids.numel(), rows, dim, -1, scale, code, code, _id_bytes(ids))
+    if y is None:
+        y = torch.empty((*ids.shape, dim), dtype=weight.dtype, device=weight.device)
+    _check(y, "y", weight.dtype, (*ids.shape, dim))
+    _same_device(weight, ids=ids, y=y)
+    with torch.cuda.device(weight.device):
+        N.kan_embed_forward(s, _p(ids), _p(weight), _p(y), _stream(weight))
+    return y
+
+
+def embed_backward(ids, dY, rows, scale=1.0, padding_idx=None, grad_dtype=torch.float32, out=None, ws=None):
+    """dW [rows, dim] = scale * the sum of dY's rows by id, in one fixed order (tokens sorted by id); ``grad_dtype``
+    float32 or bfloat16 (rounded once).  The row ``padding_idx`` and rows without a token are 0."""
+    _check(ids, "ids")
+    _check(dY, "dY")
+    if dY.dim() < 1 or tuple(dY.shape[:-1]) != tuple(ids.shape):
+        raise ValueError(f"dY has shape {tuple(dY.shape)}, expected {tuple(ids.shape)} and the row length")
+    dim = dY.shape[-1]
+    if out is not None:
+        grad_dtype = out.dtype
+    if grad_dtype not in _DT:
+        raise TypeError(f"grad_dtype {grad_dtype} not supported (float32 or bfloat16)")
+    s = N.make_embed_shape(ids.numel(), rows, dim, -1 if padding_idx is None else padding_idx, scale, _code(dY),
+                           _DT[grad_dtype], _id_bytes(ids))
+    if out is None:
+        out = torch.empty((rows, dim), dtype=grad_dtype, device=dY.device)
+    _check(out, "out", grad_dtype, (rows, dim))
+    _same_device(dY, ids=ids, out=out, ws=ws)
+    with torch.cuda.device(dY.device):
+        if ws is None:
+            ws = torch.empty(max(16, N.kan_embed_workspace_size(s)), dtype=torch.uint8, device=dY.device)
+        N.kan_embed_backward(s, _p(ids), _p(dY), _p(out), _p(ws), ws.numel(), _stream(dY))
+    return out
+
+
+class _EmbedFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, ids, weight, scale, padding_idx):
+        ids, weight = ids.contiguous(), weight.contiguous()
+        ctx.save_for_backward(ids)
+        ctx.meta = (weight.shape[0], scale, padding_idx, weight.dtype)
+        return embed_forward(ids, weight, scale)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dY):
+        (ids,) = ctx.saved_tensors
+        rows, scale, padding_idx, dtype = ctx.meta
+        dW = (embed_backward(ids, dY.contiguous(), rows, scale, padding_idx, grad_dtype=dtype)
+              if ctx.needs_input_grad[1] else None)
+        return None, dW, None, None
+
+
+class TokenEmbedding(torch.nn.Module):
+    """Rows of a table by token id, times ``scale`` (by default 1): the input of a stack of KAN layers.  The gradient
+    is summed in a fixed order, in fp32, and given in the table's dtype; ``padding_idx`` gets none."""
+
+    def __init__(self, rows, dim, scale=1.0, padding_idx=None, dtype=torch.float32, device=None):
+        super().__init__()
+        if padding_idx is not None and not 0 <= padding_idx < rows:
+            raise ValueError("padding_idx must be a row of the table")
+        self.scale, self.padding_idx = float(scale), padding_idx
+        self.weight = torch.nn.Parameter(torch.randn(rows, dim, dtype=torch.float32, device=device)
+                                         .mul_(dim ** -0.5).to(dtype))
+
+    def forward(self, ids):
+        return _EmbedFunction.apply(ids, self.weight, self.scale, self.padding_idx)
+
+
 class KANNetwork(torch.nn.Module):
     """Stack of KANLayer: ``KANNetwork([784, 64, 10])``."""
 

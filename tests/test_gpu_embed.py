@@ -1,0 +1,209 @@
+"""Embedding lookup with scaling and its gradient by sorted tokens, through the C ABI on the GPU.
+
+Bars, per element, from the roundings that happen: the lookup rounds the
+product in fp32 and once to the output type; a gradient of n rows makes n
+fp32 additions, one product and one rounding to the gradient's type, so its
+error is at most (n + 1) half steps of fp32 times the sum of the magnitudes,
+plus half a step of the result's type (each to first order, hence the factor
+1.01).
+"""
+import numpy as np
+import pytest
+import torch
+
+from kolmogorov_arnold_network_b200 import _native as N
+from kolmogorov_arnold_network_b200 import layer as L
+
+from test_gpu_guard import Guarded
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+U32 = 2.0 ** -24
+
+
+def half(dt):
+    return torch.finfo(dt).eps / 2
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+
+
+def _ids(n, rows, kind, seed, dtype=torch.int64):
+    g = torch.Generator().manual_seed(seed)
+    if kind == "uniform":
+        t = torch.randint(0, rows, (n,), generator=g)
+    elif kind == "one":
+        t = torch.full((n,), rows - 1)
+    else:                                  # frequencies fall as 1/rank
+        t = (torch.exp(torch.rand(n, generator=g, dtype=torch.float64) * np.log(rows + 1.0)) - 1).long().clamp_(0, rows - 1)
+    return t.to(dtype)
+
+
+def _grad_ref(ids, dY, rows, scale, padding_idx=None):
+    """(dW, sum of magnitudes, rows per id) in fp64."""
+    ids = ids.reshape(-1).long()
+    dY = dY.reshape(ids.numel(), -1).double()
+    keep = (ids >= 0) & (ids < rows)
+    if padding_idx is not None:
+        keep &= ids != padding_idx
+    ids, dY = ids[keep], dY[keep]
+    w = torch.zeros(rows, dY.shape[1], dtype=torch.float64).index_add_(0, ids, dY)
+    mag = torch.zeros_like(w).index_add_(0, ids, dY.abs())
+    return w * scale, mag * abs(scale), torch.bincount(ids, minlength=rows)
+
+
+def _check_grad(got, ids, dY, rows, scale, padding_idx=None):
+    w, mag, n = _grad_ref(ids.cpu(), dY.cpu(), rows, scale, padding_idx)
+    bar = 1.01 * ((n[:, None] + 1) * U32 * mag + half(got.dtype) * w.abs())
+    if got.dtype == torch.bfloat16:        # the rounded value may lie a step further where the sum's error moves it
+        bar = bar + half(got.dtype) * (n[:, None] + 1) * U32 * mag
+    err = (got.cpu().double() - w).abs()
+    assert bool((err <= bar).all()), float((err - bar).max())
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("idt", [torch.int32, torch.int64])
+@pytest.mark.parametrize("n,rows,dim", [(1, 1, 1), (1, 7, 768), (64, 1000, 768), (33, 129, 771), (5, 300, 2050), (1000, 50, 12),
+                                        (257, 5000, 6), (2, 3, 4097)])
+def test_lookup(dt, idt, n, rows, dim):
+    torch.manual_seed(n + dim)
+    W = torch.randn(rows, dim).to(DT[dt])
+    ids = _ids(n, rows, "uniform", 1, idt)
+    for scale in (1.0, dim ** 0.5, -0.37):
+        y = L.embed_forward(ids.cuda(), W.cuda(), scale)
+        s32 = float(np.float32(scale))
+        ref = W.double()[ids.long()] * s32
+        bar = 1.01 * (half(DT[dt]) + U32) * ref.abs()
+        assert bool(((y.cpu().double() - ref).abs() <= bar).all())
+    assert N.kan_sync_status(None) == 0
+
+
+GRAD = [
+    # n, rows, dim, ids
+    (1, 1, 1, "uniform"), (1, 300, 768, "uniform"), (64, 64, 64, "one"), (65, 1000, 771, "one"), (129, 5, 8, "uniform"),
+    (1000, 50257, 24, "zipf"), (8192, 5000, 96, "zipf"), (4097, 3, 130, "uniform"), (20000, 700, 33, "zipf"),
+    (33000, 2, 12, "one"), (640, 10, 1030, "uniform"),
+]
+
+
+@pytest.mark.parametrize("dt,gdt", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32"), ("f32", "bf16")])
+@pytest.mark.parametrize("case", GRAD, ids=lambda c: "n{}_v{}_d{}_{}".format(*c))
+def test_gradient(dt, gdt, case):
+    n, rows, dim, kind = case
+    torch.manual_seed(n)
+    ids = _ids(n, rows, kind, n)
+    dY = torch.randn(n, dim).to(DT[dt])
+    scale = 1.75
+    got = L.embed_backward(ids.cuda(), dY.cuda(), rows, scale, grad_dtype=DT[gdt])
+    _check_grad(got, ids, dY, rows, scale)
+    assert N.kan_sync_status(None) == 0
+
+
+@pytest.mark.parametrize("n,rows", [(300, 400_001), (5000, 700_000)])
+def test_gradient_large_table(n, rows):
+    """More rows than 256 sort blocks hold bins for."""
+    ids = _ids(n, rows, "uniform", 3)
+    dY = torch.randn(n, 4)
+    _check_grad(L.embed_backward(ids.cuda(), dY.cuda(), rows), ids, dY, rows, 1.0)
+
+
+def test_gradient_int32_shape_and_padding():
+    ids = _ids(6 * 50, 40, "zipf", 5, torch.int32).reshape(6, 50)
+    dY = torch.randn(6, 50, 40)
+    for pad in (0, 3, 39):
+        got = L.embed_backward(ids.cuda(), dY.cuda(), 40, 2.0, padding_idx=pad)
+        _check_grad(got, ids, dY, 40, 2.0, pad)
+        assert bool((got[pad] == 0).all())
+
+
+def test_bad_ids_are_reported_and_skipped():
+    ids = torch.tensor([0, 5, -1, 4, 1 << 40, 5, -(1 << 40)])
+    W = torch.randn(5, 16)
+    y = L.embed_forward(ids.cuda(), W.cuda())
+    assert N.kan_sync_status(None) == 6
+    ref = torch.zeros(7, 16)
+    ref[0], ref[3] = W[0], W[4]
+    assert torch.equal(y.cpu(), ref)
+    dY = torch.randn(7, 16)
+    got = L.embed_backward(ids.cuda(), dY.cuda(), 5)
+    assert N.kan_sync_status(None) == 6
+    _check_grad(got, ids, dY, 5, 1.0)
+    assert N.kan_sync_status(None) == 0
+
+
+def test_no_tokens():
+    ids = torch.empty(0, dtype=torch.int64, device="cuda")
+    assert L.embed_forward(ids, torch.randn(3, 5, device="cuda")).shape == (0, 5)
+    dW = L.embed_backward(ids, torch.empty(0, 5, device="cuda"), 3, out=torch.full((3, 5), 7.0, device="cuda"))
+    assert bool((dW == 0).all())
+
+
+def test_nonfinite_rows_stay_in_their_rows():
+    ids = torch.tensor([1, 2, 1, 3] * 40)
+    dY = torch.randn(160, 8)
+    dY[5] = float("nan")                      # a token of row 2
+    got = L.embed_backward(ids.cuda(), dY.cuda(), 6).cpu()
+    assert bool(got[2].isnan().all()) and bool(got[[0, 1, 3, 4, 5]].isfinite().all())
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_deterministic(dt):
+    ids = _ids(30000, 1200, "zipf", 9).cuda()
+    dY = torch.randn(30000, 136, device="cuda").to(DT[dt])
+    first = L.embed_backward(ids, dY, 1200, grad_dtype=DT[dt])
+    for _ in range(5):
+        assert torch.equal(first, L.embed_backward(ids, dY, 1200, grad_dtype=DT[dt]))
+
+
+@pytest.mark.parametrize("n,rows,dim", [(130, 37, 771), (64, 300, 96), (1000, 3, 5)])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_guard_bands(dt, n, rows, dim):
+    ids = _ids(n, rows, "zipf", 2).cuda()
+    W = torch.randn(rows, dim, device="cuda").to(DT[dt])
+    dY = torch.randn(n, dim, device="cuda").to(DT[dt])
+    y, dW = Guarded((n, dim), DT[dt]), Guarded((rows, dim), DT[dt])
+    s = N.make_embed_shape(n, rows, dim, -1, 1.0, L._code(W), L._code(W), 8)
+    ws = Guarded((N.kan_embed_workspace_size(s),), torch.uint8)
+    L.embed_forward(ids, W, y=y.t)
+    L.embed_backward(ids, dY, rows, out=dW.t, ws=ws.t)
+    torch.cuda.synchronize()
+    y.check("y")
+    dW.check("dW")
+    ws.check("workspace", all_written=False)
+
+
+def test_module_gradient_and_capture():
+    m = L.TokenEmbedding(100, 24, scale=3.0, padding_idx=0, device="cuda")
+    ids = _ids(4 * 30, 100, "zipf", 4).reshape(4, 30).cuda()
+    g = torch.randn(4, 30, 24, device="cuda")
+    (m(ids) * g).sum().backward()
+    _check_grad(m.weight.grad, ids, g, 100, 3.0, 0)
+    # captured and replayed with other ids, next to a second captured graph (workspaces are each graph's own)
+    graphs = []
+    for k in range(2):
+        i, d = ids.clone(), g.clone()
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            out = L.embed_backward(i, d, 100)
+        graphs.append((gr, i, d, out))
+    for k, (gr, i, d, out) in enumerate(graphs):
+        i.copy_(_ids(120, 100, "uniform", 50 + k).reshape(4, 30))
+        gr.replay()
+    torch.cuda.synchronize()
+    for gr, i, d, out in graphs:
+        _check_grad(out, i, d, 100, 1.0)
+
+
+def test_other_stream():
+    ids = _ids(2000, 64, "zipf", 8).cuda()
+    dY = torch.randn(2000, 40, device="cuda")
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        got = L.embed_backward(ids, dY, 64)
+    st.synchronize()
+    _check_grad(got, ids, dY, 64, 1.0)

@@ -1,0 +1,66 @@
+"""Refusals of the sequence operators (embedding, gated linear recurrence, distillation loss) on the host: every call
+below fails before anything is launched, so no GPU is needed."""
+import ctypes
+
+import pytest
+import torch
+
+from kolmogorov_arnold_network_b200 import _native as N
+from kolmogorov_arnold_network_b200 import build as B
+from kolmogorov_arnold_network_b200 import layer as L
+
+FAKE = 0x7F0000000000  # 16-byte aligned, never dereferenced
+
+
+@pytest.fixture(scope="module")
+def lib():
+    B.build()
+    return N.load()
+
+
+def embed(**kw):
+    d = dict(tokens=16, rows=100, dim=32, padding_idx=-1, scale=1.0, dtype=0, grad_dtype=0, id_bytes=8)
+    d.update(kw)
+    return N.make_embed_shape(**d)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(tokens=-1), 1), (dict(rows=0), 1), (dict(dim=0), 1), (dict(padding_idx=-2), 1), (dict(padding_idx=100), 1),
+    (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1), (dict(dtype=2), 1), (dict(grad_dtype=-1), 1),
+    (dict(id_bytes=2), 1), (dict(tokens=1 << 31), 2), (dict(rows=1 << 31), 2), (dict(dim=1 << 22), 2),
+])
+def test_embed_bad_shapes(lib, kw, code):
+    s = ctypes.byref(embed(**kw))
+    n = ctypes.c_size_t(0)
+    assert lib.kan_embed_workspace_size(s, ctypes.byref(n)) == code
+    assert lib.kan_embed_forward(s, FAKE, FAKE, FAKE, None) == code
+    assert lib.kan_embed_backward(s, FAKE, FAKE, FAKE, FAKE, 1 << 40, None) == code
+    assert lib.kan_last_error().decode() != ""
+
+
+def test_embed_bad_pointers_and_workspace(lib):
+    s = ctypes.byref(embed())
+    n = ctypes.c_size_t(0)
+    assert lib.kan_embed_workspace_size(s, ctypes.byref(n)) == 0 and n.value > 0
+    assert lib.kan_embed_workspace_size(s, None) == 1
+    assert lib.kan_embed_forward(None, FAKE, FAKE, FAKE, None) == 1
+    for a in ((None, FAKE, FAKE), (FAKE, None, FAKE), (FAKE, FAKE, None)):
+        assert lib.kan_embed_forward(s, *a, None) == 1
+        assert lib.kan_embed_backward(s, *a, FAKE, n.value, None) == 1
+    for a in ((FAKE + 4, FAKE, FAKE), (FAKE, FAKE + 8, FAKE), (FAKE, FAKE, FAKE + 2)):
+        assert lib.kan_embed_forward(s, *a, None) == 2
+        assert lib.kan_embed_backward(s, *a, FAKE, n.value, None) == 2
+    assert lib.kan_embed_backward(s, FAKE, FAKE, FAKE, None, 0, None) == 3
+    assert lib.kan_embed_backward(s, FAKE, FAKE, FAKE, FAKE, n.value - 1, None) == 3
+
+
+def test_embed_python_refusals():
+    ids = torch.zeros(3, dtype=torch.int64)
+    with pytest.raises(ValueError, match="CUDA"):
+        L.embed_forward(ids, torch.zeros(4, 8))
+    with pytest.raises(ValueError, match="CUDA"):
+        L.embed_backward(ids, torch.zeros(3, 8), 4)
+    with pytest.raises(TypeError, match="int32 or int64"):
+        L._id_bytes(torch.zeros(3))
+    with pytest.raises(ValueError, match="padding_idx"):
+        L.TokenEmbedding(4, 8, padding_idx=4)
