@@ -356,6 +356,51 @@ KAN_API kan_status kan_embed_forward(const kan_embed_shape* s, const void* ids, 
 KAN_API kan_status kan_embed_backward(const kan_embed_shape* s, const void* ids, const void* dY, void* dW,
                                       void* workspace, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Gated linear recurrence: mixes the steps of a sequence, channel by channel,
+ * next to KAN layers, which mix channels.  No counterpart on the pages.
+ * With lambda_c = softplus(decay[c]):
+ *   a_t = exp(-lambda_c sigmoid(r_t)),  m_t = sqrt(1 - a_t^2)
+ *   h_t = a_t h_{t-1} + m_t sigmoid(g_t) x_t,   y_t = h_t
+ * h_{-1} is h0 (0 if NULL).  Where reset[b, t] is not 0, h_{t-1} counts as 0,
+ * whatever it holds (inf and NaN too): several documents in one row.
+ * time = 1 is the form for one new token: h_last may be h0 itself.
+ * Backward, for dy and dh_last: dx, dr, dg, ddecay, dh0; any may be NULL.
+ * States and sums are fp32 (ddecay's sums fp64), in one fixed order, without
+ * atomic adds: bitwise reproducible.
+ *
+ * Layouts: x, r, g [batch, time, channels] in the operand dtype, channels
+ * contiguous, with their own strides (in elements) of sequence and step, so
+ * that they may be slices of one tensor; y, dy, dx, dr, dg dense in the
+ * operand dtype; decay, ddecay [channels], h0, h_last, dh_last, dh0
+ * [batch, channels] float32; reset [batch, time] bytes, or NULL.
+ * kept [batch, ceil(time / KAN_GLR_STEPS), channels] float32: the states that
+ * the forward keeps for the backward (NULL: none).  Operands need the
+ * alignment of their elements only; any channels.
+ * ------------------------------------------------------------------------ */
+#define KAN_GLR_STEPS 8
+
+typedef struct {
+    int64_t batch, time;             /* >= 0 */
+    int64_t channels;                /* >= 1 */
+    int64_t x_stride_b, x_stride_t;  /* elements, >= 0 */
+    int64_t r_stride_b, r_stride_t;
+    int64_t g_stride_b, g_stride_t;
+    int32_t dtype;                   /* kan_dtype of x, r, g, y and their gradients */
+} kan_glr_shape;
+
+/* Bytes of workspace that kan_glr_backward needs for ddecay. */
+KAN_API kan_status kan_glr_workspace_size(const kan_glr_shape* s, size_t* bytes);
+
+KAN_API kan_status kan_glr_forward(const kan_glr_shape* s, const void* x, const void* r, const void* g,
+                                   const float* decay, const unsigned char* reset, const float* h0, void* y,
+                                   float* h_last, float* kept, void* stream);
+
+KAN_API kan_status kan_glr_backward(const kan_glr_shape* s, const void* x, const void* r, const void* g,
+                                    const float* decay, const unsigned char* reset, const float* kept, const void* dy,
+                                    const float* dh_last, void* dx, void* dr, void* dg, float* ddecay, float* dh0,
+                                    void* workspace, size_t ws_bytes, void* stream);
+
 /* Static description of a status code. */
 KAN_API const char* kan_status_string(kan_status st);
 

@@ -24,6 +24,7 @@ EXPORTS = ("kan_abi_version", "kan_workspace_size", "kan_forward", "kan_backward
            "kan_ukan_layer_shape", "kan_ukan_generate", "kan_ukan_workspace_size", "kan_ukan_generate_backward",
            "kan_input_range",
            "kan_embed_workspace_size", "kan_embed_forward", "kan_embed_backward",
+           "kan_glr_workspace_size", "kan_glr_forward", "kan_glr_backward",
            "kan_selftest_wait_timeout", "kan_status_string", "kan_last_error")
 
 
@@ -49,6 +50,13 @@ class kan_embed_shape(ctypes.Structure):
     _fields_ = [("tokens", ctypes.c_int64), ("rows", ctypes.c_int64), ("dim", ctypes.c_int64),
                 ("padding_idx", ctypes.c_int64), ("scale", ctypes.c_float), ("dtype", ctypes.c_int32),
                 ("grad_dtype", ctypes.c_int32), ("id_bytes", ctypes.c_int32)]
+
+
+class kan_glr_shape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("time", ctypes.c_int64), ("channels", ctypes.c_int64),
+                ("x_stride_b", ctypes.c_int64), ("x_stride_t", ctypes.c_int64),
+                ("r_stride_b", ctypes.c_int64), ("r_stride_t", ctypes.c_int64),
+                ("g_stride_b", ctypes.c_int64), ("g_stride_t", ctypes.c_int64), ("dtype", ctypes.c_int32)]
 
 
 class KanError(RuntimeError):
@@ -122,6 +130,13 @@ def load(path: str | None = None):
     lib.kan_embed_forward.argtypes = [ep, _vp, _vp, _vp, _vp]
     lib.kan_embed_backward.restype = ctypes.c_int
     lib.kan_embed_backward.argtypes = [ep, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+    rp = ctypes.POINTER(kan_glr_shape)
+    lib.kan_glr_workspace_size.restype = ctypes.c_int
+    lib.kan_glr_workspace_size.argtypes = [rp, ctypes.POINTER(ctypes.c_size_t)]
+    lib.kan_glr_forward.restype = ctypes.c_int
+    lib.kan_glr_forward.argtypes = [rp] + [_vp] * 10
+    lib.kan_glr_backward.restype = ctypes.c_int
+    lib.kan_glr_backward.argtypes = [rp] + [_vp] * 14 + [ctypes.c_size_t, _vp]
     if path is None:
         _lib = lib
     return lib
@@ -234,6 +249,31 @@ def kan_embed_forward(shape, ids, W, y, stream):
 def kan_embed_backward(shape, ids, dY, dW, workspace, ws_bytes, stream):
     check(load().kan_embed_backward(ctypes.byref(shape), ids, dY, dW, workspace, ws_bytes, stream),
           "kan_embed_backward")
+
+
+#: steps between the states that kan_glr_forward keeps for kan_glr_backward
+KAN_GLR_STEPS = 8
+
+
+def make_glr_shape(batch, time, channels, x_strides, r_strides, g_strides, dtype) -> kan_glr_shape:
+    return kan_glr_shape(batch, time, channels, *x_strides, *r_strides, *g_strides, dtype)
+
+
+def kan_glr_workspace_size(shape: kan_glr_shape) -> int:
+    n = ctypes.c_size_t(0)
+    check(load().kan_glr_workspace_size(ctypes.byref(shape), ctypes.byref(n)), "kan_glr_workspace_size")
+    return n.value
+
+
+def kan_glr_forward(shape, x, r, g, decay, reset, h0, y, h_last, kept, stream):
+    check(load().kan_glr_forward(ctypes.byref(shape), x, r, g, decay, reset, h0, y, h_last, kept, stream),
+          "kan_glr_forward")
+
+
+def kan_glr_backward(shape, x, r, g, decay, reset, kept, dy, dh_last, dx, dr, dg, ddecay, dh0, workspace, ws_bytes,
+                     stream):
+    check(load().kan_glr_backward(ctypes.byref(shape), x, r, g, decay, reset, kept, dy, dh_last, dx, dr, dg, ddecay,
+                                  dh0, workspace, ws_bytes, stream), "kan_glr_backward")
 
 
 def kan_set_timing_marks(after_prep, after_dcoef):

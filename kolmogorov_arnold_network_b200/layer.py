@@ -7,6 +7,8 @@ of the layer itself runs in libkan_b200.so.
 """
 from __future__ import annotations
 
+import math
+
 import torch
 
 from . import _native as N
@@ -467,6 +469,121 @@ class TokenEmbedding(torch.nn.Module):
 
     def forward(self, ids):
         return _EmbedFunction.apply(ids, self.weight, self.scale, self.padding_idx)
+
+
+def _glr_operand(t, name, x):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device != x.device:
+        raise ValueError(f"{name} is on {t.device}, expected {x.device}")
+    if t.dtype != x.dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {x.dtype}")
+    if t.shape != x.shape or t.dim() != 3:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [batch, time, channels] as x")
+    sb, st, sc = t.stride()
+    if sc != 1 and t.shape[2] > 1:
+        raise ValueError(f"{name}'s channels must be contiguous")
+    return sb, st
+
+
+def _glr_shape(x, r, g, decay, reset):
+    strides = [_glr_operand(t, nm, x) for t, nm in ((x, "x"), (r, "r"), (g, "g"))]
+    B, T, C = x.shape
+    _check(decay, "decay", torch.float32, (C,))
+    if reset is not None and reset.dtype not in (torch.bool, torch.uint8):
+        raise TypeError(f"reset has dtype {reset.dtype}, expected bool or uint8")
+    _check(reset, "reset", None, (B, T))
+    _same_device(x, decay=decay, reset=reset)
+    return N.make_glr_shape(B, T, C, *strides, _code(x))
+
+
+def glr_forward(x, r, g, decay, h0=None, reset=None, keep=False, y=None, h_last=None):
+    """(y, h_last, kept) of the gated linear recurrence h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(g_t) x_t,
+    a_t = exp(-softplus(decay) sigmoid(r_t)), y_t = h_t, over x, r, g [batch, time, channels] (channels contiguous, other
+    strides free), decay [channels] and h0 [batch, channels] float32.  Where ``reset`` [batch, time] (bool or uint8) is
+    set the state starts from 0 again.  With ``keep`` the states for ``glr_backward`` come in ``kept``, else None.
+    For one new token pass time = 1 and h_last=h0 to update the state in place."""
+    s = _glr_shape(x, r, g, decay, reset)
+    B, T, C = x.shape
+    if y is None:
+        y = torch.empty((B, T, C), dtype=x.dtype, device=x.device)
+    if h_last is None:
+        h_last = torch.empty((B, C), dtype=torch.float32, device=x.device)
+    kept = (torch.empty((B, -(-T // N.KAN_GLR_STEPS), C), dtype=torch.float32, device=x.device) if keep else None)
+    _check(h0, "h0", torch.float32, (B, C))
+    _check(y, "y", x.dtype, (B, T, C))
+    _check(h_last, "h_last", torch.float32, (B, C))
+    _same_device(x, h0=h0, y=y, h_last=h_last)
+    with torch.cuda.device(x.device):
+        N.kan_glr_forward(s, _p(x), _p(r), _p(g), _p(decay), _p(reset), _p(h0), _p(y), _p(h_last), _p(kept), _stream(x))
+    return y, h_last, kept
+
+
+def glr_backward(x, r, g, decay, kept, dY, reset=None, dh_last=None, need=(True,) * 5, ws=None):
+    """(dx, dr, dg, ddecay, dh0) for upstream dY [batch, time, channels] and dh_last [batch, channels] (None: 0), from
+    the states ``kept`` by ``glr_forward``; ``need`` says which are wanted (None is returned for the others)."""
+    s = _glr_shape(x, r, g, decay, reset)
+    B, T, C = x.shape
+    _check(kept, "kept", torch.float32, (B, -(-T // N.KAN_GLR_STEPS), C))
+    _check(dY, "dY", x.dtype, (B, T, C))
+    _check(dh_last, "dh_last", torch.float32, (B, C))
+    _same_device(x, kept=kept, dY=dY, dh_last=dh_last, ws=ws)
+    dx, dr, dg = (torch.empty((B, T, C), dtype=x.dtype, device=x.device) if n else None for n in need[:3])
+    ddecay = torch.empty_like(decay) if need[3] else None
+    dh0 = torch.empty((B, C), dtype=torch.float32, device=x.device) if need[4] else None
+    with torch.cuda.device(x.device):
+        if ws is None and ddecay is not None:
+            ws = torch.empty(max(16, N.kan_glr_workspace_size(s)), dtype=torch.uint8, device=x.device)
+        N.kan_glr_backward(s, _p(x), _p(r), _p(g), _p(decay), _p(reset), _p(kept), _p(dY), _p(dh_last), _p(dx), _p(dr),
+                           _p(dg), _p(ddecay), _p(dh0), _p(ws), 0 if ws is None else ws.numel(), _stream(x))
+    return dx, dr, dg, ddecay, dh0
+
+
+class _GLRFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, r, g, decay, h0, reset):
+        ctx.set_materialize_grads(False)
+        x, r, g = (t if t.stride(-1) == 1 else t.contiguous() for t in (x, r, g))
+        h0 = None if h0 is None else h0.contiguous()
+        reset = None if reset is None else reset.contiguous()
+        y, h_last, kept = glr_forward(x, r, g, decay, h0, reset, keep=any(ctx.needs_input_grad[:5]))
+        ctx.save_for_backward(x, r, g, decay, kept, reset)
+        return y, h_last
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dY, dh_last):
+        x, r, g, decay, kept, reset = ctx.saved_tensors
+        if dY is None and dh_last is None:
+            return (None,) * 6
+        dY = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dY is None else dY.contiguous()
+        dh_last = None if dh_last is None else dh_last.contiguous()
+        return (*glr_backward(x, r, g, decay, kept, dY, reset, dh_last, need=ctx.needs_input_grad[:5]), None)
+
+
+class GatedLinearRecurrence(torch.nn.Module):
+    """Gated linear recurrence over the steps of a sequence, channel by channel, for use next to KAN layers (which mix
+    channels).  ``decay`` [channels] (float32) sets each channel's memory: it is drawn so that softplus(decay) spreads
+    from 2/``longest`` to 1 (the memory at r = 0 from 2 to ``longest`` steps)."""
+
+    def __init__(self, channels, longest=1000.0, device=None):
+        super().__init__()
+        if channels < 1 or longest <= 2:
+            raise ValueError("channels >= 1 and longest > 2")
+        self.channels = channels
+        lam = torch.exp(torch.rand(channels, dtype=torch.float32, device=device) * math.log(2.0 / longest))
+        self.decay = torch.nn.Parameter(torch.log(torch.expm1(lam)))
+
+    def forward(self, x, r, g, h0=None, reset=None):
+        """(y, h_last) for x, r, g [batch, time, channels]."""
+        return _GLRFunction.apply(x, r, g, self.decay, h0, reset)
+
+    def step(self, x, r, g, h):
+        """y for one new token (x, r, g [batch, channels]); the state h [batch, channels] float32 is updated in place.
+        For serving: no gradient."""
+        with torch.no_grad():
+            y, _, _ = glr_forward(x.unsqueeze(1), r.unsqueeze(1), g.unsqueeze(1), self.decay, h, h_last=h)
+        return y.squeeze(1)
 
 
 class KANNetwork(torch.nn.Module):

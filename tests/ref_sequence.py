@@ -1,0 +1,88 @@
+"""Plain references of the sequence operators in 64 bits (torch on the CPU), written from the formulas and
+differentiable, with magnitudes for error bounds."""
+import torch
+
+
+def glr(x, r, g, decay, h0=None, reset=None):
+    """(y, h_last) of the gated linear recurrence; inputs any dtype, computed in fp64."""
+    x, r, g, decay = (t.double() for t in (x, r, g, decay))
+    B, T, C = x.shape
+    h = torch.zeros(B, C, dtype=torch.float64) if h0 is None else h0.double()
+    lam = torch.nn.functional.softplus(decay, threshold=60)
+    out = []
+    for t in range(T):
+        log_a = -lam * torch.sigmoid(r[:, t])
+        if reset is not None:
+            h = torch.where(reset[:, t, None].bool(), torch.zeros_like(h), h)
+        m = torch.sqrt(-torch.expm1(2 * log_a))
+        h = torch.exp(log_a) * h + m * torch.sigmoid(g[:, t]) * x[:, t]
+        out.append(h)
+    return torch.stack(out, 1) if out else x.clone(), h
+
+
+def glr_bounds(x, r, g, decay, h0, reset, dy, dh_last):
+    """Magnitudes to which one fp32 half step (times a constant) bounds each output's error, by propagating the
+    roundings of every step through the recurrence: {name: tensor}."""
+    x, r, g, decay = (t.detach().double() for t in (x, r, g, decay))
+    B, T, C = x.shape
+    lam = torch.nn.functional.softplus(decay, threshold=60)
+    s, sg = torch.sigmoid(r), torch.sigmoid(g)
+    L = -lam * s
+    a = torch.exp(L)
+    em = -torch.expm1(L)
+    m = torch.sqrt(-torch.expm1(2 * L))
+    u = (sg * x).abs()
+    cut = torch.zeros(B, T, dtype=torch.bool) if reset is None else reset.bool()
+    h = torch.zeros(B, C, dtype=torch.float64) if h0 is None else h0.detach().double()
+    mh = h.abs() * 0
+    before, mbefore, my, hs = [], [], [], []
+    for t in range(T):
+        c = cut[:, t, None]
+        h, mh = torch.where(c, 0.0, h), torch.where(c, 0.0, mh)
+        before.append(h)
+        mbefore.append(mh)
+        hn = a[:, t] * h + m[:, t] * sg[:, t] * x[:, t]
+        # em carries a relative error, so do the input term and the sum
+        mh = a[:, t] * mh + em[:, t] * h.abs() + m[:, t] * u[:, t] + hn.abs() + h.abs()
+        h = hn
+        my.append(mh)
+    d = [None] * T
+    md = [None] * T
+    flow = torch.zeros(B, C, dtype=torch.float64) if dh_last is None else dh_last.double()
+    mflow = flow.abs() * 0
+    for t in range(T - 1, -1, -1):
+        d[t] = dy[:, t].double() + flow
+        md[t] = mflow + d[t].abs() + dy[:, t].double().abs()
+        keep = (~cut[:, t, None]).double()
+        flow = a[:, t] * d[t] * keep
+        mflow = (a[:, t] * md[t] + em[:, t] * d[t].abs() + d[t].abs()) * keep
+    before, mbefore, my, d, md = (torch.stack(v, 1) for v in (before, mbefore, my, d, md))
+    rm = torch.where(m > 0, 1 / m, 0.0)
+    inner = before.abs() + a * u * rm
+    # per element: the value's own relative roundings and what d and h bring with them
+    mdl = L.abs() * a * ((md + d.abs()) * inner + d.abs() * mbefore)
+    ratio = torch.sigmoid(decay) / lam
+    return {"y": my, "h_last": my[:, -1], "dx": (md + d.abs()) * m * sg, "dg": (md + d.abs()) * m * u * (1 - sg),
+            "dr": mdl * (1 - s), "ddecay": (mdl.sum((0, 1)) * ratio), "dh0": mflow}
+
+
+def distill(z, ids, teacher, temp=1.0, weight=None):
+    """Per-row loss: w T^2 sum_k p_k (log p_k - log q_{id_k}) over the valid slots, in fp64."""
+    n, vocab = z.shape
+    z = z.double() / temp
+    ids = ids.long()
+    t = teacher.double() / temp
+    there = (ids >= 0) & (ids < vocab) & (t != -float("inf"))
+    w = torch.ones(n, dtype=torch.float64) if weight is None else weight.double()
+    rows = []
+    for i in range(n):
+        ok = there[i]
+        if w[i] == 0 or not bool(ok.any()):
+            rows.append((z[i] * 0).nan_to_num().sum() * 0)
+            continue
+        logp = torch.log_softmax(t[i][ok], 0)
+        logq = z[i] - torch.logsumexp(z[i], 0)
+        p = torch.exp(logp)
+        use = p > 0
+        rows.append(w[i] * temp * temp * (p[use] * (logp[use] - logq[ids[i][ok][use]])).sum())
+    return torch.stack(rows) if rows else torch.zeros(0, dtype=torch.float64)

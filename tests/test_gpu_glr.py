@@ -1,0 +1,310 @@
+"""Gated linear recurrence on the GPU (forward, backward, single step) against the fp64 reference.
+
+Bars, per element: KAPPA half steps of fp32 times the magnitude that
+ref_sequence.glr_bounds propagates through the recurrence, plus half a step of
+the output's type.  KAPPA counts the half steps of one recurrence step: a - 1
+from r (exp 4, its argument's product up to |r| / 2 <= 8 at these inputs, sum
+and reciprocal 4, softplus 8, product 1, expm1 up to 8), the input term
+(square root half of that and 4, the other sigmoid 16, products 3), the
+composition of maps (3 each): below 64 for each of them, and the gradients
+multiply at most two such quantities: KAPPA = 128.
+"""
+import pytest
+import torch
+
+from kolmogorov_arnold_network_b200 import _native as N
+from kolmogorov_arnold_network_b200 import layer as L
+
+import ref_sequence as ref
+from test_gpu_guard import Guarded
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+KAPPA = 128
+U32 = 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+
+
+def draw(B, T, C, dt, seed=0, h0=True, reset=None, wide=False):
+    g = torch.Generator().manual_seed(seed)
+    std = 6.0 if wide else 1.0
+    d = {k: (torch.randn(B, T, C, generator=g) * (1.0 if k in "x dy" else std)).clamp(-16, 16).to(DT[dt])
+         for k in ("x", "r", "g", "dy")}
+    d["decay"] = torch.empty(C).uniform_(-6.0, 2.0, generator=g)
+    d["h0"] = torch.randn(B, C, generator=g) if h0 else None
+    d["dh_last"] = torch.randn(B, C, generator=g) if h0 else None
+    d["reset"] = None
+    if reset == "some":
+        d["reset"] = torch.rand(B, T, generator=g) < 0.05
+    elif reset == "all":
+        d["reset"] = torch.ones(B, T, dtype=torch.bool)
+    elif reset == "first":
+        d["reset"] = torch.zeros(B, T, dtype=torch.bool)
+        d["reset"][:, 0] = True
+    return d
+
+
+def reference(d):
+    leaf = {k: d[k].double().requires_grad_() for k in ("x", "r", "g", "decay")}
+    h0 = torch.zeros(d["x"].shape[0], d["x"].shape[2]) if d["h0"] is None else d["h0"]
+    leaf["h0"] = h0.double().requires_grad_()
+    y, h = ref.glr(leaf["x"], leaf["r"], leaf["g"], leaf["decay"], leaf["h0"], d["reset"])
+    total = (y * d["dy"].double()).sum()
+    if d["dh_last"] is not None:
+        total = total + (h * d["dh_last"].double()).sum()
+    grads = torch.autograd.grad(total, [leaf[k] for k in ("x", "r", "g", "decay", "h0")])
+    return dict(zip(("y", "h_last", "dx", "dr", "dg", "ddecay", "dh0"), (y.detach(), h.detach(), *grads)))
+
+
+def cuda(t):
+    return None if t is None else t.cuda()
+
+
+def run(d, strided=False):
+    x, r, g = (d[k].cuda() for k in "xrg")
+    if strided:                                  # slices of one projection, with room around them
+        C = x.shape[-1]
+        buf = torch.full((*x.shape[:2], 3 * C + 2), float("nan"), dtype=x.dtype, device="cuda")
+        views = [buf[..., i * C:(i + 1) * C] for i in range(3)]
+        for v, t in zip(views, (x, r, g)):
+            v.copy_(t)
+        x, r, g = views
+    args = (x, r, g, d["decay"].cuda())
+    y, h, kept = L.glr_forward(*args, h0=cuda(d["h0"]), reset=cuda(d["reset"]), keep=True)
+    grads = L.glr_backward(*args, kept, d["dy"].cuda(), reset=cuda(d["reset"]), dh_last=cuda(d["dh_last"]))
+    torch.cuda.synchronize()
+    assert N.kan_sync_status(None) == 0
+    return dict(zip(("y", "h_last", "dx", "dr", "dg", "ddecay", "dh0"), (y, h, *grads)))
+
+
+def check(got, want, bounds):
+    for k, w in want.items():
+        v = got[k].cpu()
+        half = torch.finfo(v.dtype).eps / 2
+        bar = KAPPA * U32 * bounds[k] + half * (w.abs() + KAPPA * U32 * bounds[k]) + 1e-37
+        err = (v.double() - w).abs()
+        assert bool((err <= bar).all()), (k, float((err / bar.clamp(min=1e-300)).max()), float(err.max()))
+
+
+def bounds_of(d):
+    return ref.glr_bounds(d["x"], d["r"], d["g"], d["decay"], d["h0"], d["reset"], d["dy"], d["dh_last"])
+
+
+CASES = [
+    # B, T, C
+    (1, 1, 1), (2, 1, 768), (64, 1, 40), (3, 7, 5), (1, 8, 64), (2, 9, 66), (5, 2, 33), (1, 511, 32), (1, 512, 33),
+    (2, 513, 100), (1, 1500, 7), (2, 1025, 130), (1, 4099, 65), (40, 64, 192),
+]
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "b{}_t{}_c{}".format(*c))
+def test_parity(dt, case):
+    d = draw(*case, dt, seed=sum(case))
+    check(run(d), reference(d), bounds_of(d))
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("reset", ["some", "all", "first"])
+@pytest.mark.parametrize("case", [(2, 130, 34), (1, 1, 3), (3, 700, 64)], ids=lambda c: "b{}_t{}_c{}".format(*c))
+def test_resets(dt, reset, case):
+    d = draw(*case, dt, seed=5, reset=reset)
+    check(run(d), reference(d), bounds_of(d))
+    d["reset"] = d["reset"].to(torch.uint8) * 3           # any byte that is not 0
+    check(run(d), reference(d), bounds_of(d))
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_strided_wide_gates_and_no_state(dt):
+    for C in (32, 45, 66):
+        d = draw(2, 600, C, dt, seed=C, h0=False, wide=True)
+        check(run(d, strided=True), reference(d), bounds_of(d))
+
+
+def test_broadcast_inputs():
+    """Inputs that repeat along time or batch (stride 0)."""
+    d = draw(3, 40, 16, "f32", seed=2)
+    full = {**d, "r": d["r"][:1, :1].expand(3, 40, 16)}
+    y, h, _ = L.glr_forward(d["x"].cuda(), full["r"][:1, :1].cuda().expand(3, 40, 16), d["g"].cuda(), d["decay"].cuda(),
+                            h0=d["h0"].cuda())
+    want = reference(full)
+    check({"y": y, "h_last": h}, {k: want[k] for k in ("y", "h_last")}, bounds_of(full))
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_reset_clears_inf_and_nan(dt):
+    """What a reset cuts off reaches neither the states nor the gradients of the steps before it."""
+    for T, at in ((5, 3), (600, 300), (600, 64)):
+        d = draw(2, T, 33, dt, seed=9)
+        d["reset"] = torch.zeros(2, T, dtype=torch.bool)
+        d["reset"][:, at] = True
+        clean = run(d)
+        d["x"][0, at - 1, 4] = float("inf")
+        d["x"][1, at - 2, 5] = float("nan")
+        got = run(d)
+        assert torch.equal(got["y"][:, at:], clean["y"][:, at:])
+        assert torch.equal(got["h_last"], clean["h_last"])
+        d = draw(2, T, 33, dt, seed=9)
+        d["reset"] = torch.zeros(2, T, dtype=torch.bool)
+        d["reset"][:, at] = True
+        d["dy"][0, at, 3] = float("inf")
+        d["dy"][1, T - 1, 7] = float("nan")
+        got = run(d)
+        for k in ("dx", "dr", "dg"):
+            assert torch.equal(got[k][:, :at], clean[k][:, :at]), k
+        assert torch.equal(got["dh0"], clean["dh0"])
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_extreme_gates_stay_finite(dt):
+    """Gates far out on both sides: a = 1 and a = 0 to all bits, no NaN; compared where the values are normal numbers."""
+    d = draw(1, 64, 8, dt, seed=1)
+    vals = torch.tensor([-300.0, -100.0, -30.0, 0.0, 30.0, 100.0, 300.0, -79.0])
+    d["r"] = vals.repeat(64, 1)[None].to(DT[dt])
+    d["g"] = vals.flip(0).repeat(64, 1)[None].to(DT[dt])
+    d["decay"] = torch.tensor([-40.0, -20.0, 0.0, 20.0, 90.0, -90.0, 1.0, 3.0])
+    got = run(d)
+    assert all(bool(v.isfinite().all()) for v in got.values())
+    want, bounds = reference(d), bounds_of(d)
+    # the sigmoid is held at e^-80 (2e-35) below -80: what that moves is below 1e-15 in every output
+    for k, w in want.items():
+        v = got[k].cpu()
+        half = torch.finfo(v.dtype).eps / 2
+        bar = KAPPA * 4 * U32 * bounds[k].nan_to_num() + half * w.abs().nan_to_num() * 1.01 + 1e-15
+        ok = w.isfinite()
+        assert bool(((v.double() - w).abs() <= bar)[ok].all()), k
+
+
+def test_no_steps():
+    x = torch.empty(2, 0, 4, device="cuda")
+    h0 = torch.randn(2, 4, device="cuda")
+    decay = torch.zeros(4, device="cuda")
+    y, h, kept = L.glr_forward(x, x, x, decay, h0=h0, keep=True)
+    assert y.shape == (2, 0, 4) and torch.equal(h, h0)
+    dx, dr, dg, dd, dh0 = L.glr_backward(x, x, x, decay, kept, x, dh_last=h0)
+    assert torch.equal(dh0, h0) and bool((dd == 0).all())
+    y, h, _ = L.glr_forward(x, x, x, decay)
+    assert bool((h == 0).all())
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_steps_one_by_one(dt):
+    """The single-token form walks to the states of the whole sequence."""
+    d = draw(4, 20, 70, dt, seed=3)
+    m = L.GatedLinearRecurrence(70, device="cuda")
+    with torch.no_grad():
+        m.decay.copy_(d["decay"])
+    h = d["h0"].cuda().clone()
+    ys = torch.stack([m.step(*(d[k][:, t].contiguous().cuda() for k in "xrg"), h) for t in range(20)], 1)
+    want = reference(d)
+    check({"y": ys, "h_last": h}, {k: want[k] for k in ("y", "h_last")}, bounds_of(d))
+
+
+def test_reference_against_differences():
+    d = draw(1, 6, 3, "f32", seed=11, reset="some")
+    leaves = [d[k].double().requires_grad_() for k in ("x", "r", "g", "decay", "h0")]
+    assert torch.autograd.gradcheck(lambda *a: ref.glr(*a, d["reset"]), leaves, eps=1e-6, atol=1e-7, rtol=1e-6)
+
+
+def test_gradient_against_differences():
+    """d loss along a direction in the inputs, from two forwards of the kernel itself: fp32 values of y carry errors of
+    about 1e-6, a step of 2^-6 leaves a truncation error of its square, so 2e-3 of the gradient's norm is ample."""
+    d = draw(2, 300, 32, "f32", seed=12, reset="some")
+    got = run(d)
+    gen = torch.Generator().manual_seed(1)
+    for name, grad in (("x", "dx"), ("r", "dr"), ("g", "dg"), ("decay", "ddecay"), ("h0", "dh0")):
+        v = torch.randn(d[name].shape, generator=gen)
+        eps = 2.0 ** -6
+
+        def loss(sign):
+            e = {**d, name: d[name] + sign * eps * v}
+            y, h, _ = L.glr_forward(*(e[k].cuda() for k in ("x", "r", "g", "decay")), h0=e["h0"].cuda(), reset=e["reset"].cuda())
+            return float((y.double().cpu() * d["dy"].double()).sum() + (h.double().cpu() * d["dh_last"].double()).sum())
+
+        diff = (loss(1) - loss(-1)) / (2 * eps)
+        want = float((got[grad].cpu().double() * v.double()).sum())
+        scale = float((got[grad].cpu().double().norm() * v.double().norm()))
+        assert abs(diff - want) <= 2e-3 * scale, (name, diff, want, scale)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_deterministic(dt):
+    d = draw(3, 2000, 72, dt, seed=4, reset="some")
+    first = run(d)
+    for _ in range(3):
+        again = run(d)
+        assert all(torch.equal(first[k], again[k]) for k in first)
+
+
+@pytest.mark.parametrize("case", [(2, 9, 33), (1, 515, 64), (3, 1, 5)], ids=lambda c: "b{}_t{}_c{}".format(*c))
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_guard_bands(dt, case):
+    B, T, C = case
+    d = draw(B, T, C, dt, seed=6, reset="some")
+    x, r, g, decay, h0, dy, dh = (d[k].cuda() for k in ("x", "r", "g", "decay", "h0", "dy", "dh_last"))
+    reset = d["reset"].cuda()
+    s = L._glr_shape(x, r, g, decay, reset)
+    big = {k: Guarded((B, T, C), DT[dt]) for k in ("y", "dx", "dr", "dg")}
+    small = {k: Guarded((B, C), torch.float32) for k in ("h_last", "dh0")}
+    small["ddecay"] = Guarded((C,), torch.float32)
+    small["kept"] = Guarded((B, -(-T // 8), C), torch.float32)
+    ws = Guarded((N.kan_glr_workspace_size(s),), torch.uint8)
+    p = {k: v.t.data_ptr() for k, v in (*big.items(), *small.items())}
+    N.kan_glr_forward(s, x.data_ptr(), r.data_ptr(), g.data_ptr(), decay.data_ptr(), reset.data_ptr(), h0.data_ptr(),
+                      p["y"], p["h_last"], p["kept"], None)
+    N.kan_glr_backward(s, x.data_ptr(), r.data_ptr(), g.data_ptr(), decay.data_ptr(), reset.data_ptr(), p["kept"],
+                       dy.data_ptr(), dh.data_ptr(), p["dx"], p["dr"], p["dg"], p["ddecay"], p["dh0"], ws.t.data_ptr(),
+                       ws.n, None)
+    torch.cuda.synchronize()
+    for k, v in (*big.items(), *small.items()):
+        v.check(k)
+    ws.check("workspace", all_written=False)
+
+
+def test_module_autograd():
+    d = draw(2, 50, 24, "f32", seed=8, reset="some")
+    m = L.GatedLinearRecurrence(24, device="cuda")
+    with torch.no_grad():
+        m.decay.copy_(d["decay"])
+    leaf = {k: d[k].cuda().requires_grad_() for k in ("x", "r", "g", "h0")}
+    y, h = m(leaf["x"], leaf["r"], leaf["g"], leaf["h0"], d["reset"].cuda())
+    ((y * d["dy"].cuda()).sum() + (h * d["dh_last"].cuda()).sum()).backward()
+    got = {"y": y.detach(), "h_last": h.detach(), "dx": leaf["x"].grad, "dr": leaf["r"].grad, "dg": leaf["g"].grad,
+           "ddecay": m.decay.grad, "dh0": leaf["h0"].grad}
+    check(got, reference(d), bounds_of(d))
+    # only the last state's gradient, and only some inputs that want one
+    d2 = {**d, "dy": torch.zeros_like(d["dy"])}
+    x = d["x"].cuda().requires_grad_()
+    _, h = m(x, d["r"].cuda(), d["g"].cuda(), d["h0"].cuda(), d["reset"].cuda())
+    (gx,) = torch.autograd.grad((h * d["dh_last"].cuda()).sum(), [x])
+    check({"dx": gx}, {"dx": reference(d2)["dx"]}, bounds_of(d2))
+    # no gradient wanted at all
+    with torch.no_grad():
+        y2, _ = m(x, d["r"].cuda(), d["g"].cuda(), d["h0"].cuda(), d["reset"].cuda())
+    assert torch.equal(y2, y)
+
+
+def test_two_captured_graphs():
+    graphs = []
+    for k in range(2):
+        d = draw(2, 700, 64, "bf16", seed=20 + k)
+        dev = {n: d[n].cuda() for n in ("x", "r", "g", "decay", "h0", "dy", "dh_last")}
+        torch.cuda.synchronize()
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            y, h, kept = L.glr_forward(dev["x"], dev["r"], dev["g"], dev["decay"], h0=dev["h0"], keep=True)
+            grads = L.glr_backward(dev["x"], dev["r"], dev["g"], dev["decay"], kept, dev["dy"], dh_last=dev["dh_last"])
+        graphs.append((gr, d, dev, dict(zip(("y", "h_last", "dx", "dr", "dg", "ddecay", "dh0"), (y, h, *grads)))))
+    for gr, d, dev, out in graphs:
+        d["x"] = torch.randn(2, 700, 64).bfloat16()
+        dev["x"].copy_(d["x"])
+        gr.replay()
+    torch.cuda.synchronize()
+    for gr, d, dev, out in graphs:
+        check(out, reference(d), bounds_of(d))

@@ -64,3 +64,52 @@ def test_embed_python_refusals():
         L._id_bytes(torch.zeros(3))
     with pytest.raises(ValueError, match="padding_idx"):
         L.TokenEmbedding(4, 8, padding_idx=4)
+
+
+def glr(**kw):
+    d = dict(batch=2, time=100, channels=32, x_strides=(3200, 32), r_strides=(3200, 32), g_strides=(3200, 32), dtype=0)
+    d.update(kw)
+    return N.make_glr_shape(**d)
+
+
+def glr_calls(lib, s, p=FAKE, ws=FAKE, wsb=1 << 40):
+    """(forward, backward) with every operand at address p."""
+    return (lib.kan_glr_forward(s, p, p, p, p, p, p, p, p, p, None),
+            lib.kan_glr_backward(s, p, p, p, p, p, p, p, p, p, p, p, p, p, ws, wsb, None))
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(batch=-1), 1), (dict(time=-1), 1), (dict(channels=0), 1), (dict(dtype=5), 1), (dict(x_strides=(-1, 32)), 1),
+    (dict(r_strides=(3200, -32)), 1), (dict(channels=1 << 25), 2), (dict(batch=1 << 30), 2),
+])
+def test_glr_bad_shapes(lib, kw, code):
+    s = ctypes.byref(glr(**kw))
+    n = ctypes.c_size_t(0)
+    assert lib.kan_glr_workspace_size(s, ctypes.byref(n)) == code
+    assert glr_calls(lib, s) == (code, code)
+    assert lib.kan_last_error().decode() != ""
+
+
+def test_glr_bad_pointers_and_workspace(lib):
+    s = ctypes.byref(glr())
+    n = ctypes.c_size_t(0)
+    assert lib.kan_glr_workspace_size(s, ctypes.byref(n)) == 0 and n.value > 0
+    assert lib.kan_glr_workspace_size(s, None) == 1
+    assert glr_calls(lib, None) == (1, 1)
+    assert glr_calls(lib, s, None) == (1, 1)
+    assert glr_calls(lib, s, FAKE + 2) == (2, 2)
+    assert glr_calls(lib, s, FAKE, FAKE + 4)[1] == 2
+    assert glr_calls(lib, s, FAKE, None, 0)[1] == 3
+    assert glr_calls(lib, s, FAKE, FAKE, 16)[1] == 3
+    b16 = ctypes.byref(glr(dtype=1))
+    assert lib.kan_glr_forward(b16, FAKE + 1, FAKE, FAKE, FAKE, None, None, FAKE, None, None, None) == 2
+
+
+def test_glr_python_refusals():
+    x = torch.zeros(1, 4, 8)
+    with pytest.raises(ValueError, match="CUDA"):
+        L.glr_forward(x, x, x, torch.zeros(8))
+    with pytest.raises(ValueError):
+        L.GatedLinearRecurrence(0)
+    with pytest.raises(ValueError):
+        L.GatedLinearRecurrence(4, longest=1.0)
