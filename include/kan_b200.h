@@ -401,6 +401,57 @@ KAN_API kan_status kan_glr_backward(const kan_glr_shape* s, const void* x, const
                                     const float* dh_last, void* dx, void* dr, void* dg, float* ddecay, float* dh0,
                                     void* workspace, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Distillation from a teacher's top logits: the loss that fits a model with
+ * KAN layers in place of its linear ones ("Drop-in Replacement", InKAN landing
+ * page) to the outputs of the model it came from.  No counterpart on the
+ * pages.  Row n has the student's logits z over the vocabulary and the
+ * teacher's `entries` kept logits t_k at tokens id_k; with temperature T and
+ * over the entries that count,
+ *   p = softmax(t / T),  q = softmax(z / T)
+ *   loss[n] = weight[n] T^2 sum_k p_k (log p_k - log q_{id_k})
+ *   dz_v    = dloss[n] weight[n] T (q_v - sum_{k: id_k = v} p_k)
+ * An entry does not count if its id is negative (an empty place) or its logit
+ * is -inf; an id >= vocab does not count either and is reported
+ * (KAN_ERR_DEVICE_CHECK by kan_sync_status).  The same id may occur more than
+ * once.  A row of weight 0, or without an entry that counts, has loss 0 and
+ * gradient 0, and its logits are not looked at (they may be NaN).  A row
+ * of -inf alone that counts gives NaN.
+ * Sums are fp32 in one fixed order, without atomic adds: bitwise reproducible.
+ *
+ * Layouts: z [rows, vocab] and dz in the operand dtype, rows ld and ld_grad
+ * elements apart (>= vocab), dz may be z itself (with ld_grad = ld); ids
+ * [rows, entries] int32 or int64; teacher [rows, entries], weight, dloss, loss
+ * [rows] float32 (weight, dloss NULL: 1); stats [rows, 2] float32, 8-byte
+ * aligned: what the backward needs of the forward (the row's maximum m and
+ * the sum of exp((z - m) / T)).  Operands need the alignment of their elements
+ * only.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+    int64_t rows;         /* >= 0 */
+    int64_t vocab;        /* >= 1 */
+    int64_t ld, ld_grad;  /* row strides of z and dz (elements) */
+    int32_t entries;      /* teacher entries per row, 1..1024 */
+    int32_t id_bytes;     /* 4 or 8 */
+    float temperature;    /* > 0, finite */
+    int32_t dtype;        /* kan_dtype of z, dz */
+} kan_distill_shape;
+
+/* The rows' losses and stats. */
+KAN_API kan_status kan_distill_forward(const kan_distill_shape* s, const void* z, const void* ids, const float* teacher,
+                                       const float* weight, float* loss, float* stats, void* stream);
+
+/* dz from the stats of the forward. */
+KAN_API kan_status kan_distill_backward(const kan_distill_shape* s, const void* z, const void* ids, const float* teacher,
+                                        const float* weight, const float* stats, const float* dloss, void* dz,
+                                        void* stream);
+
+/* Both at once, for a training step whose loss is the sum of loss[] (dloss = 1): the logits are read once where a row
+ * fits the shared memory of a cluster. */
+KAN_API kan_status kan_distill_loss_grad(const kan_distill_shape* s, const void* z, const void* ids,
+                                         const float* teacher, const float* weight, float* loss, float* stats, void* dz,
+                                         void* stream);
+
 /* Static description of a status code. */
 KAN_API const char* kan_status_string(kan_status st);
 

@@ -25,6 +25,7 @@ EXPORTS = ("kan_abi_version", "kan_workspace_size", "kan_forward", "kan_backward
            "kan_input_range",
            "kan_embed_workspace_size", "kan_embed_forward", "kan_embed_backward",
            "kan_glr_workspace_size", "kan_glr_forward", "kan_glr_backward",
+           "kan_distill_forward", "kan_distill_backward", "kan_distill_loss_grad",
            "kan_selftest_wait_timeout", "kan_status_string", "kan_last_error")
 
 
@@ -57,6 +58,12 @@ class kan_glr_shape(ctypes.Structure):
                 ("x_stride_b", ctypes.c_int64), ("x_stride_t", ctypes.c_int64),
                 ("r_stride_b", ctypes.c_int64), ("r_stride_t", ctypes.c_int64),
                 ("g_stride_b", ctypes.c_int64), ("g_stride_t", ctypes.c_int64), ("dtype", ctypes.c_int32)]
+
+
+class kan_distill_shape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("vocab", ctypes.c_int64), ("ld", ctypes.c_int64), ("ld_grad", ctypes.c_int64),
+                ("entries", ctypes.c_int32), ("id_bytes", ctypes.c_int32), ("temperature", ctypes.c_float),
+                ("dtype", ctypes.c_int32)]
 
 
 class KanError(RuntimeError):
@@ -137,6 +144,13 @@ def load(path: str | None = None):
     lib.kan_glr_forward.argtypes = [rp] + [_vp] * 10
     lib.kan_glr_backward.restype = ctypes.c_int
     lib.kan_glr_backward.argtypes = [rp] + [_vp] * 14 + [ctypes.c_size_t, _vp]
+    dp = ctypes.POINTER(kan_distill_shape)
+    lib.kan_distill_forward.restype = ctypes.c_int
+    lib.kan_distill_forward.argtypes = [dp] + [_vp] * 7
+    lib.kan_distill_backward.restype = ctypes.c_int
+    lib.kan_distill_backward.argtypes = [dp] + [_vp] * 8
+    lib.kan_distill_loss_grad.restype = ctypes.c_int
+    lib.kan_distill_loss_grad.argtypes = [dp] + [_vp] * 8
     if path is None:
         _lib = lib
     return lib
@@ -274,6 +288,25 @@ def kan_glr_backward(shape, x, r, g, decay, reset, kept, dy, dh_last, dx, dr, dg
                      stream):
     check(load().kan_glr_backward(ctypes.byref(shape), x, r, g, decay, reset, kept, dy, dh_last, dx, dr, dg, ddecay,
                                   dh0, workspace, ws_bytes, stream), "kan_glr_backward")
+
+
+def make_distill_shape(rows, vocab, ld, ld_grad, entries, id_bytes, temperature, dtype) -> kan_distill_shape:
+    return kan_distill_shape(rows, vocab, ld, ld_grad, entries, id_bytes, temperature, dtype)
+
+
+def kan_distill_forward(shape, z, ids, teacher, weight, loss, stats, stream):
+    check(load().kan_distill_forward(ctypes.byref(shape), z, ids, teacher, weight, loss, stats, stream),
+          "kan_distill_forward")
+
+
+def kan_distill_backward(shape, z, ids, teacher, weight, stats, dloss, dz, stream):
+    check(load().kan_distill_backward(ctypes.byref(shape), z, ids, teacher, weight, stats, dloss, dz, stream),
+          "kan_distill_backward")
+
+
+def kan_distill_loss_grad(shape, z, ids, teacher, weight, loss, stats, dz, stream):
+    check(load().kan_distill_loss_grad(ctypes.byref(shape), z, ids, teacher, weight, loss, stats, dz, stream),
+          "kan_distill_loss_grad")
 
 
 def kan_set_timing_marks(after_prep, after_dcoef):

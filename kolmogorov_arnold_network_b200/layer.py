@@ -586,6 +586,118 @@ class GatedLinearRecurrence(torch.nn.Module):
         return y.squeeze(1)
 
 
+def _rows_of(t, name):
+    """Row stride of a [rows, vocab] tensor whose elements of a row are contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [rows, vocab]")
+    if t.stride(1) != 1 and t.shape[1] > 1:
+        raise ValueError(f"{name}'s rows must be contiguous")
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name}'s rows overlap")
+    return max(t.stride(0), t.shape[1])
+
+
+def _distill_shape(z, ids, teacher, temperature, weight, dz=None):
+    ld = _rows_of(z, "logits")
+    n, vocab = z.shape
+    _check(ids, "ids")
+    _check(teacher, "teacher", torch.float32)
+    if ids.dim() != 2 or ids.shape[0] != n:
+        raise ValueError(f"ids has shape {tuple(ids.shape)}, expected [{n}, entries]")
+    _check(teacher, "teacher", torch.float32, tuple(ids.shape))
+    _check(weight, "weight", torch.float32, (n,))
+    ld_grad = vocab
+    if dz is not None:
+        ld_grad = _rows_of(dz, "dlogits")
+        if dz.dtype != z.dtype or dz.shape != z.shape:
+            raise ValueError("dlogits must have the logits' shape and dtype")
+    _same_device(z, ids=ids, teacher=teacher, weight=weight, dlogits=dz)
+    return N.make_distill_shape(n, vocab, ld, ld_grad, ids.shape[1], _id_bytes(ids), temperature, _code(z))
+
+
+def distill_forward(logits, ids, teacher, temperature=1.0, weight=None):
+    """(loss [rows], stats [rows, 2]) of the student's logits [rows, vocab] (rows contiguous, any row stride) against a
+    teacher's top logits ``teacher`` [rows, entries] (float32) at tokens ``ids`` [rows, entries] (int32 or int64; a
+    negative id is an empty place): loss[n] = weight[n] T^2 KL(softmax(teacher / T) || softmax(logits / T)), the teacher's
+    distribution over its entries, the student's over the vocabulary.  ``stats`` goes to ``distill_backward``."""
+    s = _distill_shape(logits, ids, teacher, temperature, weight)
+    loss = torch.empty(s.rows, dtype=torch.float32, device=logits.device)
+    stats = torch.empty((s.rows, 2), dtype=torch.float32, device=logits.device)
+    with torch.cuda.device(logits.device):
+        N.kan_distill_forward(s, _p(logits), _p(ids), _p(teacher), _p(weight), _p(loss), _p(stats), _stream(logits))
+    return loss, stats
+
+
+def distill_backward(logits, ids, teacher, stats, temperature=1.0, weight=None, dloss=None, dlogits=None):
+    """dlogits for upstream dloss [rows] (None: 1), in the logits' dtype; ``dlogits`` may be the logits themselves."""
+    if dlogits is None:
+        dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    s = _distill_shape(logits, ids, teacher, temperature, weight, dlogits)
+    _check(stats, "stats", torch.float32, (s.rows, 2))
+    _check(dloss, "dloss", torch.float32, (s.rows,))
+    _same_device(logits, stats=stats, dloss=dloss)
+    with torch.cuda.device(logits.device):
+        N.kan_distill_backward(s, _p(logits), _p(ids), _p(teacher), _p(weight), _p(stats), _p(dloss), _p(dlogits),
+                               _stream(logits))
+    return dlogits
+
+
+def distill_loss_grad(logits, ids, teacher, temperature=1.0, weight=None, dlogits=None):
+    """(loss [rows], dlogits): the losses and the gradient of their sum in one pass over the logits, for a training loop
+    that goes on with ``logits.backward(dlogits)``; ``dlogits`` may be the logits themselves."""
+    if dlogits is None:
+        dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    s = _distill_shape(logits, ids, teacher, temperature, weight, dlogits)
+    loss = torch.empty(s.rows, dtype=torch.float32, device=logits.device)
+    stats = torch.empty((s.rows, 2), dtype=torch.float32, device=logits.device)
+    with torch.cuda.device(logits.device):
+        N.kan_distill_loss_grad(s, _p(logits), _p(ids), _p(teacher), _p(weight), _p(loss), _p(stats), _p(dlogits),
+                                _stream(logits))
+    return loss, dlogits
+
+
+class _DistillFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, ids, teacher, temperature, weight):
+        logits = logits if logits.stride(-1) == 1 else logits.contiguous()
+        loss, stats = distill_forward(logits, ids, teacher, temperature, weight)
+        ctx.save_for_backward(logits, ids, teacher, stats, weight)
+        ctx.temperature = temperature
+        return loss
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dloss):
+        logits, ids, teacher, stats, weight = ctx.saved_tensors
+        if not ctx.needs_input_grad[0]:
+            return (None,) * 5
+        return distill_backward(logits, ids, teacher, stats, ctx.temperature, weight, dloss.contiguous()), None, None, None, None
+
+
+class TopLogitDistillation(torch.nn.Module):
+    """Loss against a teacher's top logits: the rows' T^2 KL(teacher || student) times their weights, as a sum
+    (``reduction="sum"``) or one by one (``"none"``).  Gradients go to the student's logits only."""
+
+    def __init__(self, temperature=1.0, reduction="sum"):
+        super().__init__()
+        if not temperature > 0 or not math.isfinite(temperature):
+            raise ValueError("temperature must be positive and finite")
+        if reduction not in ("sum", "none"):
+            raise ValueError("reduction must be 'sum' or 'none'")
+        self.temperature, self.reduction = float(temperature), reduction
+
+    def forward(self, logits, ids, teacher, weight=None):
+        """logits [..., vocab], ids and teacher [..., entries], weight [...] float32 (None: 1)."""
+        lead, vocab = logits.shape[:-1], logits.shape[-1]
+        ids = ids.reshape(-1, ids.shape[-1]).contiguous()
+        teacher = teacher.detach().reshape(ids.shape).float().contiguous()
+        weight = None if weight is None else weight.detach().reshape(-1).float().contiguous()
+        loss = _DistillFunction.apply(logits.reshape(-1, vocab), ids, teacher, self.temperature, weight)
+        return loss.sum() if self.reduction == "sum" else loss.reshape(lead)
+
+
 class KANNetwork(torch.nn.Module):
     """Stack of KANLayer: ``KANNetwork([784, 64, 10])``."""
 

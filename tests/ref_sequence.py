@@ -81,7 +81,7 @@ def distill(z, ids, teacher, temp=1.0, weight=None):
             rows.append((z[i] * 0).nan_to_num().sum() * 0)
             continue
         logp = torch.log_softmax(t[i][ok], 0)
-        logq = z[i] - torch.logsumexp(z[i], 0)
+        logq = torch.log_softmax(z[i], 0)      # the maximum is taken off first: a row at -3e38 stays exact
         p = torch.exp(logp)
         use = p > 0
         rows.append(w[i] * temp * temp * (p[use] * (logp[use] - logq[ids[i][ok][use]])).sum())

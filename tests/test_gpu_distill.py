@@ -1,0 +1,321 @@
+"""Distillation from a teacher's top logits on the GPU against the fp64 reference.
+
+Bars.  One ex2 of an argument x carries 2 half steps of fp32 per unit in the
+last place (taken as 4) plus the argument's rounding, |x| half steps times
+ln 2 <= |x|; the arguments that matter here are below 64 in magnitude, so a
+term is off by at most 70 half steps of itself and a sum of n such terms in
+32-lane trees and serial parts of n / 512 by n / 512 + 40 more.  p likewise
+(expf, 4 and |x|).  So q and p are off by (150 + n / 512) half steps: KAPPA.  The
+gradient's bar is KAPPA half steps of |c| (q + p) plus half a step of its
+type; the loss's, KAPPA half steps of w T^2 sum p (|log p| + |log q| + 1).
+"""
+import pytest
+import torch
+
+from kolmogorov_arnold_network_b200 import _native as N
+from kolmogorov_arnold_network_b200 import layer as L
+
+import ref_sequence as ref
+from test_gpu_guard import Guarded
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+U32 = 2.0 ** -24
+
+
+def kappa(vocab):
+    return 150 + vocab / 512
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+
+
+def draw(n, vocab, k, dt, seed=0, idt=torch.int64, holes=True, repeat=False, weight=True):
+    g = torch.Generator().manual_seed(seed)
+    z = (torch.randn(n, vocab, generator=g) * 3).to(DT[dt])
+    ids = torch.randint(0, max(1, vocab // 8) if repeat else vocab, (n, k), generator=g)
+    if holes:
+        ids = torch.where(torch.rand(n, k, generator=g) < 0.2, -1 - ids, ids)
+    t = torch.randn(n, k, generator=g) * 3 + 5
+    w = None
+    if weight:
+        w = torch.rand(n, generator=g)
+        w[torch.rand(n, generator=g) < 0.2] = 0
+    return z, ids.to(idt), t, w
+
+
+def reference(z, ids, t, temp, w, dloss=None):
+    zz = z.double().requires_grad_()
+    loss = ref.distill(zz, ids, t, temp, w)
+    (dz,) = torch.autograd.grad((loss * (1 if dloss is None else dloss.double())).sum(), [zz])
+    return loss.detach(), dz
+
+
+def bounds(z, ids, t, temp, w, dloss=None):
+    n, vocab = z.shape
+    w = torch.ones(n).double() if w is None else w.double()
+    ids = ids.long()
+    ok = (ids >= 0) & (ids < vocab) & (t != -float("inf"))
+    tt = (t.double() / temp).masked_fill(~ok, -float("inf"))
+    logp = torch.log_softmax(tt, 1).masked_fill(~ok, 0).nan_to_num(neginf=0)
+    p = torch.where(ok, torch.exp(logp), 0.0)
+    logq = torch.log_softmax(z.double() / temp, 1)
+    at = logq.gather(1, ids.clamp(0, vocab - 1))
+    bl = w.abs() * temp ** 2 * torch.where(p > 0, p * (logp.abs() + at.abs() + 1), 0.0).sum(1)
+    c = w.abs() * temp * (1 if dloss is None else dloss.double().abs())
+    both = torch.exp(logq).scatter_add(1, ids.clamp(0, vocab - 1), p)
+    return bl, c[:, None] * both
+
+
+def check(loss, dz, args, dloss=None):
+    wl, wd = reference(*args, dloss)
+    bl, bd = bounds(*args, dloss)
+    K = kappa(args[0].shape[1]) * U32
+    assert bool(((loss.cpu().double() - wl).abs() <= K * bl + 1e-37).all()), float(((loss.cpu().double() - wl).abs() / (K * bl + 1e-37)).max())
+    half = torch.finfo(dz.dtype).eps / 2
+    err = (dz.cpu().double() - wd).abs()
+    bar = K * bd + half * (wd.abs() + K * bd) + 1e-37
+    assert bool((err <= bar).all()), float((err / bar).max())
+
+
+def run(z, ids, t, temp, w, dloss=None):
+    dev = [None if v is None else v.cuda() for v in (z, ids, t, w)]
+    loss, stats = L.distill_forward(dev[0], dev[1], dev[2], temp, dev[3])
+    dz = L.distill_backward(dev[0], dev[1], dev[2], stats, temp, dev[3], None if dloss is None else dloss.cuda())
+    loss2, dz2 = L.distill_loss_grad(dev[0], dev[1], dev[2], temp, dev[3])
+    return loss, dz, loss2, dz2
+
+
+CASES = [
+    # rows, vocab, entries
+    (1, 1, 1), (3, 2, 2), (5, 7, 3), (4, 8, 1), (7, 33, 5), (3, 513, 64), (6, 1000, 31), (2, 4099, 1024), (9, 27001, 7),
+    (3, 32003, 600), (2, 50257, 64), (3, 65537, 20), (2, 131073, 33), (2, 200000, 256), (1, 300001, 4), (2, 450001, 9),
+    (1, 900001, 3), (300, 515, 4),
+]
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "n{}_v{}_k{}".format(*c))
+def test_parity(dt, case):
+    n, vocab, k = case
+    for temp, idt in ((1.0, torch.int64), (2.5, torch.int32)):
+        z, ids, t, w = draw(n, vocab, k, dt, seed=n + k, idt=idt)
+        if n < 3:
+            w = None
+        args = (z, ids, t, temp, w)
+        loss, dz, loss2, dz2 = run(*args)
+        check(loss, dz, args)
+        check(loss2, dz2, args)
+    assert N.kan_sync_status(None) == 0
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_upstream_and_repeated_ids(dt):
+    for vocab, k in ((40, 100), (5000, 1024), (16, 3)):
+        z, ids, t, w = draw(6, vocab, k, dt, seed=vocab, repeat=True)
+        dloss = torch.randn(6)
+        loss, dz, loss2, dz2 = run(z, ids, t, 0.7, w, dloss)
+        check(loss, dz, (z, ids, t, 0.7, w), dloss)
+        check(loss2, dz2, (z, ids, t, 0.7, w))
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("vocab", [100, 3000, 70000])
+def test_rows_that_do_not_count(dt, vocab):
+    z, ids, t, w = draw(6, vocab, 4, dt, seed=1, holes=False)
+    w = torch.ones(6)
+    w[0] = 0
+    ids[1] = -1
+    t[2] = -float("inf")
+    z[0] = float("nan")
+    z[1] = float("inf")
+    z[2] = -float("inf")
+    t[3, 0] = -float("inf")
+    loss, dz, loss2, dz2 = run(z, ids, t, 1.0, w)
+    for lo, d in ((loss, dz), (loss2, dz2)):
+        assert bool((lo[:3] == 0).all()) and bool((d[:3] == 0).all())
+        check(lo[3:], d[3:], (z[3:], ids[3:], t[3:], 1.0, w[3:]))
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("vocab", [40, 2000, 60001])
+def test_masked_vocabulary(dt, vocab):
+    """Whole stretches of -inf, of the type's lowest value, a single live token; NaN and +inf in a row stay in that row."""
+    z, ids, t, w = draw(6, vocab, 5, dt, seed=2, holes=False, weight=False)
+    lowest = torch.finfo(DT[dt]).min
+    live = torch.arange(vocab) % 2 == 1
+    ids = ids // 2 * 2 + 1
+    ids = ids.clamp(max=vocab - 1 - (vocab % 2))
+    z[0, ~live] = -float("inf")
+    z[1, ~live] = lowest
+    z[2, : vocab // 2] = -float("inf")
+    ids[2] = vocab - 1
+    z[3] = -float("inf")
+    z[3, 17] = 1.0
+    ids[3] = 17
+    args = (z[:4], ids[:4], t[:4], 1.0, None)
+    z[4, 3] = float("nan")
+    z[5, vocab - 2] = float("inf")
+    loss, dz, loss2, dz2 = run(z, ids, t, 1.0, None)
+    for lo, d in ((loss, dz), (loss2, dz2)):
+        wl, wd = reference(*args)
+        wl2 = wl.nan_to_num(posinf=0)
+        K = kappa(vocab) * U32
+        # log q of a token at the type's lowest value is never asked for here; masked tokens carry no gradient
+        assert bool(((lo[:4].cpu().double() - wl2).abs() <= K * 50 * (1 + wl2.abs())).all())
+        half = torch.finfo(d.dtype).eps / 2
+        assert bool(((d[:4].cpu().double() - wd).abs() <= (K + half) * 4).all())
+        assert bool((d[0].cpu()[~live] == 0).all()) and bool((d[1].cpu()[~live] == 0).all())
+        assert bool(lo[4].isnan()) and bool(d[4].isnan().any()) and bool(lo[5].isnan())
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("vocab", [40, 2000, 60001])
+def test_row_at_the_lowest_value(dt, vocab):
+    """A row that a mask fills with the type's lowest value: uniform."""
+    z, ids, t, _ = draw(2, vocab, 3, dt, seed=8, holes=False, weight=False)
+    z[0] = torch.finfo(DT[dt]).min
+    loss, dz, loss2, dz2 = run(z, ids, t, 1.0, None)
+    check(loss, dz, (z, ids, t, 1.0, None))
+    check(loss2, dz2, (z, ids, t, 1.0, None))
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_no_probability_left_at_a_kept_token(dt):
+    """q = 0 at a token with p > 0: the loss is +inf, the gradient finite."""
+    z, ids, t, _ = draw(2, 300, 3, dt, seed=3, holes=False)
+    ids[0] = torch.tensor([5, 6, 7])
+    z[0, 5] = -float("inf")
+    loss, dz, loss2, dz2 = run(z, ids, t, 1.0, None)
+    assert float(loss[0]) == float("inf") and float(loss2[0]) == float("inf") and bool(loss[1].isfinite())
+    assert bool(dz.isfinite().all()) and bool(dz2.isfinite().all())
+
+
+def test_bad_ids_are_reported():
+    z, ids, t, w = draw(3, 50, 4, "f32", holes=False, weight=False)
+    bad = ids.clone()
+    bad[1, 2] = 50
+    bad[2, 0] = 1 << 40
+    loss, dz, loss2, dz2 = run(z, bad, t, 1.0, None)
+    assert N.kan_sync_status(None) == 6
+    ids = torch.where(bad >= 50, -1, bad)
+    check(loss, dz, (z, ids, t, 1.0, None))
+    check(loss2, dz2, (z, ids, t, 1.0, None))
+    assert N.kan_sync_status(None) == 0
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("n,vocab,pad", [(5, 1000, 1), (4, 30001, 7), (3, 70000, 8), (3, 201, 3), (2, 120001, 15)])
+def test_row_strides_and_in_place(dt, n, vocab, pad):
+    z, ids, t, w = draw(n, vocab, 6, dt, seed=pad)
+    wide = torch.full((n, vocab + pad), float("nan"), dtype=DT[dt], device="cuda")
+    view = wide[:, :vocab]
+    view.copy_(z)
+    args = (z, ids, t, 1.5, w)
+    wd = w.cuda()
+    loss, stats = L.distill_forward(view, ids.cuda(), t.cuda(), 1.5, wd)
+    check(loss, L.distill_backward(view, ids.cuda(), t.cuda(), stats, 1.5, wd), args)
+    loss, dz = L.distill_loss_grad(view, ids.cuda(), t.cuda(), 1.5, wd)
+    check(loss, dz, args)
+    # the gradient in the logits' own place, one kernel and two
+    loss, dz = L.distill_loss_grad(view, ids.cuda(), t.cuda(), 1.5, wd, dlogits=view)
+    check(loss, dz, args)
+    assert bool(wide[:, vocab:].isnan().all())
+    view.copy_(z)
+    loss, stats = L.distill_forward(view, ids.cuda(), t.cuda(), 1.5, wd)
+    check(loss, L.distill_backward(view, ids.cuda(), t.cuda(), stats, 1.5, wd, dlogits=view), args)
+    assert bool(wide[:, vocab:].isnan().all())
+    # an address that is only element-aligned, the last row at the end of the buffer
+    flat = torch.empty(1 + n * vocab, dtype=DT[dt], device="cuda")
+    odd = flat[1:].view(n, vocab)
+    odd.copy_(z)
+    loss, dz = L.distill_loss_grad(odd, ids.cuda(), t.cuda(), 1.5, wd)
+    check(loss, dz, args)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("n,vocab", [(3, 1001), (2, 40003), (150, 2050), (2, 130001)])
+def test_guard_bands(dt, n, vocab):
+    z, ids, t, w = draw(n, vocab, 9, dt, seed=7)
+    zc, ic, tc, wc = z.cuda(), ids.cuda(), t.cuda(), w.cuda()
+    s = N.make_distill_shape(n, vocab, vocab, vocab, 9, 8, 1.0, L._code(zc))
+    for fused in (False, True):
+        loss, stats, dz = Guarded((n,), torch.float32), Guarded((n, 2), torch.float32), Guarded((n, vocab), DT[dt])
+        head = (s, zc.data_ptr(), ic.data_ptr(), tc.data_ptr(), wc.data_ptr())
+        if fused:
+            N.kan_distill_loss_grad(*head, loss.t.data_ptr(), stats.t.data_ptr(), dz.t.data_ptr(), None)
+        else:
+            N.kan_distill_forward(*head, loss.t.data_ptr(), stats.t.data_ptr(), None)
+            N.kan_distill_backward(*head, stats.t.data_ptr(), None, dz.t.data_ptr(), None)
+        torch.cuda.synchronize()
+        for k, v in (("loss", loss), ("stats", stats), ("dz", dz)):
+            v.check(k)
+        check(loss.t, dz.t, (z, ids, t, 1.0, w))
+
+
+def test_no_rows():
+    z = torch.empty(0, 10, device="cuda")
+    loss, dz = L.distill_loss_grad(z, torch.empty(0, 2, dtype=torch.int64, device="cuda"), torch.empty(0, 2, device="cuda"))
+    assert loss.shape == (0,) and dz.shape == (0, 10)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_deterministic(dt):
+    z, ids, t, w = draw(40, 30011, 50, dt, seed=4, repeat=True)
+    first = run(z, ids, t, 1.0, w)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(first, run(z, ids, t, 1.0, w)))
+
+
+def test_gradient_against_differences():
+    """Differences of the kernel's own loss along a direction: fp32 losses near 3 carry errors of 1e-5 at most, over a
+    step of 2 * 2^-5 that is 2e-4 beside a truncation error of the step's square times the third derivative (below 1):
+    5e-3 of the product of norms holds both."""
+    z, ids, t, w = draw(5, 60, 4, "f32", seed=5)
+    v = torch.randn(5, 60, generator=torch.Generator().manual_seed(1))
+    eps = 2.0 ** -5
+    side = [float(run(z + sgn * eps * v, ids, t, 1.3, w)[0].double().sum()) for sgn in (1, -1)]
+    dz = run(z, ids, t, 1.3, w)[3].cpu().double()
+    assert abs((side[0] - side[1]) / (2 * eps) - float((dz * v).sum())) <= 5e-3 * float(dz.norm() * v.double().norm())
+    leaf = z[:, :7].double().requires_grad_()
+    i7 = ids % 7
+    assert torch.autograd.gradcheck(lambda a: ref.distill(a, i7, t, 1.3, w), [leaf], eps=1e-6, atol=1e-7, rtol=1e-6)
+
+
+def test_module():
+    z, ids, t, w = draw(12, 90, 5, "f32", seed=6)
+    zc = z.cuda().reshape(3, 4, 90).requires_grad_()
+    m = L.TopLogitDistillation(2.0)
+    total = m(zc, ids.cuda().reshape(3, 4, 5), t.cuda().reshape(3, 4, 5), w.cuda().reshape(3, 4))
+    (total * 0.25).backward()
+    wl, _ = reference(z, ids, t, 2.0, w)
+    assert abs(float(total) - float(wl.sum())) <= 1e-5 * float(wl.abs().sum())
+    check(torch.as_tensor(wl), zc.grad.reshape(12, 90), (z, ids, t, 2.0, w), torch.full((12,), 0.25))
+    rows = L.TopLogitDistillation(2.0, "none")(zc, ids.cuda().reshape(3, 4, 5), t.cuda().reshape(3, 4, 5), w.cuda().reshape(3, 4))
+    assert rows.shape == (3, 4)
+    # logits whose rows are not contiguous
+    zt = z.t().contiguous().cuda().t().requires_grad_()
+    m(zt, ids.cuda(), t.cuda(), w.cuda()).backward()
+    check(rows.reshape(-1).detach(), zt.grad, (z, ids, t, 2.0, w))
+
+
+def test_two_captured_graphs():
+    graphs = []
+    for k in range(2):
+        z, ids, t, w = draw(9, 20003, 11, "bf16", seed=30 + k)
+        dev = [v.cuda() for v in (z, ids, t, w)]
+        torch.cuda.synchronize()
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            out = L.distill_loss_grad(dev[0], dev[1], dev[2], 1.0, dev[3])
+        graphs.append((gr, dev, out, (ids, t, w)))
+    for gr, dev, out, (ids, t, w) in graphs:
+        z = (torch.randn(9, 20003) * 3).bfloat16()
+        dev[0].copy_(z)
+        gr.replay()
+        torch.cuda.synchronize()
+        check(*out, (z, ids, t, 1.0, w))

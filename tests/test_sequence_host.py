@@ -113,3 +113,51 @@ def test_glr_python_refusals():
         L.GatedLinearRecurrence(0)
     with pytest.raises(ValueError):
         L.GatedLinearRecurrence(4, longest=1.0)
+
+
+def distill(**kw):
+    d = dict(rows=4, vocab=100, ld=100, ld_grad=100, entries=8, id_bytes=8, temperature=1.0, dtype=0)
+    d.update(kw)
+    return N.make_distill_shape(**d)
+
+
+def distill_calls(lib, s, z=FAKE, ids=FAKE, t=FAKE, w=None, loss=FAKE, stats=FAKE, dz=FAKE):
+    return (lib.kan_distill_forward(s, z, ids, t, w, loss, stats, None),
+            lib.kan_distill_backward(s, z, ids, t, w, stats, None, dz, None),
+            lib.kan_distill_loss_grad(s, z, ids, t, w, loss, stats, dz, None))
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(rows=-1), 1), (dict(vocab=0), 1), (dict(entries=0), 1), (dict(ld=99), 1), (dict(ld_grad=99), 1),
+    (dict(dtype=2), 1), (dict(id_bytes=1), 1), (dict(temperature=0.0), 1), (dict(temperature=-1.0), 1),
+    (dict(temperature=float("nan")), 1), (dict(temperature=float("inf")), 1), (dict(entries=1025), 2),
+    (dict(rows=1 << 31), 2), (dict(vocab=1 << 31, ld=1 << 31, ld_grad=1 << 31), 2),
+])
+def test_distill_bad_shapes(lib, kw, code):
+    assert distill_calls(lib, ctypes.byref(distill(**kw))) == (code,) * 3
+    assert lib.kan_last_error().decode() != ""
+
+
+def test_distill_bad_pointers(lib):
+    s = ctypes.byref(distill())
+    assert distill_calls(lib, None) == (1,) * 3
+    for k in ("z", "ids", "t", "stats"):
+        assert distill_calls(lib, s, **{k: None}) == (1,) * 3
+        assert distill_calls(lib, s, **{k: FAKE + 1}) == (2,) * 3
+    assert distill_calls(lib, s, stats=FAKE + 4) == (2,) * 3
+    assert distill_calls(lib, s, w=FAKE + 2) == (2,) * 3
+    assert lib.kan_distill_forward(s, FAKE, FAKE, FAKE, None, None, FAKE, None) == 1
+    assert lib.kan_distill_backward(s, FAKE, FAKE, FAKE, None, FAKE, None, None, None) == 1
+    # a refused gradient leaves no forward launched
+    assert lib.kan_distill_loss_grad(s, FAKE, FAKE, FAKE, None, FAKE, FAKE, None, None) == 1
+    assert lib.kan_distill_loss_grad(s, FAKE, FAKE, FAKE, None, FAKE, FAKE, FAKE + 2, None) == 2
+
+
+def test_distill_python_refusals():
+    z, ids, t = torch.zeros(2, 10), torch.zeros(2, 3, dtype=torch.int64), torch.zeros(2, 3)
+    with pytest.raises(ValueError, match="CUDA"):
+        L.distill_forward(z, ids, t)
+    with pytest.raises(ValueError, match="temperature"):
+        L.TopLogitDistillation(0.0)
+    with pytest.raises(ValueError, match="reduction"):
+        L.TopLogitDistillation(1.0, "mean")
