@@ -40,7 +40,8 @@ namespace kan {
 namespace {
 
 constexpr int kSteps = 8;         // steps per thread, and the spacing of the kept states
-constexpr float kHard = -2.0f;    // the factor of a map that a reset cuts
+
+constexpr int kMaxCluster = 8;    // blocks of a cluster (the portable bound)
 
 struct GlrArgs {
     const void *x, *r, *g;
@@ -61,64 +62,162 @@ struct GlrArgs {
     int strips;                         // ceil(C / (32 VEC))
 };
 
-// What the CUDA functions give: the accurate ones for fp32 operands, the fast ones (about two units in the last place
-// of fp32 for these arguments) for bf16 operands.
-template <typename T> __device__ __forceinline__ float exp_of(float v) { return sizeof(T) == 4 ? expf(v) : __expf(v); }
-template <typename T> __device__ __forceinline__ float recip(float v) { return sizeof(T) == 4 ? __frcp_rn(v) : __fdividef(1.0f, v); }
-// sigmoid(v), and 1 - sigmoid(v) without cancellation.  Below -80 the sigmoid is held at e^-80, so that e stays finite;
-// a NaN passes.
-template <typename T> __device__ __forceinline__ float sigmoid_of(float v, float& rest)
+// Factor: a number v that stands for A in [0, 1].  v in (-1, 0]: A = 1 + v;  v > 0: A = v;  v = kHard: A = 0, and what
+// it multiplies is cut off even if it is not finite (L = -inf, which stands for a reset).
+constexpr float kHard = -2.0f;
+constexpr float kTiny = 1e-37f;
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2(float x)
 {
-    const float e = exp_of<T>(-v > 80.0f ? 80.0f : -v);
-    const float s = recip<T>(1.0f + e);
-    rest = e * s;
-    return s;
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
-template <typename T> __device__ __forceinline__ float sigmoid_of(float v)
+__device__ __forceinline__ float rcp(float x)
 {
-    float rest;
-    return sigmoid_of<T>(v, rest);
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rsq(float x)
+{
+    float r;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// the smaller of both; a NaN passes
+__device__ __forceinline__ float min_nan(float x, float y)
+{
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
 }
 
-// Factor: a number v that stands for A in [0, 1].  v in (-1, 0]: A = 1 + v;  v > 0: A = v;  v = kHard: A = 0, and what
-// it multiplies is cut off even if it is not finite (a reset, or a product below fp32's range).
-constexpr float kTiny = 1e-37f;
+// E neighbouring channels of a thread; two of them go through the packed f32x2 instructions.
+template <int E> struct F;
+template <> struct F<1> {
+    float a;
+    __device__ __forceinline__ static F all(float x) { return {x}; }
+    __device__ __forceinline__ static F of(const float (&v)[1]) { return {v[0]}; }
+    __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = a; }
+};
+template <> struct F<2> {
+    uint64_t q;
+    __device__ __forceinline__ static F two(float x, float y)
+    {
+        F r;
+        asm("mov.b64 %0, {%1, %2};" : "=l"(r.q) : "f"(x), "f"(y));
+        return r;
+    }
+    __device__ __forceinline__ static F all(float x) { return two(x, x); }
+    __device__ __forceinline__ static F of(const float (&v)[2]) { return two(v[0], v[1]); }
+    __device__ __forceinline__ void get(float (&v)[2]) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(v[0]), "=f"(v[1]) : "l"(q)); }
+};
+__device__ __forceinline__ F<1> fma(F<1> x, F<1> y, F<1> z) { return {fmaf(x.a, y.a, z.a)}; }
+__device__ __forceinline__ F<1> operator*(F<1> x, F<1> y) { return {x.a * y.a}; }
+__device__ __forceinline__ F<1> operator+(F<1> x, F<1> y) { return {x.a + y.a}; }
+__device__ __forceinline__ F<2> fma(F<2> x, F<2> y, F<2> z)
+{
+    F<2> r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.q) : "l"(x.q), "l"(y.q), "l"(z.q));
+    return r;
+}
+__device__ __forceinline__ F<2> operator*(F<2> x, F<2> y)
+{
+    F<2> r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.q) : "l"(x.q), "l"(y.q));
+    return r;
+}
+__device__ __forceinline__ F<2> operator+(F<2> x, F<2> y)
+{
+    F<2> r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.q) : "l"(x.q), "l"(y.q));
+    return r;
+}
+// f of each channel
+template <int E, typename Fn> __device__ __forceinline__ F<E> each(F<E> x, Fn f)
+{
+    float v[E];
+    x.get(v);
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = f(v[e]);
+    return F<E>::of(v);
+}
+template <int E, typename Fn> __device__ __forceinline__ F<E> each(F<E> x, F<E> y, Fn f)
+{
+    float v[E], w[E];
+    x.get(v);
+    y.get(w);
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = f(v[e], w[e]);
+    return F<E>::of(v);
+}
+
+// e^-x, held at 2^TOP from above, so that what is made of it stays finite (a NaN passes).
+template <int TOP, int E> __device__ __forceinline__ F<E> exp_minus(F<E> x)
+{
+    return each(x * F<E>::all(-kLog2e), [](float t) { return ex2(min_nan(t, (float)TOP)); });
+}
+template <int E> __device__ __forceinline__ F<E> rcp_of(F<E> x)
+{
+    return each(x, [](float t) { return rcp(t); });
+}
 
 // The factor exp(L), L <= 0 (a NaN passes).
-template <typename T> __device__ __forceinline__ float factor_of(float L)
+template <int E> __device__ __forceinline__ F<E> factor_of(F<E> L)
 {
-    const float big = exp_of<T>(L);
     // exp(L) - 1 = sum_{k=1..8} L^k / k!; the next term is below 2^-26 of the sum at L = -0.5
-    float s = fmaf(L, 1.0f / 40320.0f, 1.0f / 5040.0f);
-    s = fmaf(s, L, 1.0f / 720.0f);
-    s = fmaf(s, L, 1.0f / 120.0f);
-    s = fmaf(s, L, 1.0f / 24.0f);
-    s = fmaf(s, L, 1.0f / 6.0f);
-    s = fmaf(s, L, 0.5f);
-    s = fmaf(s, L, 1.0f);
-    return L > -0.5f ? s * L : (big < kTiny ? kTiny : big);
+    F<E> s = fma(L, F<E>::all(1.0f / 40320.0f), F<E>::all(1.0f / 5040.0f));
+    s = fma(s, L, F<E>::all(1.0f / 720.0f));
+    s = fma(s, L, F<E>::all(1.0f / 120.0f));
+    s = fma(s, L, F<E>::all(1.0f / 24.0f));
+    s = fma(s, L, F<E>::all(1.0f / 6.0f));
+    s = fma(s, L, F<E>::all(0.5f));
+    s = fma(s, L, F<E>::all(1.0f)) * L;
+    const F<E> big = each(L * F<E>::all(kLog2e), [](float t) {
+        const float x = ex2(t);
+        return x < kTiny ? kTiny : x;
+    });
+    float l[E], p[E], b[E];
+    L.get(l);
+    s.get(p);
+    big.get(b);
+#pragma unroll
+    for (int e = 0; e < E; ++e) p[e] = l[e] > -0.5f ? p[e] : b[e];
+    return F<E>::of(p);
 }
 __device__ __forceinline__ float value_of(float v) { return v > 0.0f ? v : 1.0f + v; }      // not for kHard
-__device__ __forceinline__ float one_minus_sq(float v) { return v > 0.0f ? fmaf(-v, v, 1.0f) : -v * (2.0f + v); }
-// A h + B, v not kHard
-__device__ __forceinline__ float walk(float v, float B, float h)
+// 1 - A^2
+template <int E> __device__ __forceinline__ F<E> one_minus_sq(F<E> v)
 {
-    return fmaf(v, h, B) + (v > 0.0f ? 0.0f : h);
+    // -v v + c with c = 1 (v = A) or -2 v (v = A - 1)
+    const F<E> c = each(v, [](float t) { return t > 0.0f ? 1.0f : -2.0f * t; });
+    return fma(v * F<E>::all(-1.0f), v, c);
 }
-
-template <typename T> __device__ __forceinline__ float sqrt_of(float v) { return sizeof(T) == 4 ? __fsqrt_rn(v) : v * rsqrtf(fmaxf(v, 1e-37f)); }
+// A h + B, v not kHard
+template <int E> __device__ __forceinline__ F<E> walk(F<E> v, F<E> B, F<E> h)
+{
+    return fma(v, h, B) + each(v, h, [](float t, float x) { return t > 0.0f ? 0.0f : x; });
+}
+template <int E> __device__ __forceinline__ F<E> apply(F<E> v, F<E> B, F<E> h)
+{
+    float t[E], b[E], r[E];
+    walk(v, B, h).get(r);
+    v.get(t);
+    B.get(b);
+#pragma unroll
+    for (int e = 0; e < E; ++e) r[e] = t[e] == kHard ? b[e] : r[e];
+    return F<E>::of(r);
+}
+// the factor of steps whose L sum up to this; -inf: a reset was among them
+template <int E> __device__ __forceinline__ F<E> factor_or_cut(F<E> L)
+{
+    const F<E> v = factor_of(L);
+    return each(L, v, [](float l, float t) { return l == -INFINITY ? kHard : t; });
+}
 
 __device__ __forceinline__ float softplus_of(float d) { return fmaxf(d, 0.0f) + log1pf(expf(-fabsf(d))); }
-
-__device__ __forceinline__ float apply(float v, float B, float h) { return v == kHard ? B : walk(v, B, h); }
-// (V, B) first, then (v, b)
-__device__ __forceinline__ void compose(float& V, float& B, float v, float b)
-{
-    B = apply(v, b, B);
-    const float sum = fmaf(V, v, V + v), prod = value_of(V) * value_of(v);
-    const bool small = V > 0.0f || v > 0.0f || sum < -0.5f;   // the product is kept as A
-    V = V == kHard || v == kHard || (small && prod < kTiny) ? kHard : (small ? prod : sum);
-}
 
 __device__ __forceinline__ uint32_t cluster_rank()
 {
@@ -137,267 +236,336 @@ __device__ __forceinline__ void st_cluster(const void* local, uint32_t rank, flo
     asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(d), "f"(v.x), "f"(v.y) : "memory");
 }
 
-// Exchange of one step of the cluster: every thread gives its map (P, B); on
-// return each thread holds the state that enters its steps in `in`, and `run`
-// has moved past the whole cluster's steps.  Position 0 comes first in the
-// direction of the scan.
-template <int VEC, int W, int CL>
-__device__ __forceinline__ void exchange(float2 (*agg)[VEC][32], float2 (*tot)[CL][VEC][32], int parity, int wpos,
-                                         int cpos, const float (&P)[VEC], const float (&B)[VEC], float (&run)[VEC],
-                                         float (&in)[VEC])
+// Shared memory of the exchange: maps (factor, offset) and sums of L of the block's warps, maps of the cluster's blocks
+// (two sets, written by turns).
+template <int E, int W, int CL> struct Meet {
+    float2 agg[W][E][32];
+    float len[W][E][32];
+    float2 tot[2][CL][E][32];
+};
+
+// Exchange of one span of the cluster: every thread gives its map (L, B); it gets the state that enters its steps, and
+// `run` moves past the whole span.  Position 0 comes first in the direction of the scan.  Factors multiply as sums of L.
+template <int E, int W, int CL>
+__device__ __forceinline__ F<E> exchange(Meet<E, W, CL>& s, int parity, int wpos, int cpos, F<E> L, F<E> B, F<E>& run)
 {
     const int lane = threadIdx.x & 31;
+    const F<E> v = factor_or_cut(L);
+    F<E> in = run;
     if constexpr (W * CL == 1) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            in[e] = run[e];
-            run[e] = apply(P[e], B[e], run[e]);
-        }
-        return;
+        run = apply(v, B, run);
+        return in;
     }
+    auto put = [&](float2 (*to)[32], F<E> x, F<E> y) {
+        float p[E], q[E];
+        x.get(p);
+        y.get(q);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) agg[wpos][e][lane] = make_float2(P[e], B[e]);
+        for (int e = 0; e < E; ++e) to[e][lane] = make_float2(p[e], q[e]);
+    };
+    auto step = [&](const float2 (*from)[32], F<E> h) {
+        float p[E], q[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const float2 t = from[e][lane];
+            p[e] = t.x;
+            q[e] = t.y;
+        }
+        return apply(F<E>::of(p), F<E>::of(q), h);
+    };
+    put(s.agg[wpos], v, B);
+    if constexpr (CL > 1) {
+        float l[E];
+        L.get(l);
+#pragma unroll
+        for (int e = 0; e < E; ++e) s.len[wpos][e][lane] = l[e];
+    }
     __syncthreads();
-    float Pp[VEC], Bp[VEC], Pt[VEC], Bt[VEC];            // what lies before this warp in the block; the whole block
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-        Pt[e] = 0.0f;
-        Bt[e] = 0.0f;
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-            if (w == wpos) {
-                Pp[e] = Pt[e];
-                Bp[e] = Bt[e];
-            }
-            const float2 q = agg[w][e][lane];
-            compose(Pt[e], Bt[e], q.x, q.y);
-        }
-    }
     if constexpr (CL > 1) {
         if (wpos == 0) {
+            F<E> bt = F<E>::all(0.0f);
+            float lt[E] = {};
 #pragma unroll
-            for (int e = 0; e < VEC; ++e)
+            for (int w = 0; w < W; ++w) {
+                bt = step(s.agg[w], bt);
 #pragma unroll
-                for (int q = 0; q < CL; ++q) st_cluster(&tot[parity][cpos][e][lane], q, make_float2(Pt[e], Bt[e]));
+                for (int e = 0; e < E; ++e) {
+                    const float l = s.len[w][e][lane];
+                    lt[e] = l == -INFINITY ? l : lt[e] + l;          // a reset cuts off a NaN before it
+                }
+            }
+            float p[E], q[E];
+            factor_or_cut(F<E>::of(lt)).get(p);
+            bt.get(q);
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+#pragma unroll
+                for (int c = 0; c < CL; ++c) st_cluster(&s.tot[parity][cpos][e][lane], c, make_float2(p[e], q[e]));
         }
         cluster_sync_all();
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            float h = run[e];
-#pragma unroll
-            for (int q = 0; q < CL; ++q) {
-                if (q == cpos) in[e] = h;
-                const float2 v = tot[parity][q][e][lane];
-                h = apply(v.x, v.y, h);
-            }
-            run[e] = h;
-            in[e] = apply(Pp[e], Bp[e], in[e]);
+        for (int c = 0; c < CL; ++c) {
+            if (c == cpos) in = run;
+            run = step(s.tot[parity][c], run);
         }
-    } else {
+        for (int w = 0; w < wpos; ++w) in = step(s.agg[w], in);
+        // the next span's maps are written after the next pass of the barrier above at the earliest by this block's
+        // warps that have read these: one more block barrier
         __syncthreads();
+    } else {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            in[e] = apply(Pp[e], Bp[e], run[e]);
-            run[e] = apply(Pt[e], Bt[e], run[e]);
+        for (int w = 0; w < W; ++w) {
+            if (w == wpos) in = run;
+            run = step(s.agg[w], run);
         }
+        __syncthreads();
     }
+    return in;
 }
 
-template <typename T, int VEC, int S, int W, int CL, bool BWD>
-__global__ void __launch_bounds__(32 * W) glr_kernel(const GlrArgs a)
+// Forward: S steps a thread, W warps a block, CL blocks a cluster.
+template <typename T, int E, int S, int W, int CL>
+__global__ void __launch_bounds__(32 * W, W == 8 ? 4 : 1) glr_forward_kernel(const GlrArgs a)
 {
-    __shared__ float2 agg[W][VEC][32];
-    __shared__ float2 tot[2][CL][VEC][32];
+    __shared__ Meet<E, W, CL> meet;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rank = CL > 1 ? (int)cluster_rank() : 0;
     const int64_t unit = blockIdx.x / CL;                // (sequence, strip of channels)
     const int64_t b = unit / a.strips;
-    const int64_t c = (unit - b * a.strips) * (32 * VEC) + lane * VEC;
-    const bool on = c < a.C;                             // VEC divides C
-    const int wpos = BWD ? W - 1 - warp : warp, cpos = BWD ? CL - 1 - rank : rank;
+    const int64_t c = (unit - b * a.strips) * (32 * E) + lane * E;
+    const bool on = c < a.C;                             // E divides C
     constexpr int64_t SPAN = (int64_t)S * W * CL;
-    const int64_t spans = (a.T + SPAN - 1) / SPAN;
-    const int64_t off = ((int64_t)rank * W + warp) * S;  // this thread's first step within a span
-    using V = Pack<T, VEC>;
+    using V = Pack<T, E>;
+    const int64_t first = ((int64_t)rank * W + warp) * S;    // this thread's first step within a span
     const T* X = reinterpret_cast<const T*>(a.x) + b * a.xb + c;
     const T* R = reinterpret_cast<const T*>(a.r) + b * a.rb + c;
     const T* G = reinterpret_cast<const T*>(a.g) + b * a.gb + c;
-    const int64_t bt = b * a.T;
-    const int64_t blocks = (a.T + kSteps - 1) / kSteps;
+    T* Y = reinterpret_cast<T*>(a.y) + b * a.T * a.C + c;
+    const unsigned char* Z = a.reset ? a.reset + b * a.T : nullptr;
+    float* K = a.kept ? a.kept + b * ((a.T + kSteps - 1) / kSteps) * a.C + c : nullptr;
 
-    float lambda[VEC], run[VEC];
+    float t0[E], t1[E];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-        lambda[e] = on ? softplus_of(a.decay[c + e]) : 0.0f;
-        const float* first = BWD ? a.dh_last : a.h0;
-        run[e] = on && first ? first[b * a.C + c + e] : 0.0f;
+    for (int e = 0; e < E; ++e) {
+        t0[e] = on ? -softplus_of(a.decay[c + e]) : 0.0f;
+        t1[e] = on && a.h0 ? a.h0[b * a.C + c + e] : 0.0f;
     }
-    double acc[VEC];                                     // sum of dL L
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) acc[e] = 0.0;
+    const F<E> neg_lambda = F<E>::of(t0), one = F<E>::all(1.0f), zero = F<E>::all(0.0f);
+    F<E> run = F<E>::of(t1);
+    if constexpr (CL > 1) cluster_sync_all();            // every block of the cluster runs before its memory is written
 
-    V qx[S], qr[S], qg[S], qd[BWD ? S : 1];
-    float kept[VEC];
-    uint32_t cut = 0, live = 0;                          // steps of this thread: reset set; within the sequence
-    auto fetch = [&](int64_t span) {
-        const int64_t t0 = span * SPAN + off;
-        cut = live = 0;
+    int parity = 0;
+    for (int64_t base = 0; base < a.T; base += SPAN, parity ^= 1) {
+        const int64_t t = base + first;
+        const int live = (int)min((int64_t)S, max((int64_t)0, a.T - t));
+        V qx[S], qr[S], qg[S];
+        uint32_t cut = 0;
 #pragma unroll
         for (int i = 0; i < S; ++i) {
-            const int64_t t = t0 + i;
-            if (t < a.T) {
-                live |= 1u << i;
-                if (a.reset && a.reset[bt + t]) cut |= 1u << i;
+            qx[i] = qr[i] = qg[i] = V::zero();
+            if (i < live && on) {
+                qr[i] = V::load(R + (t + i) * a.rt);
+                qg[i] = V::load(G + (t + i) * a.gt);
+                qx[i] = V::load(X + (t + i) * a.xt);
+            }
+        }
+        if (Z) {
+#pragma unroll
+            for (int i = 0; i < S; ++i)
+                if (i < live && Z[t + i]) cut |= 1u << i;
+        }
+        F<E> fa[S], bb[S], L = zero, B = zero;
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+            float vx[E], vr[E], vg[E];
+            qx[i].unpack(vx);
+            qr[i].unpack(vr);
+            qg[i].unpack(vg);
+            const F<E> s = rcp_of(one + exp_minus<115>(F<E>::of(vr)));
+            const F<E> l = s * (i < live ? neg_lambda : zero);       // past the end: a = 1
+            fa[i] = factor_of(l);
+            // m sigmoid(g) = sqrt(m^2) / (1 + e) = m^2 / sqrt(m^2 (1 + e)^2), one rsqrt
+            const F<E> m2 = one_minus_sq(fa[i]), q = one + exp_minus<60>(F<E>::of(vg));
+            const F<E> w = m2 * each(m2 * q * q, [](float u) { return rsq(u < kTiny ? kTiny : u); });
+            bb[i] = w * F<E>::of(vx);
+            const bool z = cut >> i & 1;
+            L = z ? F<E>::all(-INFINITY) : L + l;
+            B = walk(fa[i], bb[i], z ? zero : B);
+        }
+        F<E> h = exchange<E, W, CL>(meet, parity, warp, rank, L, B, run);
+        if (K && live > 0 && on) {
+            float f[E];
+            h.get(f);
+#pragma unroll
+            for (int e = 0; e < E; ++e) K[(t / kSteps) * a.C + e] = f[e];
+        }
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+            h = walk(fa[i], bb[i], cut >> i & 1 ? zero : h);
+            if (i < live && on) {
+                float f[E];
+                h.get(f);
+                V::pack(f).store(Y + (t + i) * a.C);
+            }
+        }
+    }
+    if (a.h_last && on && rank == 0 && warp == 0) {
+        float f[E];
+        run.get(f);
+#pragma unroll
+        for (int e = 0; e < E; ++e) a.h_last[b * a.C + c + e] = f[e];
+    }
+}
+
+// Backward: the same split, walked from the end of the sequence.
+template <typename T, int E, int S, int W, int CL>
+__global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_backward_kernel(const GlrArgs a)
+{
+    static_assert(S == kSteps, "a thread's steps begin at a kept state");
+    __shared__ Meet<E, W, CL> meet;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int rank = CL > 1 ? (int)cluster_rank() : 0;
+    const int64_t unit = blockIdx.x / CL;
+    const int64_t b = unit / a.strips;
+    const int64_t c = (unit - b * a.strips) * (32 * E) + lane * E;
+    const bool on = c < a.C;
+    constexpr int64_t SPAN = (int64_t)S * W * CL;
+    using V = Pack<T, E>;
+    const int64_t first = ((int64_t)rank * W + warp) * S;
+    const T* X = reinterpret_cast<const T*>(a.x) + b * a.xb + c;
+    const T* R = reinterpret_cast<const T*>(a.r) + b * a.rb + c;
+    const T* G = reinterpret_cast<const T*>(a.g) + b * a.gb + c;
+    const int64_t dense = b * a.T * a.C + c;
+    const T* D = reinterpret_cast<const T*>(a.dy) + dense;
+    const unsigned char* Z = a.reset ? a.reset + b * a.T : nullptr;
+    const float* K = a.kept + b * ((a.T + kSteps - 1) / kSteps) * a.C + c;
+
+    float t0[E], t1[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        t0[e] = on ? -softplus_of(a.decay[c + e]) : 0.0f;
+        t1[e] = on && a.dh_last ? a.dh_last[b * a.C + c + e] : 0.0f;
+    }
+    const F<E> neg_lambda = F<E>::of(t0), one = F<E>::all(1.0f), zero = F<E>::all(0.0f);
+    F<E> run = F<E>::of(t1);
+    double acc[E];                                       // sum of dL L
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.0;
+    if constexpr (CL > 1) cluster_sync_all();
+
+    int parity = 0;
+    for (int64_t base = (a.T - 1) / SPAN * SPAN; base >= 0; base -= SPAN, parity ^= 1) {
+        const int64_t t = base + first;
+        const int live = (int)min((int64_t)S, max((int64_t)0, a.T - t));
+        V qx[S], qr[S], qg[S], qd[S];
+        uint32_t cut = 0;
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+            qx[i] = qr[i] = qg[i] = qd[i] = V::zero();
+            if (i < live && on) {
+                qr[i] = V::load(R + (t + i) * a.rt);
+                qg[i] = V::load(G + (t + i) * a.gt);
+                qx[i] = V::load(X + (t + i) * a.xt);
+                qd[i] = V::load(D + (t + i) * a.C);
+            }
+        }
+        if (Z) {
+#pragma unroll
+            for (int i = 0; i < S; ++i)
+                if (i < live && Z[t + i]) cut |= 1u << i;
+        }
+        F<E> h = zero;
+        if (live > 0 && on) {
+            float f[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) f[e] = K[(t / kSteps) * a.C + e];
+            h = F<E>::of(f);
+        }
+        // per step: the factor, and what d multiplies in each gradient:
+        //   dx = d cx,  dg = dx cg,  dL L = d cl,  dr = dL L cr
+        F<E> fa[S], cx[S], cg[S], cl[S], cr[S], L = zero;
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+            float vx[E], vr[E], vg[E];
+            qx[i].unpack(vx);
+            qr[i].unpack(vr);
+            qg[i].unpack(vg);
+            const F<E> er = exp_minus<115>(F<E>::of(vr)), eg = exp_minus<115>(F<E>::of(vg));
+            const F<E> s = rcp_of(one + er), sg = rcp_of(one + eg), x = F<E>::of(vx);
+            const F<E> l = s * (i < live ? neg_lambda : zero);
+            fa[i] = factor_of(l);
+            const F<E> m2 = one_minus_sq(fa[i]);
+            const F<E> rm = each(m2, [](float u) { return u < kTiny ? 0.0f : rsq(u); });   // 1 / m; L / m goes to 0 with L
+            const F<E> av = each(fa[i], [](float v) { return value_of(v); });
+            const F<E> u = sg * x, hp = cut >> i & 1 ? zero : h;
+            cx[i] = m2 * rm * sg;
+            cg[i] = x * (eg * sg);
+            cr[i] = er * s;
+            cl[i] = av * l * fma(av * F<E>::all(-1.0f), u * rm, hp);
+            h = walk(fa[i], cx[i] * x, hp);
+            L = cut >> i & 1 ? F<E>::all(-INFINITY) : L + l;
+        }
+        // the map of these steps, from the last to the first: gamma -> a (gamma + dy)
+        F<E> B = zero;
+#pragma unroll
+        for (int i = S - 1; i >= 0; --i) {
+            float vd[E];
+            qd[i].unpack(vd);
+            const F<E> d = B + F<E>::of(vd);
+            B = cut >> i & 1 ? zero : walk(fa[i], zero, d);
+        }
+        // (a reset cuts off what comes from later steps, a NaN of which would pass the sum of L)
+        if (cut) L = F<E>::all(-INFINITY);
+        F<E> flow = exchange<E, W, CL>(meet, parity, W - 1 - warp, CL - 1 - rank, L, B, run);
+        F<E> part = zero;
+#pragma unroll
+        for (int i = S - 1; i >= 0; --i) {
+            if (i < live) {
+                float vd[E], f[E];
+                qd[i].unpack(vd);
+                const F<E> d = flow + F<E>::of(vd);
+                const F<E> ox = d * cx[i], ol = d * cl[i];
+                part = part + ol;
+                flow = cut >> i & 1 ? zero : walk(fa[i], zero, d);
                 if (on) {
-                    qx[i] = V::load(X + t * a.xt);
-                    qr[i] = V::load(R + t * a.rt);
-                    qg[i] = V::load(G + t * a.gt);
-                    if constexpr (BWD) qd[i] = V::load(reinterpret_cast<const T*>(a.dy) + (bt + t) * a.C + c);
-                }
-            }
-        }
-        if constexpr (BWD) {
-            if (on && t0 < a.T) {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) kept[e] = a.kept[(b * blocks + t0 / kSteps) * a.C + c + e];
-            }
-        }
-    };
-    fetch(BWD ? spans - 1 : 0);
-    if constexpr (CL > 1) cluster_sync_all();            // every block of the cluster runs before its memory is written
-    for (int64_t n = 0; n < spans; ++n) {
-        const int64_t span = BWD ? spans - 1 - n : n;
-        const int64_t t0 = span * SPAN + off;
-        const uint32_t live_n = on ? live : 0, cut_n = cut;
-        float fa[S][VEC], in[VEC];
-        if constexpr (!BWD) {
-            float bb[S][VEC], P[VEC], B[VEC];
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) P[e] = B[e] = 0.0f;
-#pragma unroll
-            for (int i = 0; i < S; ++i) {
-                float fx[VEC], fr[VEC], fg[VEC];
-                qx[i].unpack(fx);
-                qr[i].unpack(fr);
-                qg[i].unpack(fg);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    fa[i][e] = factor_of<T>(-lambda[e] * sigmoid_of<T>(fr[e]));
-                    bb[i][e] = sqrt_of<T>(one_minus_sq(fa[i][e])) * (sigmoid_of<T>(fg[e]) * fx[e]);
-                    if (!(live_n >> i & 1)) fa[i][e] = bb[i][e] = 0.0f;
-                    compose(P[e], B[e], cut_n >> i & 1 ? kHard : fa[i][e], bb[i][e]);
-                }
-            }
-            if (n + 1 < spans) fetch(span + 1);
-            exchange<VEC, W, CL>(agg, tot, (int)(n & 1), wpos, cpos, P, B, run, in);
-            if (a.kept && live_n) {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) a.kept[(b * blocks + t0 / kSteps) * a.C + c + e] = in[e];
-            }
-            T* Y = reinterpret_cast<T*>(a.y) + (bt + t0) * a.C + c;
-#pragma unroll
-            for (int i = 0; i < S; ++i) {
-                if (live_n >> i & 1) {
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) in[e] = apply(cut_n >> i & 1 ? kHard : fa[i][e], bb[i][e], in[e]);
-                    V::pack(in).store(Y + (int64_t)i * a.C);
-                }
-            }
-        } else {
-            float hp[S][VEC], P[VEC], B[VEC];
-            // the states before each step, from the kept one
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) in[e] = live_n ? kept[e] : 0.0f;
-#pragma unroll
-            for (int i = 0; i < S; ++i) {
-                float fx[VEC], fr[VEC], fg[VEC];
-                qx[i].unpack(fx);
-                qr[i].unpack(fr);
-                qg[i].unpack(fg);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    fa[i][e] = factor_of<T>(-lambda[e] * sigmoid_of<T>(fr[e]));
-                    const float bb = sqrt_of<T>(one_minus_sq(fa[i][e])) * (sigmoid_of<T>(fg[e]) * fx[e]);
-                    hp[i][e] = cut_n >> i & 1 ? 0.0f : in[e];
-                    in[e] = walk(fa[i][e], bb, hp[i][e]);
-                    if (!(live_n >> i & 1)) fa[i][e] = 0.0f;
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) P[e] = B[e] = 0.0f;
-#pragma unroll
-            for (int i = S - 1; i >= 0; --i) {
-                float fd[VEC];
-                qd[i].unpack(fd);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    // gamma -> a (gamma + dy): offset a dy
-                    const float d = live_n >> i & 1 ? fd[e] : 0.0f;
-                    if (cut_n >> i & 1) {
-                        P[e] = kHard;
-                        B[e] = 0.0f;
-                    } else {
-                        compose(P[e], B[e], fa[i][e], walk(fa[i][e], 0.0f, d));
+                    const int64_t at = dense + (t + i) * a.C;
+                    if (a.dx) {
+                        ox.get(f);
+                        V::pack(f).store(reinterpret_cast<T*>(a.dx) + at);
+                    }
+                    if (a.dr) {
+                        (ol * cr[i]).get(f);
+                        V::pack(f).store(reinterpret_cast<T*>(a.dr) + at);
+                    }
+                    if (a.dg) {
+                        (ox * cg[i]).get(f);
+                        V::pack(f).store(reinterpret_cast<T*>(a.dg) + at);
                     }
                 }
             }
-            exchange<VEC, W, CL>(agg, tot, (int)(n & 1), wpos, cpos, P, B, run, in);
-            const int64_t o = (bt + t0) * a.C + c;
-            float part[VEC];
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) part[e] = 0.0f;
-#pragma unroll
-            for (int i = S - 1; i >= 0; --i) {
-                if (!(live_n >> i & 1)) continue;
-                float fx[VEC], fr[VEC], fg[VEC], fd[VEC], ox[VEC], orr[VEC], og[VEC];
-                qx[i].unpack(fx);
-                qr[i].unpack(fr);
-                qg[i].unpack(fg);
-                qd[i].unpack(fd);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    float rest_r, rest_g;
-                    const float s = sigmoid_of<T>(fr[e], rest_r), L = -lambda[e] * s, av = value_of(fa[i][e]);
-                    const float sg = sigmoid_of<T>(fg[e], rest_g), m = sqrt_of<T>(one_minus_sq(fa[i][e]));
-                    // as L -> 0, L / m -> 0: no division by zero
-                    const float rm = m > 1e-18f ? recip<T>(m) : 0.0f;
-                    const float d = fd[e] + in[e];
-                    const float u = sg * fx[e];
-                    const float dl = d * av * (hp[i][e] - av * u * rm) * L;
-                    ox[e] = d * m * sg;
-                    og[e] = ox[e] * fx[e] * rest_g;
-                    orr[e] = dl * rest_r;
-                    part[e] += dl;
-                    in[e] = cut_n >> i & 1 ? 0.0f : walk(fa[i][e], 0.0f, d);
-                }
-                const int64_t at = o + (int64_t)i * a.C;
-                if (a.dx) V::pack(ox).store(reinterpret_cast<T*>(a.dx) + at);
-                if (a.dr) V::pack(orr).store(reinterpret_cast<T*>(a.dr) + at);
-                if (a.dg) V::pack(og).store(reinterpret_cast<T*>(a.dg) + at);
-            }
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) acc[e] += (double)part[e];
-            if (n + 1 < spans) fetch(span - 1);
         }
+        float f[E];
+        part.get(f);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] += (double)f[e];
     }
-    float* last = BWD ? a.dh0 : a.h_last;
-    if (last && on && rank == 0 && warp == 0) {
+    if (a.dh0 && on && rank == 0 && warp == 0) {
+        float f[E];
+        run.get(f);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) last[b * a.C + c + e] = run[e];
+        for (int e = 0; e < E; ++e) a.dh0[b * a.C + c + e] = f[e];
     }
-    if constexpr (BWD) {
-        if (a.part) {
-            __shared__ double red[W][VEC][32];
+    if (a.part) {
+        __shared__ double red[W][E][32];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) red[warp][e][lane] = acc[e];
-            __syncthreads();
-            if (warp == 0 && on) {
+        for (int e = 0; e < E; ++e) red[warp][e][lane] = acc[e];
+        __syncthreads();
+        if (warp == 0 && on) {
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    double v = 0.0;
-                    for (int w = 0; w < W; ++w) v += red[w][e][lane];
-                    a.part[(b * CL + rank) * a.C + c + e] = v;
-                }
+            for (int e = 0; e < E; ++e) {
+                double v = 0.0;
+                for (int w = 0; w < W; ++w) v += red[w][e][lane];
+                a.part[(b * CL + rank) * a.C + c + e] = v;
             }
         }
     }
@@ -437,45 +605,61 @@ struct GlrPlan {
     int vec, cluster, warps, steps, strips;
 };
 
-GlrPlan plan_of(const kan_glr_shape& s, int vec)
+// Blocks of 8 warps; as many blocks of a cluster side by side in time as fill the SMs once (kResident blocks fit), at
+// most 8, no more than the sequence has steps for.  A block of one warp where 8 steps (or one) are all there is.
+GlrPlan plan_of(const kan_glr_shape& s, int vec, bool backward)
 {
     GlrPlan P{};
     P.vec = vec;
     P.strips = (int)((s.channels + 32 * vec - 1) / (32 * vec));
-    P.warps = 8;
-    P.steps = kSteps;
-    P.cluster = 8;
+    P.steps = s.time == 1 && !backward ? 1 : kSteps;
+    P.warps = s.time <= kSteps ? 1 : 8;
+    P.cluster = 1;
+    const int64_t resident = 148 * (backward ? 2 : 4), units = s.batch * P.strips;
+    if (P.warps == 8)
+        while (P.cluster < kMaxCluster && units * P.cluster * 2 <= resident && s.time > (int64_t)P.cluster * 8 * kSteps)
+            P.cluster *= 2;
     return P;
 }
 
-template <typename T, int VEC, int S, int W, int CL, bool BWD>
-cudaError_t launch(const GlrArgs& a, cudaStream_t st)
+template <typename K> cudaError_t launch(K kernel, int warps, int cluster, const GlrArgs& a, cudaStream_t st)
 {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(a.B * a.strips * CL));
-    cfg.blockDim = dim3(32 * W);
+    cfg.gridDim = dim3((unsigned)(a.B * a.strips * cluster));
+    cfg.blockDim = dim3(32 * warps);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = CL;
+    at[0].val.clusterDim.x = cluster;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = CL > 1 ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, glr_kernel<T, VEC, S, W, CL, BWD>, a);
+    cfg.numAttrs = cluster > 1 ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
     if (e == cudaSuccess) count_launch();
     return e;
 }
 
-template <typename T, int VEC, bool BWD>
-cudaError_t run(const GlrPlan&, const GlrArgs& a, cudaStream_t st)
+template <typename T, int E> cudaError_t forward_of(const GlrPlan& P, const GlrArgs& a, cudaStream_t st)
 {
-    return launch<T, VEC, kSteps, 8, 8, BWD>(a, st);
+    if (P.steps == 1) return launch(glr_forward_kernel<T, E, 1, 1, 1>, 1, 1, a, st);
+    if (P.warps == 1) return launch(glr_forward_kernel<T, E, kSteps, 1, 1>, 1, 1, a, st);
+    switch (P.cluster) {
+    case 1: return launch(glr_forward_kernel<T, E, kSteps, 8, 1>, 8, 1, a, st);
+    case 2: return launch(glr_forward_kernel<T, E, kSteps, 8, 2>, 8, 2, a, st);
+    case 4: return launch(glr_forward_kernel<T, E, kSteps, 8, 4>, 8, 4, a, st);
+    default: return launch(glr_forward_kernel<T, E, kSteps, 8, 8>, 8, 8, a, st);
+    }
 }
 
-template <bool BWD> cudaError_t run_any(const kan_glr_shape& s, const GlrPlan& P, const GlrArgs& a, cudaStream_t st)
+template <typename T, int E> cudaError_t backward_of(const GlrPlan& P, const GlrArgs& a, cudaStream_t st)
 {
-    if (s.dtype == KAN_F32) return run<float, 1, BWD>(P, a, st);
-    return P.vec == 2 ? run<__nv_bfloat16, 2, BWD>(P, a, st) : run<__nv_bfloat16, 1, BWD>(P, a, st);
+    if (P.warps == 1) return launch(glr_backward_kernel<T, E, kSteps, 1, 1>, 1, 1, a, st);
+    switch (P.cluster) {
+    case 1: return launch(glr_backward_kernel<T, E, kSteps, 8, 1>, 8, 1, a, st);
+    case 2: return launch(glr_backward_kernel<T, E, kSteps, 8, 2>, 8, 2, a, st);
+    case 4: return launch(glr_backward_kernel<T, E, kSteps, 8, 4>, 8, 4, a, st);
+    default: return launch(glr_backward_kernel<T, E, kSteps, 8, 8>, 8, 8, a, st);
+    }
 }
 
 // Two bf16 channels per thread where every row of every operand begins on 4 bytes.
@@ -508,8 +692,6 @@ bool misaligned(const kan_glr_shape& s, std::initializer_list<const void*> ops, 
         if (reinterpret_cast<uintptr_t>(p) % 4) return true;
     return false;
 }
-
-constexpr int kMaxCluster = 8;
 
 }  // namespace
 }  // namespace kan
@@ -548,9 +730,10 @@ kan_status kan_glr_forward(const kan_glr_shape* s, const void* x, const void* r,
     common_args(*s, a);
     a.x = x, a.r = r, a.g = g, a.decay = decay, a.reset = reset, a.h0 = h0;
     a.y = y, a.h_last = h_last, a.kept = kept;
-    const GlrPlan P = plan_of(*s, vec_of(*s, a));
+    const GlrPlan P = plan_of(*s, vec_of(*s, a), false);
     a.strips = P.strips;
-    e = run_any<false>(*s, P, a, cs);
+    if (s->dtype == KAN_F32) e = forward_of<float, 1>(P, a, cs);
+    else e = P.vec == 2 ? forward_of<__nv_bfloat16, 2>(P, a, cs) : forward_of<__nv_bfloat16, 1>(P, a, cs);
     return e == cudaSuccess ? KAN_OK : gl_fail(KAN_ERR_CUDA, cudaGetErrorString(e));
 }
 
@@ -577,7 +760,7 @@ kan_status kan_glr_backward(const kan_glr_shape* s, const void* x, const void* r
     common_args(*s, a);
     a.x = x, a.r = r, a.g = g, a.decay = decay, a.reset = reset, a.kept = const_cast<float*>(kept);
     a.dy = dy, a.dh_last = dh_last, a.dx = dx, a.dr = dr, a.dg = dg, a.dh0 = dh0;
-    const GlrPlan P = plan_of(*s, vec_of(*s, a));
+    const GlrPlan P = plan_of(*s, vec_of(*s, a), true);
     a.strips = P.strips;
     const int64_t parts = s->batch * P.cluster;
     if (ddecay) {
@@ -585,7 +768,8 @@ kan_status kan_glr_backward(const kan_glr_shape* s, const void* x, const void* r
             return gl_fail(KAN_ERR_WORKSPACE, "workspace too small");
         a.part = reinterpret_cast<double*>(workspace);
     }
-    e = run_any<true>(*s, P, a, cs);
+    if (s->dtype == KAN_F32) e = backward_of<float, 1>(P, a, cs);
+    else e = P.vec == 2 ? backward_of<__nv_bfloat16, 2>(P, a, cs) : backward_of<__nv_bfloat16, 1>(P, a, cs);
     if (e == cudaSuccess && ddecay) {
         glr_decay_kernel<<<(unsigned)((s->channels + 127) / 128), 128, 0, cs>>>(a.part, parts, s->channels, decay, ddecay);
         count_launch();
