@@ -12,10 +12,11 @@
 //   dL = d (a h_{t-1} - a^2 u / m)          (with respect to L = log a)
 //   dr = dL L (1 - s),  ddecay = sum dL L sigmoid(decay) / lambda
 //
-// Both directions are scans of affine maps h -> A h + B.  A long memory has A
-// next to 1, where fp32 holds A - 1 but not A to 24 bits, a short one has A
-// next to 0, where it is the other way round: a factor is kept as A - 1 (not
-// positive) above about one half and as A (positive) below, see Factor.
+// Both directions are scans of affine maps h -> A h + B.  Within a thread's
+// steps a step is one fused multiply-add.  Between threads factors multiply as
+// sums of y = -log a, and A goes as A - 1 above about one half (a long memory
+// has A next to 1, where fp32 holds A - 1 but not A to 24 bits) and as A below
+// (next to 0 it is the other way round): see Factor.
 //
 // Split (one pass over HBM): a warp's lanes hold neighbouring channels, a
 // thread S steps of its channels in registers; the W warps of a block and the
@@ -32,6 +33,7 @@
 // (fp32): the backward recomputes the states within a block from it, so it
 // reads 1/2 byte an element instead of y, and unrounded states.
 #include <algorithm>
+#include <atomic>
 
 #include "kan_device.cuh"
 #include "kan_vec.cuh"
@@ -59,11 +61,11 @@ struct GlrArgs {
     float* dh0;                         // [B, C] or null
     double* part;                       // [B * cluster][C] partial sums for ddecay, or null
     int64_t B, T, C;
-    int strips;                         // ceil(C / (32 VEC))
+    int strips;                         // ceil(C / 64)
 };
 
-// Factor: a number v that stands for A in [0, 1].  v in (-1, 0]: A = 1 + v;  v > 0: A = v;  v = kHard: A = 0, and what
-// it multiplies is cut off even if it is not finite (L = -inf, which stands for a reset).
+// Factor of many steps: a number v that stands for A in [0, 1].  v in (-1, 0]: A = 1 + v;  v > 0: A = v;  v = kHard:
+// A = 0, and what it multiplies is cut off even if it is not finite (a reset).
 constexpr float kHard = -2.0f;
 constexpr float kTiny = 1e-37f;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -91,6 +93,12 @@ __device__ __forceinline__ float min_nan(float x, float y)
 {
     float r;
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float x, float y)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
     return r;
 }
 
@@ -164,57 +172,57 @@ template <int E> __device__ __forceinline__ F<E> rcp_of(F<E> x)
     return each(x, [](float t) { return rcp(t); });
 }
 
-// The factor exp(L), L <= 0 (a NaN passes).
-template <int E> __device__ __forceinline__ F<E> factor_of(F<E> L)
+// 1 - e^-y for 0 <= y <= 1/2: y sum_{k=0..7} (-y)^k / (k+1)!; the next term is below 2^-26 of it
+template <int E> __device__ __forceinline__ F<E> rest_series(F<E> y)
 {
-    // exp(L) - 1 = sum_{k=1..8} L^k / k!; the next term is below 2^-26 of the sum at L = -0.5
-    F<E> s = fma(L, F<E>::all(1.0f / 40320.0f), F<E>::all(1.0f / 5040.0f));
-    s = fma(s, L, F<E>::all(1.0f / 720.0f));
-    s = fma(s, L, F<E>::all(1.0f / 120.0f));
-    s = fma(s, L, F<E>::all(1.0f / 24.0f));
-    s = fma(s, L, F<E>::all(1.0f / 6.0f));
-    s = fma(s, L, F<E>::all(0.5f));
-    s = fma(s, L, F<E>::all(1.0f)) * L;
-    const F<E> big = each(L * F<E>::all(kLog2e), [](float t) {
-        const float x = ex2(t);
-        return x < kTiny ? kTiny : x;
-    });
-    float l[E], p[E], b[E];
-    L.get(l);
-    s.get(p);
-    big.get(b);
+    F<E> s = fma(y, F<E>::all(-1.0f / 40320.0f), F<E>::all(1.0f / 5040.0f));
+    s = fma(s, y, F<E>::all(-1.0f / 720.0f));
+    s = fma(s, y, F<E>::all(1.0f / 120.0f));
+    s = fma(s, y, F<E>::all(-1.0f / 24.0f));
+    s = fma(s, y, F<E>::all(1.0f / 6.0f));
+    s = fma(s, y, F<E>::all(-0.5f));
+    return fma(s, y, F<E>::all(1.0f)) * y;
+}
+template <int E> __device__ __forceinline__ F<E> exp_neg(F<E> y)
+{
+    return each(y * F<E>::all(-kLog2e), [](float t) { return ex2(t); });
+}
+template <int E> __device__ __forceinline__ F<E> pick_small(F<E> y, F<E> small, F<E> large)
+{
+    float t[E], p[E], q[E];
+    y.get(t);
+    small.get(p);
+    large.get(q);
 #pragma unroll
-    for (int e = 0; e < E; ++e) p[e] = l[e] > -0.5f ? p[e] : b[e];
+    for (int e = 0; e < E; ++e) p[e] = t[e] < 0.5f ? p[e] : q[e];
     return F<E>::of(p);
 }
-__device__ __forceinline__ float value_of(float v) { return v > 0.0f ? v : 1.0f + v; }      // not for kHard
-// 1 - A^2
-template <int E> __device__ __forceinline__ F<E> one_minus_sq(F<E> v)
+// A step's a = e^-y and 1 - a^2 (a NaN passes).
+template <int E> __device__ __forceinline__ void decay_of(F<E> y, F<E>& av, F<E>& m2)
 {
-    // -v v + c with c = 1 (v = A) or -2 v (v = A - 1)
-    const F<E> c = each(v, [](float t) { return t > 0.0f ? 1.0f : -2.0f * t; });
-    return fma(v * F<E>::all(-1.0f), v, c);
+    const F<E> r = rest_series(y), big = exp_neg(y), one = F<E>::all(1.0f), neg = F<E>::all(-1.0f);
+    const F<E> rest = pick_small(y, r, fma(big, neg, one));
+    av = pick_small(y, fma(r, neg, one), big);
+    m2 = rest * fma(rest, neg, F<E>::all(2.0f));
 }
-// A h + B, v not kHard
-template <int E> __device__ __forceinline__ F<E> walk(F<E> v, F<E> B, F<E> h)
+
+// Factor of many steps, whose y sum up to this (inf: a reset was among them).
+template <int E> __device__ __forceinline__ F<E> factor_of(F<E> y)
 {
-    return fma(v, h, B) + each(v, h, [](float t, float x) { return t > 0.0f ? 0.0f : x; });
+    const F<E> big = each(exp_neg(y), [](float t) { return t < kTiny ? kTiny : t; });
+    const F<E> v = pick_small(y, rest_series(y) * F<E>::all(-1.0f), big);
+    return each(y, v, [](float l, float t) { return l == INFINITY ? kHard : t; });
 }
+// A h + B
 template <int E> __device__ __forceinline__ F<E> apply(F<E> v, F<E> B, F<E> h)
 {
     float t[E], b[E], r[E];
-    walk(v, B, h).get(r);
+    (fma(v, h, B) + each(v, h, [](float u, float x) { return u > 0.0f ? 0.0f : x; })).get(r);
     v.get(t);
     B.get(b);
 #pragma unroll
     for (int e = 0; e < E; ++e) r[e] = t[e] == kHard ? b[e] : r[e];
     return F<E>::of(r);
-}
-// the factor of steps whose L sum up to this; -inf: a reset was among them
-template <int E> __device__ __forceinline__ F<E> factor_or_cut(F<E> L)
-{
-    const F<E> v = factor_of(L);
-    return each(L, v, [](float l, float t) { return l == -INFINITY ? kHard : t; });
 }
 
 __device__ __forceinline__ float softplus_of(float d) { return fmaxf(d, 0.0f) + log1pf(expf(-fabsf(d))); }
@@ -236,7 +244,7 @@ __device__ __forceinline__ void st_cluster(const void* local, uint32_t rank, flo
     asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(d), "f"(v.x), "f"(v.y) : "memory");
 }
 
-// Shared memory of the exchange: maps (factor, offset) and sums of L of the block's warps, maps of the cluster's blocks
+// Shared memory of the exchange: maps (factor, offset) and sums of y of the block's warps, maps of the cluster's blocks
 // (two sets, written by turns).
 template <int E, int W, int CL> struct Meet {
     float2 agg[W][E][32];
@@ -244,13 +252,13 @@ template <int E, int W, int CL> struct Meet {
     float2 tot[2][CL][E][32];
 };
 
-// Exchange of one span of the cluster: every thread gives its map (L, B); it gets the state that enters its steps, and
-// `run` moves past the whole span.  Position 0 comes first in the direction of the scan.  Factors multiply as sums of L.
+// Exchange of one span of the cluster: every thread gives its map (y, B); it gets the state that enters its steps, and
+// `run` moves past the whole span.  Position 0 comes first in the direction of the scan.
 template <int E, int W, int CL>
 __device__ __forceinline__ F<E> exchange(Meet<E, W, CL>& s, int parity, int wpos, int cpos, F<E> L, F<E> B, F<E>& run)
 {
     const int lane = threadIdx.x & 31;
-    const F<E> v = factor_or_cut(L);
+    const F<E> v = factor_of(L);
     F<E> in = run;
     if constexpr (W * CL == 1) {
         run = apply(v, B, run);
@@ -291,11 +299,11 @@ __device__ __forceinline__ F<E> exchange(Meet<E, W, CL>& s, int parity, int wpos
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
                     const float l = s.len[w][e][lane];
-                    lt[e] = l == -INFINITY ? l : lt[e] + l;          // a reset cuts off a NaN before it
+                    lt[e] = l == INFINITY ? l : lt[e] + l;           // a reset cuts off a NaN before it
                 }
             }
             float p[E], q[E];
-            factor_or_cut(F<E>::of(lt)).get(p);
+            factor_of(F<E>::of(lt)).get(p);
             bt.get(q);
 #pragma unroll
             for (int e = 0; e < E; ++e)
@@ -323,131 +331,191 @@ __device__ __forceinline__ F<E> exchange(Meet<E, W, CL>& s, int parity, int wpos
     return in;
 }
 
+// The inputs of a thread's S steps of E neighbouring channels, as they lie in memory: one vector a step, or (LV = 1)
+// one element at a time where rows are not whole vectors.
+template <typename T, int E, int LV, int S> struct Steps {
+    Pack<T, LV> q[S][E / LV];
+    __device__ __forceinline__ void load(const T* p, int64_t stride, int live, int chans)
+    {
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+#pragma unroll
+            for (int j = 0; j < E / LV; ++j) {
+                q[i][j] = Pack<T, LV>::zero();
+                if (i < live && j * LV < chans) q[i][j] = Pack<T, LV>::load(p + j * LV);
+            }
+            p += stride;
+        }
+    }
+    __device__ __forceinline__ F<E> get(int i) const
+    {
+        float v[E];
+#pragma unroll
+        for (int j = 0; j < E / LV; ++j) {
+            float w[LV];
+            q[i][j].unpack(w);
+#pragma unroll
+            for (int e = 0; e < LV; ++e) v[j * LV + e] = w[e];
+        }
+        return F<E>::of(v);
+    }
+};
+template <typename T, int LV, int E> __device__ __forceinline__ void store_step(T* p, F<E> x, int chans)
+{
+    float v[E];
+    x.get(v);
+#pragma unroll
+    for (int j = 0; j < E / LV; ++j) {
+        if (j * LV < chans) {
+            float w[LV];
+#pragma unroll
+            for (int e = 0; e < LV; ++e) w[e] = v[j * LV + e];
+            Pack<T, LV>::pack(w).store(p + j * LV);
+        }
+    }
+}
+template <int E> __device__ __forceinline__ F<E> load_f32(const float* p, int chans)
+{
+    float v[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = e < chans ? p[e] : 0.0f;
+    return F<E>::of(v);
+}
+template <int E> __device__ __forceinline__ void store_f32(float* p, F<E> x, int chans)
+{
+    float v[E];
+    x.get(v);
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        if (e < chans) p[e] = v[e];
+}
+template <int S> __device__ __forceinline__ uint32_t cuts_of(const unsigned char* z, int live)
+{
+    uint32_t cut = 0;
+    if (z) {
+#pragma unroll
+        for (int i = 0; i < S; ++i)
+            if (i < live && z[i]) cut |= 1u << i;
+    }
+    return cut;
+}
+
+constexpr int E = 2;              // channels per thread: their arithmetic goes through the packed f32x2 instructions
+
+// Where a thread stands: its block's unit is (sequence b, strip of channels).
+struct Place {
+    int warp, rank, chans;           // chans: channels of this thread that exist (0..E)
+    int64_t b, c;
+    __device__ __forceinline__ Place(const GlrArgs& a, int cl)
+    {
+        warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
+        rank = cl > 1 ? (int)cluster_rank() : 0;
+        const int unit = blockIdx.x / cl;
+        b = unit / a.strips;
+        c = (unit - b * a.strips) * (32 * E) + (threadIdx.x & 31) * E;
+        chans = (int)max((int64_t)0, min((int64_t)E, a.C - c));
+    }
+};
+
 // Forward: S steps a thread, W warps a block, CL blocks a cluster.
-template <typename T, int E, int S, int W, int CL>
-__global__ void __launch_bounds__(32 * W, W == 8 ? 4 : 1) glr_forward_kernel(const GlrArgs a)
+template <typename T, int LV, int S, int W, int CL>
+__global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_forward_kernel(const GlrArgs a)
 {
     __shared__ Meet<E, W, CL> meet;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int rank = CL > 1 ? (int)cluster_rank() : 0;
-    const int64_t unit = blockIdx.x / CL;                // (sequence, strip of channels)
-    const int64_t b = unit / a.strips;
-    const int64_t c = (unit - b * a.strips) * (32 * E) + lane * E;
-    const bool on = c < a.C;                             // E divides C
+    const Place at(a, CL);
     constexpr int64_t SPAN = (int64_t)S * W * CL;
-    using V = Pack<T, E>;
-    const int64_t first = ((int64_t)rank * W + warp) * S;    // this thread's first step within a span
-    const T* X = reinterpret_cast<const T*>(a.x) + b * a.xb + c;
-    const T* R = reinterpret_cast<const T*>(a.r) + b * a.rb + c;
-    const T* G = reinterpret_cast<const T*>(a.g) + b * a.gb + c;
-    T* Y = reinterpret_cast<T*>(a.y) + b * a.T * a.C + c;
-    const unsigned char* Z = a.reset ? a.reset + b * a.T : nullptr;
-    float* K = a.kept ? a.kept + b * ((a.T + kSteps - 1) / kSteps) * a.C + c : nullptr;
+    const int64_t first = ((int64_t)at.rank * W + at.warp) * S;      // this thread's first step within a span
+    const int chans = at.chans;
+    const int64_t state = at.b * a.C + at.c;
+    const T* X = reinterpret_cast<const T*>(a.x) + at.b * a.xb + at.c;
+    const T* R = reinterpret_cast<const T*>(a.r) + at.b * a.rb + at.c;
+    const T* G = reinterpret_cast<const T*>(a.g) + at.b * a.gb + at.c;
+    T* Y = reinterpret_cast<T*>(a.y) + at.b * a.T * a.C + at.c;
+    const unsigned char* Z = a.reset ? a.reset + at.b * a.T : nullptr;
+    float* K = a.kept ? a.kept + at.b * ((a.T + kSteps - 1) / kSteps) * a.C + at.c : nullptr;
 
-    float t0[E], t1[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        t0[e] = on ? -softplus_of(a.decay[c + e]) : 0.0f;
-        t1[e] = on && a.h0 ? a.h0[b * a.C + c + e] : 0.0f;
-    }
-    const F<E> neg_lambda = F<E>::of(t0), one = F<E>::all(1.0f), zero = F<E>::all(0.0f);
-    F<E> run = F<E>::of(t1);
+    const F<E> lambda = each(load_f32<E>(a.decay + at.c, chans), [](float d) { return softplus_of(d); });
+    const F<E> one = F<E>::all(1.0f), zero = F<E>::all(0.0f);
+    F<E> run = a.h0 ? load_f32<E>(a.h0 + state, chans) : zero;
+    Steps<T, E, LV, S> qx, qr, qg;
+    uint32_t cut;
+    auto fetch = [&](int64_t t) {
+        const int live = (int)min((int64_t)S, a.T - t);              // may be negative
+        qr.load(R + t * a.rt, a.rt, live, chans);
+        qg.load(G + t * a.gt, a.gt, live, chans);
+        qx.load(X + t * a.xt, a.xt, live, chans);
+        cut = cuts_of<S>(Z + t, Z ? live : 0);
+    };
+    fetch(first);
     if constexpr (CL > 1) cluster_sync_all();            // every block of the cluster runs before its memory is written
 
     int parity = 0;
     for (int64_t base = 0; base < a.T; base += SPAN, parity ^= 1) {
         const int64_t t = base + first;
         const int live = (int)min((int64_t)S, max((int64_t)0, a.T - t));
-        V qx[S], qr[S], qg[S];
-        uint32_t cut = 0;
+        const uint32_t cuts = cut;
+        F<E> fa[S], bb[S], len = zero, B = zero;
 #pragma unroll
         for (int i = 0; i < S; ++i) {
-            qx[i] = qr[i] = qg[i] = V::zero();
-            if (i < live && on) {
-                qr[i] = V::load(R + (t + i) * a.rt);
-                qg[i] = V::load(G + (t + i) * a.gt);
-                qx[i] = V::load(X + (t + i) * a.xt);
+            const F<E> s = rcp_of(one + exp_minus<115>(qr.get(i)));
+            const F<E> y = s * (i < live ? lambda : zero);           // past the end: a = 1
+            F<E> m2;
+            decay_of(y, fa[i], m2);
+            // m sigmoid(g) = m^2 / sqrt(m^2 (1 + e)^2) with e = exp(-g): one rsqrt
+            const F<E> q = one + exp_minus<60>(qg.get(i));
+            bb[i] = m2 * each(m2 * q * q, [](float u) { return rsq(max_nan(u, kTiny)); }) * qx.get(i);
+            len = len + y;
+            B = fma(fa[i], B, bb[i]);
+        }
+        if (base + SPAN < a.T) fetch(t + SPAN);
+        if (cuts) {                                      // resets among the steps: they cut off what comes before them
+            B = zero;
+            bool after = false;
+#pragma unroll
+            for (int i = 0; i < S; ++i) {
+                if (cuts >> i & 1) {
+                    B = zero;
+                    after = true;
+                }
+                B = fma(fa[i], B, bb[i]);
             }
+            if (after) len = F<E>::all(INFINITY);
         }
-        if (Z) {
-#pragma unroll
-            for (int i = 0; i < S; ++i)
-                if (i < live && Z[t + i]) cut |= 1u << i;
-        }
-        F<E> fa[S], bb[S], L = zero, B = zero;
+        F<E> h = exchange<E, W, CL>(meet, parity, at.warp, at.rank, len, B, run);
+        if (K && live > 0) store_f32<E>(K + (t / kSteps) * a.C, h, chans);
+        T* y = Y + t * a.C;
 #pragma unroll
         for (int i = 0; i < S; ++i) {
-            float vx[E], vr[E], vg[E];
-            qx[i].unpack(vx);
-            qr[i].unpack(vr);
-            qg[i].unpack(vg);
-            const F<E> s = rcp_of(one + exp_minus<115>(F<E>::of(vr)));
-            const F<E> l = s * (i < live ? neg_lambda : zero);       // past the end: a = 1
-            fa[i] = factor_of(l);
-            // m sigmoid(g) = sqrt(m^2) / (1 + e) = m^2 / sqrt(m^2 (1 + e)^2), one rsqrt
-            const F<E> m2 = one_minus_sq(fa[i]), q = one + exp_minus<60>(F<E>::of(vg));
-            const F<E> w = m2 * each(m2 * q * q, [](float u) { return rsq(u < kTiny ? kTiny : u); });
-            bb[i] = w * F<E>::of(vx);
-            const bool z = cut >> i & 1;
-            L = z ? F<E>::all(-INFINITY) : L + l;
-            B = walk(fa[i], bb[i], z ? zero : B);
-        }
-        F<E> h = exchange<E, W, CL>(meet, parity, warp, rank, L, B, run);
-        if (K && live > 0 && on) {
-            float f[E];
-            h.get(f);
-#pragma unroll
-            for (int e = 0; e < E; ++e) K[(t / kSteps) * a.C + e] = f[e];
-        }
-#pragma unroll
-        for (int i = 0; i < S; ++i) {
-            h = walk(fa[i], bb[i], cut >> i & 1 ? zero : h);
-            if (i < live && on) {
-                float f[E];
-                h.get(f);
-                V::pack(f).store(Y + (t + i) * a.C);
-            }
+            if (cuts >> i & 1) h = zero;
+            h = fma(fa[i], h, bb[i]);
+            if (i < live) store_step<T, LV, E>(y, h, chans);
+            y += a.C;
         }
     }
-    if (a.h_last && on && rank == 0 && warp == 0) {
-        float f[E];
-        run.get(f);
-#pragma unroll
-        for (int e = 0; e < E; ++e) a.h_last[b * a.C + c + e] = f[e];
-    }
+    if (a.h_last && at.rank == 0 && at.warp == 0) store_f32<E>(a.h_last + state, run, chans);
 }
 
 // Backward: the same split, walked from the end of the sequence.
-template <typename T, int E, int S, int W, int CL>
+template <typename T, int LV, int W, int CL>
 __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_backward_kernel(const GlrArgs a)
 {
-    static_assert(S == kSteps, "a thread's steps begin at a kept state");
+    constexpr int S = kSteps;                            // a thread's steps begin at a kept state
     __shared__ Meet<E, W, CL> meet;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int rank = CL > 1 ? (int)cluster_rank() : 0;
-    const int64_t unit = blockIdx.x / CL;
-    const int64_t b = unit / a.strips;
-    const int64_t c = (unit - b * a.strips) * (32 * E) + lane * E;
-    const bool on = c < a.C;
+    const Place at(a, CL);
     constexpr int64_t SPAN = (int64_t)S * W * CL;
-    using V = Pack<T, E>;
-    const int64_t first = ((int64_t)rank * W + warp) * S;
-    const T* X = reinterpret_cast<const T*>(a.x) + b * a.xb + c;
-    const T* R = reinterpret_cast<const T*>(a.r) + b * a.rb + c;
-    const T* G = reinterpret_cast<const T*>(a.g) + b * a.gb + c;
-    const int64_t dense = b * a.T * a.C + c;
+    const int64_t first = ((int64_t)at.rank * W + at.warp) * S;
+    const int chans = at.chans;
+    const int64_t state = at.b * a.C + at.c, dense = at.b * a.T * a.C + at.c;
+    const T* X = reinterpret_cast<const T*>(a.x) + at.b * a.xb + at.c;
+    const T* R = reinterpret_cast<const T*>(a.r) + at.b * a.rb + at.c;
+    const T* G = reinterpret_cast<const T*>(a.g) + at.b * a.gb + at.c;
     const T* D = reinterpret_cast<const T*>(a.dy) + dense;
-    const unsigned char* Z = a.reset ? a.reset + b * a.T : nullptr;
-    const float* K = a.kept + b * ((a.T + kSteps - 1) / kSteps) * a.C + c;
+    const unsigned char* Z = a.reset ? a.reset + at.b * a.T : nullptr;
+    const float* K = a.kept + at.b * ((a.T + kSteps - 1) / kSteps) * a.C + at.c;
 
-    float t0[E], t1[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        t0[e] = on ? -softplus_of(a.decay[c + e]) : 0.0f;
-        t1[e] = on && a.dh_last ? a.dh_last[b * a.C + c + e] : 0.0f;
-    }
-    const F<E> neg_lambda = F<E>::of(t0), one = F<E>::all(1.0f), zero = F<E>::all(0.0f);
-    F<E> run = F<E>::of(t1);
+    const F<E> lambda = each(load_f32<E>(a.decay + at.c, chans), [](float d) { return softplus_of(d); });
+    const F<E> one = F<E>::all(1.0f), zero = F<E>::all(0.0f), neg = F<E>::all(-1.0f);
+    F<E> run = a.dh_last ? load_f32<E>(a.dh_last + state, chans) : zero;
     double acc[E];                                       // sum of dL L
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.0;
@@ -457,115 +525,77 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_backward_kernel(co
     for (int64_t base = (a.T - 1) / SPAN * SPAN; base >= 0; base -= SPAN, parity ^= 1) {
         const int64_t t = base + first;
         const int live = (int)min((int64_t)S, max((int64_t)0, a.T - t));
-        V qx[S], qr[S], qg[S], qd[S];
-        uint32_t cut = 0;
-#pragma unroll
-        for (int i = 0; i < S; ++i) {
-            qx[i] = qr[i] = qg[i] = qd[i] = V::zero();
-            if (i < live && on) {
-                qr[i] = V::load(R + (t + i) * a.rt);
-                qg[i] = V::load(G + (t + i) * a.gt);
-                qx[i] = V::load(X + (t + i) * a.xt);
-                qd[i] = V::load(D + (t + i) * a.C);
-            }
-        }
-        if (Z) {
-#pragma unroll
-            for (int i = 0; i < S; ++i)
-                if (i < live && Z[t + i]) cut |= 1u << i;
-        }
-        F<E> h = zero;
-        if (live > 0 && on) {
-            float f[E];
-#pragma unroll
-            for (int e = 0; e < E; ++e) f[e] = K[(t / kSteps) * a.C + e];
-            h = F<E>::of(f);
-        }
+        Steps<T, E, LV, S> qx, qr, qg, qd;
+        qr.load(R + t * a.rt, a.rt, live, chans);
+        qg.load(G + t * a.gt, a.gt, live, chans);
+        qx.load(X + t * a.xt, a.xt, live, chans);
+        qd.load(D + t * a.C, a.C, live, chans);
+        const uint32_t cut = cuts_of<S>(Z + t, Z ? live : 0);
+        F<E> h = live > 0 ? load_f32<E>(K + (t / kSteps) * a.C, chans) : zero;
         // per step: the factor, and what d multiplies in each gradient:
         //   dx = d cx,  dg = dx cg,  dL L = d cl,  dr = dL L cr
-        F<E> fa[S], cx[S], cg[S], cl[S], cr[S], L = zero;
+        F<E> fa[S], cx[S], cg[S], cl[S], cr[S], len = zero;
 #pragma unroll
         for (int i = 0; i < S; ++i) {
-            float vx[E], vr[E], vg[E];
-            qx[i].unpack(vx);
-            qr[i].unpack(vr);
-            qg[i].unpack(vg);
-            const F<E> er = exp_minus<115>(F<E>::of(vr)), eg = exp_minus<115>(F<E>::of(vg));
-            const F<E> s = rcp_of(one + er), sg = rcp_of(one + eg), x = F<E>::of(vx);
-            const F<E> l = s * (i < live ? neg_lambda : zero);
-            fa[i] = factor_of(l);
-            const F<E> m2 = one_minus_sq(fa[i]);
-            const F<E> rm = each(m2, [](float u) { return u < kTiny ? 0.0f : rsq(u); });   // 1 / m; L / m goes to 0 with L
-            const F<E> av = each(fa[i], [](float v) { return value_of(v); });
-            const F<E> u = sg * x, hp = cut >> i & 1 ? zero : h;
+            const F<E> er = exp_minus<115>(qr.get(i)), eg = exp_minus<115>(qg.get(i));
+            const F<E> s = rcp_of(one + er), sg = rcp_of(one + eg), x = qx.get(i);
+            const F<E> y = s * (i < live ? lambda : zero);
+            F<E> m2;
+            decay_of(y, fa[i], m2);
+            // 1 / m, held where m is 0 (there y is 0 too, and y / m goes to 0 with it)
+            const F<E> rm = each(m2, [](float u) { return rsq(max_nan(u, kTiny)); });
+            if (cut >> i & 1) h = zero;
             cx[i] = m2 * rm * sg;
             cg[i] = x * (eg * sg);
             cr[i] = er * s;
-            cl[i] = av * l * fma(av * F<E>::all(-1.0f), u * rm, hp);
-            h = walk(fa[i], cx[i] * x, hp);
-            L = cut >> i & 1 ? F<E>::all(-INFINITY) : L + l;
+            // a L (h - a u / m), L = -y
+            cl[i] = fa[i] * y * fma(fa[i] * rm, sg * x, h * neg);
+            h = fma(fa[i], h, cx[i] * x);
+            len = len + y;
         }
         // the map of these steps, from the last to the first: gamma -> a (gamma + dy)
         F<E> B = zero;
 #pragma unroll
         for (int i = S - 1; i >= 0; --i) {
-            float vd[E];
-            qd[i].unpack(vd);
-            const F<E> d = B + F<E>::of(vd);
-            B = cut >> i & 1 ? zero : walk(fa[i], zero, d);
+            B = fa[i] * (B + qd.get(i));
+            if (cut >> i & 1) B = zero;
         }
-        // (a reset cuts off what comes from later steps, a NaN of which would pass the sum of L)
-        if (cut) L = F<E>::all(-INFINITY);
-        F<E> flow = exchange<E, W, CL>(meet, parity, W - 1 - warp, CL - 1 - rank, L, B, run);
+        if (cut) len = F<E>::all(INFINITY);
+        F<E> flow = exchange<E, W, CL>(meet, parity, W - 1 - at.warp, CL - 1 - at.rank, len, B, run);
         F<E> part = zero;
+        int64_t o = dense + (t + S - 1) * a.C;
 #pragma unroll
         for (int i = S - 1; i >= 0; --i) {
+            const F<E> d = flow + qd.get(i);
+            const F<E> ox = d * cx[i], ol = d * cl[i];
+            flow = fa[i] * d;
+            if (cut >> i & 1) flow = zero;
             if (i < live) {
-                float vd[E], f[E];
-                qd[i].unpack(vd);
-                const F<E> d = flow + F<E>::of(vd);
-                const F<E> ox = d * cx[i], ol = d * cl[i];
                 part = part + ol;
-                flow = cut >> i & 1 ? zero : walk(fa[i], zero, d);
-                if (on) {
-                    const int64_t at = dense + (t + i) * a.C;
-                    if (a.dx) {
-                        ox.get(f);
-                        V::pack(f).store(reinterpret_cast<T*>(a.dx) + at);
-                    }
-                    if (a.dr) {
-                        (ol * cr[i]).get(f);
-                        V::pack(f).store(reinterpret_cast<T*>(a.dr) + at);
-                    }
-                    if (a.dg) {
-                        (ox * cg[i]).get(f);
-                        V::pack(f).store(reinterpret_cast<T*>(a.dg) + at);
-                    }
-                }
+                if (a.dx) store_step<T, LV, E>(reinterpret_cast<T*>(a.dx) + o, ox, chans);
+                if (a.dr) store_step<T, LV, E>(reinterpret_cast<T*>(a.dr) + o, ol * cr[i], chans);
+                if (a.dg) store_step<T, LV, E>(reinterpret_cast<T*>(a.dg) + o, ox * cg[i], chans);
             }
+            o -= a.C;
         }
         float f[E];
         part.get(f);
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] += (double)f[e];
     }
-    if (a.dh0 && on && rank == 0 && warp == 0) {
-        float f[E];
-        run.get(f);
-#pragma unroll
-        for (int e = 0; e < E; ++e) a.dh0[b * a.C + c + e] = f[e];
-    }
+    if (a.dh0 && at.rank == 0 && at.warp == 0) store_f32<E>(a.dh0 + state, run, chans);
     if (a.part) {
         __shared__ double red[W][E][32];
+        const int lane = threadIdx.x & 31;
 #pragma unroll
-        for (int e = 0; e < E; ++e) red[warp][e][lane] = acc[e];
+        for (int e = 0; e < E; ++e) red[at.warp][e][lane] = acc[e];
         __syncthreads();
-        if (warp == 0 && on) {
+        if (at.warp == 0) {
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 double v = 0.0;
                 for (int w = 0; w < W; ++w) v += red[w][e][lane];
-                a.part[(b * CL + rank) * a.C + c + e] = v;
+                if (e < chans) a.part[(at.b * CL + at.rank) * a.C + at.c + e] = v;
             }
         }
     }
@@ -601,25 +631,28 @@ kan_status validate(const kan_glr_shape* s)
     return KAN_OK;
 }
 
-struct GlrPlan {
-    int vec, cluster, warps, steps, strips;
-};
-
-// Blocks of 8 warps; as many blocks of a cluster side by side in time as fill the SMs once (kResident blocks fit), at
-// most 8, no more than the sequence has steps for.  A block of one warp where 8 steps (or one) are all there is.
-GlrPlan plan_of(const kan_glr_shape& s, int vec, bool backward)
+// Clusters of a kernel that run at once on the current device, looked up once per device (a table per kernel).
+template <typename K> int resident(K kernel, int warps, int cluster, std::atomic<int> (&known)[64])
 {
-    GlrPlan P{};
-    P.vec = vec;
-    P.strips = (int)((s.channels + 32 * vec - 1) / (32 * vec));
-    P.steps = s.time == 1 && !backward ? 1 : kSteps;
-    P.warps = s.time <= kSteps ? 1 : 8;
-    P.cluster = 1;
-    const int64_t resident = 148 * (backward ? 2 : 4), units = s.batch * P.strips;
-    if (P.warps == 8)
-        while (P.cluster < kMaxCluster && units * P.cluster * 2 <= resident && s.time > (int64_t)P.cluster * 8 * kSteps)
-            P.cluster *= 2;
-    return P;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (n) return n;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(cluster);
+    cfg.blockDim = dim3(32 * warps);
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = cluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        n = 1;
+    }
+    known[dev].store(n, std::memory_order_relaxed);
+    return n;
 }
 
 template <typename K> cudaError_t launch(K kernel, int warps, int cluster, const GlrArgs& a, cudaStream_t st)
@@ -639,40 +672,67 @@ template <typename K> cudaError_t launch(K kernel, int warps, int cluster, const
     return e;
 }
 
-template <typename T, int E> cudaError_t forward_of(const GlrPlan& P, const GlrArgs& a, cudaStream_t st)
-{
-    if (P.steps == 1) return launch(glr_forward_kernel<T, E, 1, 1, 1>, 1, 1, a, st);
-    if (P.warps == 1) return launch(glr_forward_kernel<T, E, kSteps, 1, 1>, 1, 1, a, st);
-    switch (P.cluster) {
-    case 1: return launch(glr_forward_kernel<T, E, kSteps, 8, 1>, 8, 1, a, st);
-    case 2: return launch(glr_forward_kernel<T, E, kSteps, 8, 2>, 8, 2, a, st);
-    case 4: return launch(glr_forward_kernel<T, E, kSteps, 8, 4>, 8, 4, a, st);
-    default: return launch(glr_forward_kernel<T, E, kSteps, 8, 8>, 8, 8, a, st);
+// The kernels of one direction and operand type: blocks of 8 warps in clusters of 1 to 8, and a block of one warp for
+// sequences of at most 8 steps (and, forward, for a single one).
+template <typename T, int LV, bool BWD> struct Kernels {
+    static void (*of(int cluster))(const GlrArgs)
+    {
+        if constexpr (BWD)
+            return cluster == 1 ? glr_backward_kernel<T, LV, 8, 1> : cluster == 2 ? glr_backward_kernel<T, LV, 8, 2>
+                 : cluster == 4 ? glr_backward_kernel<T, LV, 8, 4> : glr_backward_kernel<T, LV, 8, 8>;
+        else
+            return cluster == 1 ? glr_forward_kernel<T, LV, kSteps, 8, 1> : cluster == 2 ? glr_forward_kernel<T, LV, kSteps, 8, 2>
+                 : cluster == 4 ? glr_forward_kernel<T, LV, kSteps, 8, 4> : glr_forward_kernel<T, LV, kSteps, 8, 8>;
     }
-}
-
-template <typename T, int E> cudaError_t backward_of(const GlrPlan& P, const GlrArgs& a, cudaStream_t st)
-{
-    if (P.warps == 1) return launch(glr_backward_kernel<T, E, kSteps, 1, 1>, 1, 1, a, st);
-    switch (P.cluster) {
-    case 1: return launch(glr_backward_kernel<T, E, kSteps, 8, 1>, 8, 1, a, st);
-    case 2: return launch(glr_backward_kernel<T, E, kSteps, 8, 2>, 8, 2, a, st);
-    case 4: return launch(glr_backward_kernel<T, E, kSteps, 8, 4>, 8, 4, a, st);
-    default: return launch(glr_backward_kernel<T, E, kSteps, 8, 8>, 8, 8, a, st);
+    // Blocks of a cluster lie side by side in time: the size that needs the fewest rounds of spans on a full device.
+    static int cluster_for(const GlrArgs& a)
+    {
+        static std::atomic<int> known[4][64];
+        const int64_t units = a.B * a.strips;
+        int best = 1;
+        int64_t cost = -1;
+        for (int i = 0; i < 4; ++i) {
+            const int cl = 1 << i;
+            const int64_t at_once = resident(of(cl), 8, cl, known[i]);
+            const int64_t c = (units + at_once - 1) / at_once * ((a.T + 8 * kSteps * cl - 1) / (8 * kSteps * cl));
+            if (cost < 0 || c < cost) {
+                cost = c;
+                best = cl;
+            }
+        }
+        return best;
     }
-}
+    static cudaError_t run(GlrArgs& a, int& cluster, cudaStream_t st)
+    {
+        cluster = 1;
+        if (a.T <= kSteps) {
+            if constexpr (BWD) return launch(glr_backward_kernel<T, LV, 1, 1>, 1, 1, a, st);
+            else if (a.T == 1) return launch(glr_forward_kernel<T, LV, 1, 1, 1>, 1, 1, a, st);
+            else return launch(glr_forward_kernel<T, LV, kSteps, 1, 1>, 1, 1, a, st);
+        }
+        cluster = cluster_for(a);
+        return launch(of(cluster), 8, cluster, a, st);
+    }
+};
 
-// Two bf16 channels per thread where every row of every operand begins on 4 bytes.
-int vec_of(const kan_glr_shape& s, const GlrArgs& a)
+// Whole vectors of the two channels of a thread where every row of every operand begins on one.
+bool pairs(const kan_glr_shape& s, const GlrArgs& a)
 {
-    if (s.dtype == KAN_F32) return 1;
     const uint64_t odd = (uint64_t)(s.channels | s.x_stride_b | s.x_stride_t | s.r_stride_b | s.r_stride_t | s.g_stride_b |
                                     s.g_stride_t) & 1;
     const uint64_t addr = (reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.r) |
                            reinterpret_cast<uintptr_t>(a.g) | reinterpret_cast<uintptr_t>(a.y) |
                            reinterpret_cast<uintptr_t>(a.dy) | reinterpret_cast<uintptr_t>(a.dx) |
-                           reinterpret_cast<uintptr_t>(a.dr) | reinterpret_cast<uintptr_t>(a.dg)) & 3;
-    return odd || addr ? 1 : 2;
+                           reinterpret_cast<uintptr_t>(a.dr) | reinterpret_cast<uintptr_t>(a.dg));
+    return !odd && addr % (s.dtype == KAN_F32 ? 8 : 4) == 0;
+}
+
+template <bool BWD> cudaError_t run(const kan_glr_shape& s, GlrArgs& a, int& cluster, cudaStream_t st)
+{
+    if (s.dtype == KAN_F32)
+        return pairs(s, a) ? Kernels<float, 2, BWD>::run(a, cluster, st) : Kernels<float, 1, BWD>::run(a, cluster, st);
+    return pairs(s, a) ? Kernels<__nv_bfloat16, 2, BWD>::run(a, cluster, st)
+                       : Kernels<__nv_bfloat16, 1, BWD>::run(a, cluster, st);
 }
 
 void common_args(const kan_glr_shape& s, GlrArgs& a)
@@ -681,6 +741,7 @@ void common_args(const kan_glr_shape& s, GlrArgs& a)
     a.rb = s.r_stride_b, a.rt = s.r_stride_t;
     a.gb = s.g_stride_b, a.gt = s.g_stride_t;
     a.B = s.batch, a.T = s.time, a.C = s.channels;
+    a.strips = (int)((s.channels + 32 * E - 1) / (32 * E));
 }
 
 bool misaligned(const kan_glr_shape& s, std::initializer_list<const void*> ops, std::initializer_list<const void*> f32)
@@ -730,10 +791,8 @@ kan_status kan_glr_forward(const kan_glr_shape* s, const void* x, const void* r,
     common_args(*s, a);
     a.x = x, a.r = r, a.g = g, a.decay = decay, a.reset = reset, a.h0 = h0;
     a.y = y, a.h_last = h_last, a.kept = kept;
-    const GlrPlan P = plan_of(*s, vec_of(*s, a), false);
-    a.strips = P.strips;
-    if (s->dtype == KAN_F32) e = forward_of<float, 1>(P, a, cs);
-    else e = P.vec == 2 ? forward_of<__nv_bfloat16, 2>(P, a, cs) : forward_of<__nv_bfloat16, 1>(P, a, cs);
+    int cluster;
+    e = run<false>(*s, a, cluster, cs);
     return e == cudaSuccess ? KAN_OK : gl_fail(KAN_ERR_CUDA, cudaGetErrorString(e));
 }
 
@@ -760,18 +819,15 @@ kan_status kan_glr_backward(const kan_glr_shape* s, const void* x, const void* r
     common_args(*s, a);
     a.x = x, a.r = r, a.g = g, a.decay = decay, a.reset = reset, a.kept = const_cast<float*>(kept);
     a.dy = dy, a.dh_last = dh_last, a.dx = dx, a.dr = dr, a.dg = dg, a.dh0 = dh0;
-    const GlrPlan P = plan_of(*s, vec_of(*s, a), true);
-    a.strips = P.strips;
-    const int64_t parts = s->batch * P.cluster;
     if (ddecay) {
-        if (!workspace || ws_bytes < (size_t)parts * s->channels * sizeof(double))
+        if (!workspace || ws_bytes < (size_t)s->batch * kMaxCluster * s->channels * sizeof(double))
             return gl_fail(KAN_ERR_WORKSPACE, "workspace too small");
         a.part = reinterpret_cast<double*>(workspace);
     }
-    if (s->dtype == KAN_F32) e = backward_of<float, 1>(P, a, cs);
-    else e = P.vec == 2 ? backward_of<__nv_bfloat16, 2>(P, a, cs) : backward_of<__nv_bfloat16, 1>(P, a, cs);
+    int cluster;
+    e = run<true>(*s, a, cluster, cs);
     if (e == cudaSuccess && ddecay) {
-        glr_decay_kernel<<<(unsigned)((s->channels + 127) / 128), 128, 0, cs>>>(a.part, parts, s->channels, decay, ddecay);
+        glr_decay_kernel<<<(unsigned)((s->channels + 127) / 128), 128, 0, cs>>>(a.part, s->batch * cluster, s->channels, decay, ddecay);
         count_launch();
         e = cudaGetLastError();
     }
