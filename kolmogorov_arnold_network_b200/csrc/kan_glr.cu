@@ -62,11 +62,10 @@ struct GlrArgs {
     double* part;                       // [B * cluster][C] partial sums for ddecay, or null
     int64_t B, T, C;
     int strips;                         // ceil(C / 64)
+    unsigned int* status;
 };
 
-// Factor of many steps: a number v that stands for A in [0, 1].  v in (-1, 0]: A = 1 + v;  v > 0: A = v;  v = kHard:
-// A = 0, and what it multiplies is cut off even if it is not finite (a reset).
-constexpr float kHard = -2.0f;
+constexpr float kCut = -1.0f;
 constexpr float kTiny = 1e-37f;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -102,45 +101,48 @@ __device__ __forceinline__ float max_nan(float x, float y)
     return r;
 }
 
-// E neighbouring channels of a thread; two of them go through the packed f32x2 instructions.
-template <int E> struct F;
-template <> struct F<1> {
-    float a;
-    __device__ __forceinline__ static F all(float x) { return {x}; }
-    __device__ __forceinline__ static F of(const float (&v)[1]) { return {v[0]}; }
-    __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = a; }
-};
-template <> struct F<2> {
-    uint64_t q;
-    __device__ __forceinline__ static F two(float x, float y)
+// E neighbouring channels of a thread.
+template <int E> struct F {
+    float v[E];
+    __device__ __forceinline__ static F all(float x)
     {
         F r;
-        asm("mov.b64 %0, {%1, %2};" : "=l"(r.q) : "f"(x), "f"(y));
+#pragma unroll
+        for (int e = 0; e < E; ++e) r.v[e] = x;
         return r;
     }
-    __device__ __forceinline__ static F all(float x) { return two(x, x); }
-    __device__ __forceinline__ static F of(const float (&v)[2]) { return two(v[0], v[1]); }
-    __device__ __forceinline__ void get(float (&v)[2]) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(v[0]), "=f"(v[1]) : "l"(q)); }
+    __device__ __forceinline__ static F of(const float (&x)[E])
+    {
+        F r;
+#pragma unroll
+        for (int e = 0; e < E; ++e) r.v[e] = x[e];
+        return r;
+    }
+    __device__ __forceinline__ void get(float (&x)[E]) const
+    {
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = v[e];
+    }
 };
-__device__ __forceinline__ F<1> fma(F<1> x, F<1> y, F<1> z) { return {fmaf(x.a, y.a, z.a)}; }
-__device__ __forceinline__ F<1> operator*(F<1> x, F<1> y) { return {x.a * y.a}; }
-__device__ __forceinline__ F<1> operator+(F<1> x, F<1> y) { return {x.a + y.a}; }
-__device__ __forceinline__ F<2> fma(F<2> x, F<2> y, F<2> z)
+template <int E> __device__ __forceinline__ F<E> fma(F<E> x, F<E> y, F<E> z)
 {
-    F<2> r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.q) : "l"(x.q), "l"(y.q), "l"(z.q));
+    F<E> r;
+#pragma unroll
+    for (int e = 0; e < E; ++e) r.v[e] = fmaf(x.v[e], y.v[e], z.v[e]);
     return r;
 }
-__device__ __forceinline__ F<2> operator*(F<2> x, F<2> y)
+template <int E> __device__ __forceinline__ F<E> operator*(F<E> x, F<E> y)
 {
-    F<2> r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.q) : "l"(x.q), "l"(y.q));
+    F<E> r;
+#pragma unroll
+    for (int e = 0; e < E; ++e) r.v[e] = x.v[e] * y.v[e];
     return r;
 }
-__device__ __forceinline__ F<2> operator+(F<2> x, F<2> y)
+template <int E> __device__ __forceinline__ F<E> operator+(F<E> x, F<E> y)
 {
-    F<2> r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.q) : "l"(x.q), "l"(y.q));
+    F<E> r;
+#pragma unroll
+    for (int e = 0; e < E; ++e) r.v[e] = x.v[e] + y.v[e];
     return r;
 }
 // f of each channel
@@ -172,11 +174,10 @@ template <int E> __device__ __forceinline__ F<E> rcp_of(F<E> x)
     return each(x, [](float t) { return rcp(t); });
 }
 
-// 1 - e^-y for 0 <= y <= 1/2: y sum_{k=0..7} (-y)^k / (k+1)!; the next term is below 2^-26 of it
+// 1 - e^-y for 0 <= y <= 1/4: y sum_{k=0..6} (-y)^k / (k+1)!; the next term is below 2^-29 of it
 template <int E> __device__ __forceinline__ F<E> rest_series(F<E> y)
 {
-    F<E> s = fma(y, F<E>::all(-1.0f / 40320.0f), F<E>::all(1.0f / 5040.0f));
-    s = fma(s, y, F<E>::all(-1.0f / 720.0f));
+    F<E> s = fma(y, F<E>::all(1.0f / 5040.0f), F<E>::all(-1.0f / 720.0f));
     s = fma(s, y, F<E>::all(1.0f / 120.0f));
     s = fma(s, y, F<E>::all(-1.0f / 24.0f));
     s = fma(s, y, F<E>::all(1.0f / 6.0f));
@@ -194,7 +195,7 @@ template <int E> __device__ __forceinline__ F<E> pick_small(F<E> y, F<E> small, 
     small.get(p);
     large.get(q);
 #pragma unroll
-    for (int e = 0; e < E; ++e) p[e] = t[e] < 0.5f ? p[e] : q[e];
+    for (int e = 0; e < E; ++e) p[e] = t[e] < 0.25f ? p[e] : q[e];
     return F<E>::of(p);
 }
 // A step's a = e^-y and 1 - a^2 (a NaN passes).
@@ -206,23 +207,23 @@ template <int E> __device__ __forceinline__ void decay_of(F<E> y, F<E>& av, F<E>
     m2 = rest * fma(rest, neg, F<E>::all(2.0f));
 }
 
-// Factor of many steps, whose y sum up to this (inf: a reset was among them).
-template <int E> __device__ __forceinline__ F<E> factor_of(F<E> y)
+// The map h -> A h + B of many steps as h -> (k h + (p h + B)): k = 1, p = A - 1 for A above 3/4, else k = 0, p = A;
+// k = kCut: what h holds is cut off even if it is not finite (a reset was among the steps; y is inf).
+template <int E> struct Map {
+    F<E> p, k, b;
+};
+template <int E> __device__ __forceinline__ Map<E> map_of(F<E> y, F<E> B)
 {
-    const F<E> big = each(exp_neg(y), [](float t) { return t < kTiny ? kTiny : t; });
-    const F<E> v = pick_small(y, rest_series(y) * F<E>::all(-1.0f), big);
-    return each(y, v, [](float l, float t) { return l == INFINITY ? kHard : t; });
+    Map<E> m;
+    m.p = pick_small(y, rest_series(y) * F<E>::all(-1.0f), exp_neg(y));
+    m.k = each(y, [](float t) { return t < 0.25f ? 1.0f : t == INFINITY ? kCut : 0.0f; });
+    m.b = B;
+    return m;
 }
-// A h + B
-template <int E> __device__ __forceinline__ F<E> apply(F<E> v, F<E> B, F<E> h)
+template <bool CUTS, int E> __device__ __forceinline__ F<E> apply(const Map<E>& m, F<E> h)
 {
-    float t[E], b[E], r[E];
-    (fma(v, h, B) + each(v, h, [](float u, float x) { return u > 0.0f ? 0.0f : x; })).get(r);
-    v.get(t);
-    B.get(b);
-#pragma unroll
-    for (int e = 0; e < E; ++e) r[e] = t[e] == kHard ? b[e] : r[e];
-    return F<E>::of(r);
+    if (CUTS) h = each(m.k, h, [](float k, float x) { return k == kCut ? 0.0f : x; });
+    return fma(m.k, h, fma(m.p, h, m.b));
 }
 
 __device__ __forceinline__ float softplus_of(float d) { return fmaxf(d, 0.0f) + log1pf(expf(-fabsf(d))); }
@@ -237,98 +238,112 @@ __device__ __forceinline__ void cluster_sync_all()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void st_cluster(const void* local, uint32_t rank, float2 v)
+__device__ __forceinline__ uint32_t peer_addr(uint32_t local, uint32_t rank)
 {
-    uint32_t a = (uint32_t)__cvta_generic_to_shared(local), d;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(rank));
-    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(d), "f"(v.x), "f"(v.y) : "memory");
+    uint32_t d;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(local), "r"(rank));
+    return d;
+}
+// 16 / 8 bytes to another block's shared memory; its mbarrier counts them as they arrive.
+__device__ __forceinline__ void st_async(uint32_t to, uint32_t bar, float a, float b, float c, float d)
+{
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%2, %3, %4, %5}, [%1];" ::"r"(to),
+                 "r"(bar), "f"(a), "f"(b), "f"(c), "f"(d)
+                 : "memory");
+}
+__device__ __forceinline__ void st_async(uint32_t to, uint32_t bar, float a, float b)
+{
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%2, %3}, [%1];" ::"r"(to),
+                 "r"(bar), "f"(a), "f"(b)
+                 : "memory");
 }
 
-// Shared memory of the exchange: maps (factor, offset) and sums of y of the block's warps, maps of the cluster's blocks
-// (two sets, written by turns).
-template <int E, int W, int CL> struct Meet {
-    float2 agg[W][E][32];
-    float len[W][E][32];
-    float2 tot[2][CL][E][32];
-};
+constexpr int E = 2;              // channels per thread
 
-// Exchange of one span of the cluster: every thread gives its map (y, B); it gets the state that enters its steps, and
-// `run` moves past the whole span.  Position 0 comes first in the direction of the scan.
-template <int E, int W, int CL>
-__device__ __forceinline__ F<E> exchange(Meet<E, W, CL>& s, int parity, int wpos, int cpos, F<E> L, F<E> B, F<E>& run)
+// Shared memory of the exchange, two sets used by turns: maps of the block's warps and their sums of y, maps of the
+// cluster's blocks with the mbarrier that counts them.
+template <int W, int CL> struct Meet {
+    float4 pk[2][W][32];
+    float2 b[2][W][32], len[2][W][32];
+    float4 tot_pk[2][CL][32];
+    float2 tot_b[2][CL][32];
+    uint64_t full[2];
+};
+constexpr uint32_t kMapBytes = 32 * (sizeof(float4) + sizeof(float2));
+
+template <int W, int CL> __device__ __forceinline__ void meet_init(Meet<W, CL>& s)
 {
-    const int lane = threadIdx.x & 31;
-    const F<E> v = factor_of(L);
-    F<E> in = run;
-    if constexpr (W * CL == 1) {
-        run = apply(v, B, run);
-        return in;
-    }
-    auto put = [&](float2 (*to)[32], F<E> x, F<E> y) {
-        float p[E], q[E];
-        x.get(p);
-        y.get(q);
-#pragma unroll
-        for (int e = 0; e < E; ++e) to[e][lane] = make_float2(p[e], q[e]);
-    };
-    auto step = [&](const float2 (*from)[32], F<E> h) {
-        float p[E], q[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const float2 t = from[e][lane];
-            p[e] = t.x;
-            q[e] = t.y;
+    if constexpr (CL > 1) {
+        if (threadIdx.x == 0) {
+            mbar_init(smem_addr(&s.full[0]), 1);
+            mbar_init(smem_addr(&s.full[1]), 1);
+            fence_barrier_init();
         }
-        return apply(F<E>::of(p), F<E>::of(q), h);
-    };
-    put(s.agg[wpos], v, B);
-    if constexpr (CL > 1) {
-        float l[E];
-        L.get(l);
-#pragma unroll
-        for (int e = 0; e < E; ++e) s.len[wpos][e][lane] = l[e];
+        cluster_sync_all();                              // every block of the cluster runs, its barriers are set up
     }
-    __syncthreads();
-    if constexpr (CL > 1) {
-        if (wpos == 0) {
-            F<E> bt = F<E>::all(0.0f);
-            float lt[E] = {};
+}
+
+// Exchange of span n of the cluster: every thread gives its map (y, B); it gets the state that enters its steps, and
+// `run` moves past the whole span.  Position 0 comes first in the direction of the scan.  One block barrier a span: a
+// set is written again only two spans later, when all warps have passed the barrier in between, and a block's maps
+// for that span are sent only after it has the whole cluster's of the span in between.  A wait that gives up is
+// recorded; the walk goes on (its results are void) and ends.
+template <int W, int CL, bool CUTS>
+__device__ __forceinline__ F<E> exchange(Meet<W, CL>& s, int n, int wpos, int cpos, F<E> y, F<E> B, F<E>& run,
+                                         unsigned int* status, bool& waits)
+{
+    const int lane = threadIdx.x & 31, set = n & 1;
+    const Map<E> m = map_of(y, B);
+    if constexpr (W * CL == 1) {
+        const F<E> in = run;
+        run = apply<CUTS>(m, run);
+        return in;
+    } else {
+        auto get = [&](const float4& q, const float2& b) {
+            Map<E> t;
+            t.p.v[0] = q.x, t.p.v[1] = q.y, t.k.v[0] = q.z, t.k.v[1] = q.w;
+            t.b.v[0] = b.x, t.b.v[1] = b.y;
+            return t;
+        };
+        s.pk[set][wpos][lane] = make_float4(m.p.v[0], m.p.v[1], m.k.v[0], m.k.v[1]);
+        s.b[set][wpos][lane] = make_float2(B.v[0], B.v[1]);
+        if constexpr (CL > 1) s.len[set][wpos][lane] = make_float2(y.v[0], y.v[1]);
+        __syncthreads();
+        F<E> in;
+        if constexpr (CL > 1) {
+            if (wpos == 0) {
+                F<E> bt = F<E>::all(0.0f), yt = F<E>::all(0.0f);
 #pragma unroll
-            for (int w = 0; w < W; ++w) {
-                bt = step(s.agg[w], bt);
+                for (int w = 0; w < W; ++w) {
+                    bt = apply<CUTS>(get(s.pk[set][w][lane], s.b[set][w][lane]), bt);
+                    const float2 l = s.len[set][w][lane];
+                    // a reset cuts off a NaN before it
+                    yt.v[0] = CUTS && l.x == INFINITY ? l.x : yt.v[0] + l.x;
+                    yt.v[1] = CUTS && l.y == INFINITY ? l.y : yt.v[1] + l.y;
+                }
+                const Map<E> t = map_of(yt, bt);
+                const uint32_t bar = smem_addr(&s.full[set]), pk = smem_addr(&s.tot_pk[set][cpos][lane]),
+                               bb = smem_addr(&s.tot_b[set][cpos][lane]);
+                if (lane == 0) mbar_arrive_expect_tx(bar, CL * kMapBytes);
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const float l = s.len[w][e][lane];
-                    lt[e] = l == INFINITY ? l : lt[e] + l;           // a reset cuts off a NaN before it
+                for (int c = 0; c < CL; ++c) {
+                    const uint32_t pb = peer_addr(bar, c);
+                    st_async(peer_addr(pk, c), pb, t.p.v[0], t.p.v[1], t.k.v[0], t.k.v[1]);
+                    st_async(peer_addr(bb, c), pb, t.b.v[0], t.b.v[1]);
                 }
             }
-            float p[E], q[E];
-            factor_of(F<E>::of(lt)).get(p);
-            bt.get(q);
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-#pragma unroll
-                for (int c = 0; c < CL; ++c) st_cluster(&s.tot[parity][cpos][e][lane], c, make_float2(p[e], q[e]));
+            if (waits) waits = mbar_wait(smem_addr(&s.full[set]), (n >> 1) & 1, status);
+            for (int c = 0; c < cpos; ++c) run = apply<CUTS>(get(s.tot_pk[set][c][lane], s.tot_b[set][c][lane]), run);
+            in = run;
+            for (int c = cpos; c < CL; ++c) run = apply<CUTS>(get(s.tot_pk[set][c][lane], s.tot_b[set][c][lane]), run);
+            for (int w = 0; w < wpos; ++w) in = apply<CUTS>(get(s.pk[set][w][lane], s.b[set][w][lane]), in);
+        } else {
+            for (int w = 0; w < wpos; ++w) run = apply<CUTS>(get(s.pk[set][w][lane], s.b[set][w][lane]), run);
+            in = run;
+            for (int w = wpos; w < W; ++w) run = apply<CUTS>(get(s.pk[set][w][lane], s.b[set][w][lane]), run);
         }
-        cluster_sync_all();
-#pragma unroll
-        for (int c = 0; c < CL; ++c) {
-            if (c == cpos) in = run;
-            run = step(s.tot[parity][c], run);
-        }
-        for (int w = 0; w < wpos; ++w) in = step(s.agg[w], in);
-        // the next span's maps are written after the next pass of the barrier above at the earliest by this block's
-        // warps that have read these: one more block barrier
-        __syncthreads();
-    } else {
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-            if (w == wpos) in = run;
-            run = step(s.agg[w], run);
-        }
-        __syncthreads();
+        return in;
     }
-    return in;
 }
 
 // The inputs of a thread's S steps of E neighbouring channels, as they lie in memory: one vector a step, or (LV = 1)
@@ -400,8 +415,6 @@ template <int S> __device__ __forceinline__ uint32_t cuts_of(const unsigned char
     return cut;
 }
 
-constexpr int E = 2;              // channels per thread: their arithmetic goes through the packed f32x2 instructions
-
 // Where a thread stands: its block's unit is (sequence b, strip of channels).
 struct Place {
     int warp, rank, chans;           // chans: channels of this thread that exist (0..E)
@@ -421,7 +434,7 @@ struct Place {
 template <typename T, int LV, int S, int W, int CL>
 __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_forward_kernel(const GlrArgs a)
 {
-    __shared__ Meet<E, W, CL> meet;
+    __shared__ Meet<W, CL> meet;
     const Place at(a, CL);
     constexpr int64_t SPAN = (int64_t)S * W * CL;
     const int64_t first = ((int64_t)at.rank * W + at.warp) * S;      // this thread's first step within a span
@@ -447,10 +460,11 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_forward_kernel(con
         cut = cuts_of<S>(Z + t, Z ? live : 0);
     };
     fetch(first);
-    if constexpr (CL > 1) cluster_sync_all();            // every block of the cluster runs before its memory is written
+    meet_init(meet);
+    bool waits = true;
 
-    int parity = 0;
-    for (int64_t base = 0; base < a.T; base += SPAN, parity ^= 1) {
+    int n = 0;
+    for (int64_t base = 0; base < a.T; base += SPAN, ++n) {
         const int64_t t = base + first;
         const int live = (int)min((int64_t)S, max((int64_t)0, a.T - t));
         const uint32_t cuts = cut;
@@ -481,7 +495,8 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_forward_kernel(con
             }
             if (after) len = F<E>::all(INFINITY);
         }
-        F<E> h = exchange<E, W, CL>(meet, parity, at.warp, at.rank, len, B, run);
+        F<E> h = Z ? exchange<W, CL, true>(meet, n, at.warp, at.rank, len, B, run, a.status, waits)
+                   : exchange<W, CL, false>(meet, n, at.warp, at.rank, len, B, run, a.status, waits);
         if (K && live > 0) store_f32<E>(K + (t / kSteps) * a.C, h, chans);
         T* y = Y + t * a.C;
 #pragma unroll
@@ -500,7 +515,7 @@ template <typename T, int LV, int W, int CL>
 __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_backward_kernel(const GlrArgs a)
 {
     constexpr int S = kSteps;                            // a thread's steps begin at a kept state
-    __shared__ Meet<E, W, CL> meet;
+    __shared__ Meet<W, CL> meet;
     const Place at(a, CL);
     constexpr int64_t SPAN = (int64_t)S * W * CL;
     const int64_t first = ((int64_t)at.rank * W + at.warp) * S;
@@ -519,10 +534,11 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_backward_kernel(co
     double acc[E];                                       // sum of dL L
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.0;
-    if constexpr (CL > 1) cluster_sync_all();
+    meet_init(meet);
+    bool waits = true;
 
-    int parity = 0;
-    for (int64_t base = (a.T - 1) / SPAN * SPAN; base >= 0; base -= SPAN, parity ^= 1) {
+    int n = 0;
+    for (int64_t base = (a.T - 1) / SPAN * SPAN; base >= 0; base -= SPAN, ++n) {
         const int64_t t = base + first;
         const int live = (int)min((int64_t)S, max((int64_t)0, a.T - t));
         Steps<T, E, LV, S> qx, qr, qg, qd;
@@ -561,7 +577,8 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_backward_kernel(co
             if (cut >> i & 1) B = zero;
         }
         if (cut) len = F<E>::all(INFINITY);
-        F<E> flow = exchange<E, W, CL>(meet, parity, W - 1 - at.warp, CL - 1 - at.rank, len, B, run);
+        F<E> flow = Z ? exchange<W, CL, true>(meet, n, W - 1 - at.warp, CL - 1 - at.rank, len, B, run, a.status, waits)
+                      : exchange<W, CL, false>(meet, n, W - 1 - at.warp, CL - 1 - at.rank, len, B, run, a.status, waits);
         F<E> part = zero;
         int64_t o = dense + (t + S - 1) * a.C;
 #pragma unroll
@@ -742,6 +759,7 @@ void common_args(const kan_glr_shape& s, GlrArgs& a)
     a.gb = s.g_stride_b, a.gt = s.g_stride_t;
     a.B = s.batch, a.T = s.time, a.C = s.channels;
     a.strips = (int)((s.channels + 32 * E - 1) / (32 * E));
+    a.status = device_status_ptr();
 }
 
 bool misaligned(const kan_glr_shape& s, std::initializer_list<const void*> ops, std::initializer_list<const void*> f32)
