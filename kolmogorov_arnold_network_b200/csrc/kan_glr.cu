@@ -164,10 +164,18 @@ template <int E, typename Fn> __device__ __forceinline__ F<E> each(F<E> x, F<E> 
     return F<E>::of(v);
 }
 
-// e^-x, held at 2^TOP from above, so that what is made of it stays finite (a NaN passes).
+// e^-x; with TOP, held at 2^TOP from above, so that what is made of it stays finite (a NaN passes).
 template <int TOP, int E> __device__ __forceinline__ F<E> exp_minus(F<E> x)
 {
     return each(x * F<E>::all(-kLog2e), [](float t) { return ex2(min_nan(t, (float)TOP)); });
+}
+template <int E> __device__ __forceinline__ F<E> exp_minus(F<E> x)
+{
+    return each(x * F<E>::all(-kLog2e), [](float t) { return ex2(t); });
+}
+template <int E> __device__ __forceinline__ F<E> rsq_of(F<E> x)
+{
+    return each(x, [](float t) { return rsq(t); });
 }
 template <int E> __device__ __forceinline__ F<E> rcp_of(F<E> x)
 {
@@ -198,13 +206,21 @@ template <int E> __device__ __forceinline__ F<E> pick_small(F<E> y, F<E> small, 
     for (int e = 0; e < E; ++e) p[e] = t[e] < 0.25f ? p[e] : q[e];
     return F<E>::of(p);
 }
-// A step's a = e^-y and 1 - a^2 (a NaN passes).
-template <int E> __device__ __forceinline__ void decay_of(F<E> y, F<E>& av, F<E>& m2)
+// 1 - a of a step with a = e^-y (a NaN passes), and a itself to its own last bit where it is small.
+template <int E> __device__ __forceinline__ F<E> rest_of(F<E> y)
+{
+    return pick_small(y, rest_series(y), fma(exp_neg(y), F<E>::all(-1.0f), F<E>::all(1.0f)));
+}
+template <int E> __device__ __forceinline__ void decay_of(F<E> y, F<E>& av, F<E>& rest)
 {
     const F<E> r = rest_series(y), big = exp_neg(y), one = F<E>::all(1.0f), neg = F<E>::all(-1.0f);
-    const F<E> rest = pick_small(y, r, fma(big, neg, one));
+    rest = pick_small(y, r, fma(big, neg, one));
     av = pick_small(y, fma(r, neg, one), big);
-    m2 = rest * fma(rest, neg, F<E>::all(2.0f));
+}
+// 1 - a^2
+template <int E> __device__ __forceinline__ F<E> square_rest(F<E> rest)
+{
+    return rest * fma(rest, F<E>::all(-1.0f), F<E>::all(2.0f));
 }
 
 // The map h -> A h + B of many steps as h -> (k h + (p h + B)): k = 1, p = A - 1 for A above 3/4, else k = 0, p = A;
@@ -347,19 +363,20 @@ __device__ __forceinline__ F<E> exchange(Meet<W, CL>& s, int n, int wpos, int cp
 }
 
 // The inputs of a thread's S steps of E neighbouring channels, as they lie in memory: one vector a step, or (LV = 1)
-// one element at a time where rows are not whole vectors.
+// one element at a time where rows are not whole vectors.  `p` points at channels that exist: a thread beyond the last
+// channel reads others' (and stores nothing), `second` is where its second channel lies.
 template <typename T, int E, int LV, int S> struct Steps {
     Pack<T, LV> q[S][E / LV];
-    __device__ __forceinline__ void load(const T* p, int64_t stride, int live, int chans)
+    template <bool FULL> __device__ __forceinline__ void load(const T* p, uint32_t stride, int live, int second)
     {
 #pragma unroll
         for (int i = 0; i < S; ++i) {
-#pragma unroll
-            for (int j = 0; j < E / LV; ++j) {
-                q[i][j] = Pack<T, LV>::zero();
-                if (i < live && j * LV < chans) q[i][j] = Pack<T, LV>::load(p + j * LV);
+            const T* at = p + (size_t)(i * stride);
+            if (!FULL) q[i][0] = q[i][E / LV - 1] = Pack<T, LV>::zero();
+            if (FULL || i < live) {
+                q[i][0] = Pack<T, LV>::load(at);
+                if (LV < E) q[i][E / LV - 1] = Pack<T, LV>::load(at + second);
             }
-            p += stride;
         }
     }
     __device__ __forceinline__ F<E> get(int i) const
@@ -404,21 +421,18 @@ template <int E> __device__ __forceinline__ void store_f32(float* p, F<E> x, int
     for (int e = 0; e < E; ++e)
         if (e < chans) p[e] = v[e];
 }
-template <int S> __device__ __forceinline__ uint32_t cuts_of(const unsigned char* z, int live)
+// Bits of the steps whose reset is set; the whole warp asks for the same steps.
+__device__ __forceinline__ uint32_t cuts_of(const unsigned char* z, int live)
 {
-    uint32_t cut = 0;
-    if (z) {
-#pragma unroll
-        for (int i = 0; i < S; ++i)
-            if (i < live && z[i]) cut |= 1u << i;
-    }
-    return cut;
+    const int lane = threadIdx.x & 31;
+    return z ? __ballot_sync(0xffffffffu, lane < live && z[lane] != 0) : 0;
 }
 
 // Where a thread stands: its block's unit is (sequence b, strip of channels).
 struct Place {
     int warp, rank, chans;           // chans: channels of this thread that exist (0..E)
-    int64_t b, c;
+    int second;                      // where the second one is read from (a channel that exists)
+    int64_t b, c, read;              // read: the channel that is read (c, or 0 beyond the last)
     __device__ __forceinline__ Place(const GlrArgs& a, int cl)
     {
         warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
@@ -427,6 +441,8 @@ struct Place {
         b = unit / a.strips;
         c = (unit - b * a.strips) * (32 * E) + (threadIdx.x & 31) * E;
         chans = (int)max((int64_t)0, min((int64_t)E, a.C - c));
+        read = chans > 0 ? c : 0;
+        second = chans > 1 ? 1 : 0;
     }
 };
 
@@ -440,24 +456,30 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_forward_kernel(con
     const int64_t first = ((int64_t)at.rank * W + at.warp) * S;      // this thread's first step within a span
     const int chans = at.chans;
     const int64_t state = at.b * a.C + at.c;
-    const T* X = reinterpret_cast<const T*>(a.x) + at.b * a.xb + at.c;
-    const T* R = reinterpret_cast<const T*>(a.r) + at.b * a.rb + at.c;
-    const T* G = reinterpret_cast<const T*>(a.g) + at.b * a.gb + at.c;
+    const T* X = reinterpret_cast<const T*>(a.x) + at.b * a.xb + at.read;
+    const T* R = reinterpret_cast<const T*>(a.r) + at.b * a.rb + at.read;
+    const T* G = reinterpret_cast<const T*>(a.g) + at.b * a.gb + at.read;
     T* Y = reinterpret_cast<T*>(a.y) + at.b * a.T * a.C + at.c;
     const unsigned char* Z = a.reset ? a.reset + at.b * a.T : nullptr;
     float* K = a.kept ? a.kept + at.b * ((a.T + kSteps - 1) / kSteps) * a.C + at.c : nullptr;
 
     const F<E> lambda = each(load_f32<E>(a.decay + at.c, chans), [](float d) { return softplus_of(d); });
-    const F<E> one = F<E>::all(1.0f), zero = F<E>::all(0.0f);
+    const F<E> one = F<E>::all(1.0f), zero = F<E>::all(0.0f), neg = F<E>::all(-1.0f);
     F<E> run = a.h0 ? load_f32<E>(a.h0 + state, chans) : zero;
     Steps<T, E, LV, S> qx, qr, qg;
     uint32_t cut;
     auto fetch = [&](int64_t t) {
-        const int live = (int)min((int64_t)S, a.T - t);              // may be negative
-        qr.load(R + t * a.rt, a.rt, live, chans);
-        qg.load(G + t * a.gt, a.gt, live, chans);
-        qx.load(X + t * a.xt, a.xt, live, chans);
-        cut = cuts_of<S>(Z + t, Z ? live : 0);
+        const int live = (int)min((int64_t)S, max((int64_t)0, a.T - t));
+        if (live == S) {
+            qr.template load<true>(R + t * a.rt, (uint32_t)a.rt, S, at.second);
+            qg.template load<true>(G + t * a.gt, (uint32_t)a.gt, S, at.second);
+            qx.template load<true>(X + t * a.xt, (uint32_t)a.xt, S, at.second);
+        } else {
+            qr.template load<false>(R + t * a.rt, (uint32_t)a.rt, live, at.second);
+            qg.template load<false>(G + t * a.gt, (uint32_t)a.gt, live, at.second);
+            qx.template load<false>(X + t * a.xt, (uint32_t)a.xt, live, at.second);
+        }
+        cut = cuts_of(Z + t, Z ? live : 0);
     };
     fetch(first);
     meet_init(meet);
@@ -471,40 +493,53 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_forward_kernel(con
         F<E> fa[S], bb[S], len = zero, B = zero;
 #pragma unroll
         for (int i = 0; i < S; ++i) {
-            const F<E> s = rcp_of(one + exp_minus<115>(qr.get(i)));
-            const F<E> y = s * (i < live ? lambda : zero);           // past the end: a = 1
-            F<E> m2;
-            decay_of(y, fa[i], m2);
-            // m sigmoid(g) = m^2 / sqrt(m^2 (1 + e)^2) with e = exp(-g): one rsqrt
+            const F<E> y = rcp_of(one + exp_minus(qr.get(i))) * lambda;
+            const F<E> rest = rest_of(y), m2 = square_rest(rest);
+            // m sigmoid(g) = m^2 / sqrt(m^2 (1 + e)^2) with e = exp(-g): one rsqrt, held where m is 0
             const F<E> q = one + exp_minus<60>(qg.get(i));
-            bb[i] = m2 * each(m2 * q * q, [](float u) { return rsq(max_nan(u, kTiny)); }) * qx.get(i);
+            bb[i] = m2 * rsq_of(fma(m2 * q, q, F<E>::all(kTiny))) * qx.get(i);
+            fa[i] = one + rest * neg;
             len = len + y;
             B = fma(fa[i], B, bb[i]);
+        }
+        if (live < S) {                                  // past the end: a = 1, nothing comes in
+            len = B = zero;
+#pragma unroll
+            for (int i = 0; i < S; ++i) {
+                if (i < live) {
+                    const F<E> y = rcp_of(one + exp_minus(qr.get(i))) * lambda;
+                    len = len + y;
+                    B = fma(fa[i], B, bb[i]);
+                }
+            }
         }
         if (base + SPAN < a.T) fetch(t + SPAN);
         if (cuts) {                                      // resets among the steps: they cut off what comes before them
             B = zero;
-            bool after = false;
+            len = F<E>::all(INFINITY);
 #pragma unroll
             for (int i = 0; i < S; ++i) {
-                if (cuts >> i & 1) {
-                    B = zero;
-                    after = true;
-                }
-                B = fma(fa[i], B, bb[i]);
+                if (cuts >> i & 1) B = zero;
+                if (i < live) B = fma(fa[i], B, bb[i]);
             }
-            if (after) len = F<E>::all(INFINITY);
         }
         F<E> h = Z ? exchange<W, CL, true>(meet, n, at.warp, at.rank, len, B, run, a.status, waits)
                    : exchange<W, CL, false>(meet, n, at.warp, at.rank, len, B, run, a.status, waits);
         if (K && live > 0) store_f32<E>(K + (t / kSteps) * a.C, h, chans);
         T* y = Y + t * a.C;
+        if (live == S && !cuts) {
 #pragma unroll
-        for (int i = 0; i < S; ++i) {
-            if (cuts >> i & 1) h = zero;
-            h = fma(fa[i], h, bb[i]);
-            if (i < live) store_step<T, LV, E>(y, h, chans);
-            y += a.C;
+            for (int i = 0; i < S; ++i) {
+                h = fma(fa[i], h, bb[i]);
+                store_step<T, LV, E>(y + (size_t)(i * (uint32_t)a.C), h, chans);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < S; ++i) {
+                if (cuts >> i & 1) h = zero;
+                h = fma(fa[i], h, bb[i]);
+                if (i < live) store_step<T, LV, E>(y + (size_t)(i * (uint32_t)a.C), h, chans);
+            }
         }
     }
     if (a.h_last && at.rank == 0 && at.warp == 0) store_f32<E>(a.h_last + state, run, chans);
@@ -521,10 +556,10 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_backward_kernel(co
     const int64_t first = ((int64_t)at.rank * W + at.warp) * S;
     const int chans = at.chans;
     const int64_t state = at.b * a.C + at.c, dense = at.b * a.T * a.C + at.c;
-    const T* X = reinterpret_cast<const T*>(a.x) + at.b * a.xb + at.c;
-    const T* R = reinterpret_cast<const T*>(a.r) + at.b * a.rb + at.c;
-    const T* G = reinterpret_cast<const T*>(a.g) + at.b * a.gb + at.c;
-    const T* D = reinterpret_cast<const T*>(a.dy) + dense;
+    const T* X = reinterpret_cast<const T*>(a.x) + at.b * a.xb + at.read;
+    const T* R = reinterpret_cast<const T*>(a.r) + at.b * a.rb + at.read;
+    const T* G = reinterpret_cast<const T*>(a.g) + at.b * a.gb + at.read;
+    const T* D = reinterpret_cast<const T*>(a.dy) + at.b * a.T * a.C + at.read;
     const unsigned char* Z = a.reset ? a.reset + at.b * a.T : nullptr;
     const float* K = a.kept + at.b * ((a.T + kSteps - 1) / kSteps) * a.C + at.c;
 
@@ -542,11 +577,18 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_backward_kernel(co
         const int64_t t = base + first;
         const int live = (int)min((int64_t)S, max((int64_t)0, a.T - t));
         Steps<T, E, LV, S> qx, qr, qg, qd;
-        qr.load(R + t * a.rt, a.rt, live, chans);
-        qg.load(G + t * a.gt, a.gt, live, chans);
-        qx.load(X + t * a.xt, a.xt, live, chans);
-        qd.load(D + t * a.C, a.C, live, chans);
-        const uint32_t cut = cuts_of<S>(Z + t, Z ? live : 0);
+        if (live == S) {
+            qr.template load<true>(R + t * a.rt, (uint32_t)a.rt, S, at.second);
+            qg.template load<true>(G + t * a.gt, (uint32_t)a.gt, S, at.second);
+            qx.template load<true>(X + t * a.xt, (uint32_t)a.xt, S, at.second);
+            qd.template load<true>(D + t * a.C, (uint32_t)a.C, S, at.second);
+        } else {
+            qr.template load<false>(R + t * a.rt, (uint32_t)a.rt, live, at.second);
+            qg.template load<false>(G + t * a.gt, (uint32_t)a.gt, live, at.second);
+            qx.template load<false>(X + t * a.xt, (uint32_t)a.xt, live, at.second);
+            qd.template load<false>(D + t * a.C, (uint32_t)a.C, live, at.second);
+        }
+        const uint32_t cut = cuts_of(Z + t, Z ? live : 0);
         F<E> h = live > 0 ? load_f32<E>(K + (t / kSteps) * a.C, chans) : zero;
         // per step: the factor, and what d multiplies in each gradient:
         //   dx = d cx,  dg = dx cg,  dL L = d cl,  dr = dL L cr
@@ -555,11 +597,11 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_backward_kernel(co
         for (int i = 0; i < S; ++i) {
             const F<E> er = exp_minus<115>(qr.get(i)), eg = exp_minus<115>(qg.get(i));
             const F<E> s = rcp_of(one + er), sg = rcp_of(one + eg), x = qx.get(i);
-            const F<E> y = s * (i < live ? lambda : zero);
-            F<E> m2;
-            decay_of(y, fa[i], m2);
+            const F<E> y = s * lambda;
+            F<E> rest;
+            decay_of(y, fa[i], rest);
             // 1 / m, held where m is 0 (there y is 0 too, and y / m goes to 0 with it)
-            const F<E> rm = each(m2, [](float u) { return rsq(max_nan(u, kTiny)); });
+            const F<E> m2 = square_rest(rest), rm = rsq_of(m2 + F<E>::all(kTiny));
             if (cut >> i & 1) h = zero;
             cx[i] = m2 * rm * sg;
             cg[i] = x * (eg * sg);
@@ -567,7 +609,8 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_backward_kernel(co
             // a L (h - a u / m), L = -y
             cl[i] = fa[i] * y * fma(fa[i] * rm, sg * x, h * neg);
             h = fma(fa[i], h, cx[i] * x);
-            len = len + y;
+            if (live < S && i >= live) fa[i] = one;      // past the end: gamma passes (dy is 0 there)
+            else len = len + y;
         }
         // the map of these steps, from the last to the first: gamma -> a (gamma + dy)
         F<E> B = zero;
@@ -580,20 +623,20 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_backward_kernel(co
         F<E> flow = Z ? exchange<W, CL, true>(meet, n, W - 1 - at.warp, CL - 1 - at.rank, len, B, run, a.status, waits)
                       : exchange<W, CL, false>(meet, n, W - 1 - at.warp, CL - 1 - at.rank, len, B, run, a.status, waits);
         F<E> part = zero;
-        int64_t o = dense + (t + S - 1) * a.C;
+        const int64_t o = dense + t * a.C;
+        T *ox = reinterpret_cast<T*>(a.dx) + o, *orr = reinterpret_cast<T*>(a.dr) + o, *og = reinterpret_cast<T*>(a.dg) + o;
 #pragma unroll
         for (int i = S - 1; i >= 0; --i) {
-            const F<E> d = flow + qd.get(i);
-            const F<E> ox = d * cx[i], ol = d * cl[i];
+            const F<E> d = flow + qd.get(i), gx = d * cx[i], gl = d * cl[i];
             flow = fa[i] * d;
             if (cut >> i & 1) flow = zero;
             if (i < live) {
-                part = part + ol;
-                if (a.dx) store_step<T, LV, E>(reinterpret_cast<T*>(a.dx) + o, ox, chans);
-                if (a.dr) store_step<T, LV, E>(reinterpret_cast<T*>(a.dr) + o, ol * cr[i], chans);
-                if (a.dg) store_step<T, LV, E>(reinterpret_cast<T*>(a.dg) + o, ox * cg[i], chans);
+                const size_t step = (size_t)(i * (uint32_t)a.C);
+                part = part + gl;
+                if (a.dx) store_step<T, LV, E>(ox + step, gx, chans);
+                if (a.dr) store_step<T, LV, E>(orr + step, gl * cr[i], chans);
+                if (a.dg) store_step<T, LV, E>(og + step, gx * cg[i], chans);
             }
-            o -= a.C;
         }
         float f[E];
         part.get(f);
@@ -642,6 +685,8 @@ kan_status validate(const kan_glr_shape* s)
     const int64_t st[] = {s->x_stride_b, s->x_stride_t, s->r_stride_b, s->r_stride_t, s->g_stride_b, s->g_stride_t};
     for (int64_t v : st)
         if (v < 0) return gl_fail(KAN_ERR_INVALID_ARG, "negative stride");
+    for (int i = 1; i < 6; i += 2)
+        if (st[i] > ((int64_t)1 << 28)) return gl_fail(KAN_ERR_UNSUPPORTED, "a stride of steps above 2^28 elements");
     if (s->channels > ((int64_t)1 << 24) || s->time > ((int64_t)1 << 40) || s->batch > ((int64_t)1 << 31) ||
         s->batch * ((s->channels + 31) / 32) > ((int64_t)1 << 27))
         return gl_fail(KAN_ERR_UNSUPPORTED, "sizes too large");
