@@ -44,6 +44,7 @@ namespace {
 constexpr int kSteps = 8;         // steps per thread, and the spacing of the kept states
 
 constexpr int kMaxCluster = 8;    // blocks of a cluster (the portable bound)
+constexpr int64_t kMaxStride = 1 << 20;   // elements from a step to the next: a span of 512 steps stays within 32 bits of bytes
 
 struct GlrArgs {
     const void *x, *r, *g;
@@ -61,11 +62,10 @@ struct GlrArgs {
     float* dh0;                         // [B, C] or null
     double* part;                       // [B * cluster][C] partial sums for ddecay, or null
     int64_t B, T, C;
-    int strips;                         // ceil(C / 64)
+    int strips;                         // of 128 bytes
     unsigned int* status;
 };
 
-constexpr float kCut = -1.0f;
 constexpr float kTiny = 1e-37f;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -92,12 +92,6 @@ __device__ __forceinline__ float min_nan(float x, float y)
 {
     float r;
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
-    return r;
-}
-__device__ __forceinline__ float max_nan(float x, float y)
-{
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
     return r;
 }
 
@@ -223,22 +217,23 @@ template <int E> __device__ __forceinline__ F<E> square_rest(F<E> rest)
     return rest * fma(rest, F<E>::all(-1.0f), F<E>::all(2.0f));
 }
 
-// The map h -> A h + B of many steps as h -> (k h + (p h + B)): k = 1, p = A - 1 for A above 3/4, else k = 0, p = A;
-// k = kCut: what h holds is cut off even if it is not finite (a reset was among the steps; y is inf).
+// The map h -> A h + B of many steps as h -> (k h + (p h + B)): k = 1, p = A - 1 for A above 3/4, else k = 0, p = A.
+// A reset among the steps (y is inf) gives k = 0, p = -0: B alone for every finite h, and CUTS looks at p for the others.
 template <int E> struct Map {
     F<E> p, k, b;
 };
 template <int E> __device__ __forceinline__ Map<E> map_of(F<E> y, F<E> B)
 {
     Map<E> m;
-    m.p = pick_small(y, rest_series(y) * F<E>::all(-1.0f), exp_neg(y));
-    m.k = each(y, [](float t) { return t < 0.25f ? 1.0f : t == INFINITY ? kCut : 0.0f; });
+    m.p = pick_small(y, fma(rest_series(y), F<E>::all(-1.0f), F<E>::all(0.0f)), exp_neg(y));      // never -0
+    m.p = each(m.p, y, [](float p, float t) { return t == INFINITY ? -0.0f : p; });
+    m.k = each(y, [](float t) { return t < 0.25f ? 1.0f : 0.0f; });
     m.b = B;
     return m;
 }
 template <bool CUTS, int E> __device__ __forceinline__ F<E> apply(const Map<E>& m, F<E> h)
 {
-    if (CUTS) h = each(m.k, h, [](float k, float x) { return k == kCut ? 0.0f : x; });
+    if (CUTS) h = each(m.p, h, [](float p, float x) { return __float_as_uint(p) == 0x80000000u ? 0.0f : x; });
     return fma(m.k, h, fma(m.p, h, m.b));
 }
 
@@ -260,34 +255,53 @@ __device__ __forceinline__ uint32_t peer_addr(uint32_t local, uint32_t rank)
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(local), "r"(rank));
     return d;
 }
-// 16 / 8 bytes to another block's shared memory; its mbarrier counts them as they arrive.
-__device__ __forceinline__ void st_async(uint32_t to, uint32_t bar, float a, float b, float c, float d)
+// 16, 8 or 4 bytes to another block's shared memory; its mbarrier counts them as they arrive.
+__device__ __forceinline__ void st_async(uint32_t to, uint32_t bar, float4 v)
 {
     asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%2, %3, %4, %5}, [%1];" ::"r"(to),
-                 "r"(bar), "f"(a), "f"(b), "f"(c), "f"(d)
+                 "r"(bar), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
                  : "memory");
 }
-__device__ __forceinline__ void st_async(uint32_t to, uint32_t bar, float a, float b)
+__device__ __forceinline__ void st_async(uint32_t to, uint32_t bar, float2 v)
 {
     asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%2, %3}, [%1];" ::"r"(to),
-                 "r"(bar), "f"(a), "f"(b)
+                 "r"(bar), "f"(v.x), "f"(v.y)
+                 : "memory");
+}
+__device__ __forceinline__ void st_async(uint32_t to, uint32_t bar, float v)
+{
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.f32 [%0], %2, [%1];" ::"r"(to), "r"(bar), "f"(v)
                  : "memory");
 }
 
-constexpr int E = 2;              // channels per thread
+template <int E> struct Vecs;
+template <> struct Vecs<1> {
+    using One = float;
+    using Two = float2;
+};
+template <> struct Vecs<2> {
+    using One = float2;
+    using Two = float4;
+};
+__device__ __forceinline__ float one_of(F<1> x) { return x.v[0]; }
+__device__ __forceinline__ float2 one_of(F<2> x) { return make_float2(x.v[0], x.v[1]); }
+__device__ __forceinline__ F<1> of_one(float x) { return {{x}}; }
+__device__ __forceinline__ F<2> of_one(float2 x) { return {{x.x, x.y}}; }
+__device__ __forceinline__ float2 two_of(F<1> x, F<1> y) { return make_float2(x.v[0], y.v[0]); }
+__device__ __forceinline__ float4 two_of(F<2> x, F<2> y) { return make_float4(x.v[0], x.v[1], y.v[0], y.v[1]); }
+__device__ __forceinline__ Map<1> of_two(float2 t, float b) { return {{{t.x}}, {{t.y}}, {{b}}}; }
+__device__ __forceinline__ Map<2> of_two(float4 t, float2 b) { return {{{t.x, t.y}}, {{t.z, t.w}}, {{b.x, b.y}}}; }
 
 // Shared memory of the exchange, two sets used by turns: maps of the block's warps and their sums of y, maps of the
 // cluster's blocks with the mbarrier that counts them.
-template <int W, int CL> struct Meet {
-    float4 pk[2][W][32];
-    float2 b[2][W][32], len[2][W][32];
-    float4 tot_pk[2][CL][32];
-    float2 tot_b[2][CL][32];
+template <int E, int W, int CL> struct Meet {
+    typename Vecs<E>::Two pk[2][W][32], tot_pk[2][CL][32];
+    typename Vecs<E>::One b[2][W][32], len[2][W][32], tot_b[2][CL][32];
     uint64_t full[2];
+    static constexpr uint32_t kMapBytes = 32 * 12 * E;
 };
-constexpr uint32_t kMapBytes = 32 * (sizeof(float4) + sizeof(float2));
 
-template <int W, int CL> __device__ __forceinline__ void meet_init(Meet<W, CL>& s)
+template <int E, int W, int CL> __device__ __forceinline__ void meet_init(Meet<E, W, CL>& s)
 {
     if constexpr (CL > 1) {
         if (threadIdx.x == 0) {
@@ -304,94 +318,185 @@ template <int W, int CL> __device__ __forceinline__ void meet_init(Meet<W, CL>& 
 // set is written again only two spans later, when all warps have passed the barrier in between, and a block's maps
 // for that span are sent only after it has the whole cluster's of the span in between.  A wait that gives up is
 // recorded; the walk goes on (its results are void) and ends.
-template <int W, int CL, bool CUTS>
-__device__ __forceinline__ F<E> exchange(Meet<W, CL>& s, int n, int wpos, int cpos, F<E> y, F<E> B, F<E>& run,
-                                         unsigned int* status, bool& waits)
+template <int E, int W, int CL> struct Walk {
+    Meet<E, W, CL>& s;
+    int set, lane;
+    // the block's warps `from` <= w < `to`
+    template <bool CUTS> __device__ __forceinline__ F<E> warps(int from, int to, F<E> h) const
+    {
+#pragma unroll(CUTS ? 1 : 4)
+        for (int w = from; w < to; ++w) h = apply<CUTS>(of_two(s.pk[set][w][lane], s.b[set][w][lane]), h);
+        return h;
+    }
+    // the cluster's blocks
+    template <bool CUTS> __device__ __forceinline__ F<E> blocks(int from, int to, F<E> h) const
+    {
+#pragma unroll(CUTS ? 1 : 4)
+        for (int c = from; c < to; ++c) h = apply<CUTS>(of_two(s.tot_pk[set][c][lane], s.tot_b[set][c][lane]), h);
+        return h;
+    }
+    template <bool CUTS> __device__ __forceinline__ void states(int wpos, int cpos, F<E>& run, F<E>& in) const
+    {
+        if constexpr (CL > 1) {
+            in = blocks<CUTS>(0, cpos, run);
+            run = blocks<CUTS>(cpos, CL, in);
+            in = warps<CUTS>(0, wpos, in);
+        } else {
+            in = warps<CUTS>(0, wpos, run);
+            run = warps<CUTS>(wpos, W, in);
+        }
+    }
+};
+
+// at_barrier runs right before the block's barrier, past_barrier right after it.
+template <int E, int W, int CL, typename At, typename Past>
+__device__ __forceinline__ F<E> exchange(Meet<E, W, CL>& s, int n, int wpos, int cpos, F<E> y, F<E> B, F<E>& run, bool cuts,
+                                         unsigned int* status, bool& waits, At at_barrier, Past past_barrier)
 {
     const int lane = threadIdx.x & 31, set = n & 1;
     const Map<E> m = map_of(y, B);
+    F<E> in = run;
     if constexpr (W * CL == 1) {
-        const F<E> in = run;
-        run = apply<CUTS>(m, run);
-        return in;
+        run = apply<true>(m, run);
     } else {
-        auto get = [&](const float4& q, const float2& b) {
-            Map<E> t;
-            t.p.v[0] = q.x, t.p.v[1] = q.y, t.k.v[0] = q.z, t.k.v[1] = q.w;
-            t.b.v[0] = b.x, t.b.v[1] = b.y;
-            return t;
-        };
-        s.pk[set][wpos][lane] = make_float4(m.p.v[0], m.p.v[1], m.k.v[0], m.k.v[1]);
-        s.b[set][wpos][lane] = make_float2(B.v[0], B.v[1]);
-        if constexpr (CL > 1) s.len[set][wpos][lane] = make_float2(y.v[0], y.v[1]);
+        const Walk<E, W, CL> walk{s, set, lane};
+        s.pk[set][wpos][lane] = two_of(m.p, m.k);
+        s.b[set][wpos][lane] = one_of(B);
+        if constexpr (CL > 1) s.len[set][wpos][lane] = one_of(y);
+        at_barrier();
         __syncthreads();
-        F<E> in;
         if constexpr (CL > 1) {
             if (wpos == 0) {
-                F<E> bt = F<E>::all(0.0f), yt = F<E>::all(0.0f);
+                F<E> yt = F<E>::all(0.0f);
+                const F<E> bt = cuts ? walk.template warps<true>(0, W, yt) : walk.template warps<false>(0, W, yt);
 #pragma unroll
-                for (int w = 0; w < W; ++w) {
-                    bt = apply<CUTS>(get(s.pk[set][w][lane], s.b[set][w][lane]), bt);
-                    const float2 l = s.len[set][w][lane];
-                    // a reset cuts off a NaN before it
-                    yt.v[0] = CUTS && l.x == INFINITY ? l.x : yt.v[0] + l.x;
-                    yt.v[1] = CUTS && l.y == INFINITY ? l.y : yt.v[1] + l.y;
-                }
+                for (int w = 0; w < W; ++w)              // a reset cuts off a NaN before it
+                    yt = each(yt, of_one(s.len[set][w][lane]), [](float t, float l) { return l == INFINITY ? l : t + l; });
                 const Map<E> t = map_of(yt, bt);
                 const uint32_t bar = smem_addr(&s.full[set]), pk = smem_addr(&s.tot_pk[set][cpos][lane]),
                                bb = smem_addr(&s.tot_b[set][cpos][lane]);
-                if (lane == 0) mbar_arrive_expect_tx(bar, CL * kMapBytes);
+                if (lane == 0) mbar_arrive_expect_tx(bar, CL * s.kMapBytes);
 #pragma unroll
                 for (int c = 0; c < CL; ++c) {
                     const uint32_t pb = peer_addr(bar, c);
-                    st_async(peer_addr(pk, c), pb, t.p.v[0], t.p.v[1], t.k.v[0], t.k.v[1]);
-                    st_async(peer_addr(bb, c), pb, t.b.v[0], t.b.v[1]);
+                    st_async(peer_addr(pk, c), pb, two_of(t.p, t.k));
+                    st_async(peer_addr(bb, c), pb, one_of(t.b));
                 }
             }
-            if (waits) waits = mbar_wait(smem_addr(&s.full[set]), (n >> 1) & 1, status);
-            for (int c = 0; c < cpos; ++c) run = apply<CUTS>(get(s.tot_pk[set][c][lane], s.tot_b[set][c][lane]), run);
-            in = run;
-            for (int c = cpos; c < CL; ++c) run = apply<CUTS>(get(s.tot_pk[set][c][lane], s.tot_b[set][c][lane]), run);
-            for (int w = 0; w < wpos; ++w) in = apply<CUTS>(get(s.pk[set][w][lane], s.b[set][w][lane]), in);
-        } else {
-            for (int w = 0; w < wpos; ++w) run = apply<CUTS>(get(s.pk[set][w][lane], s.b[set][w][lane]), run);
-            in = run;
-            for (int w = wpos; w < W; ++w) run = apply<CUTS>(get(s.pk[set][w][lane], s.b[set][w][lane]), run);
         }
-        return in;
+        past_barrier();
+        if constexpr (CL > 1) {
+            if (waits) waits = mbar_wait(smem_addr(&s.full[set]), (n >> 1) & 1, status);
+        }
+        const F<E> first = run;
+        walk.template states<false>(wpos, cpos, run, in);
+        if (cuts) {
+            // A cut map is B + 0 h: right unless h is not finite.  Then (what comes out is a NaN) once more with care.
+            float t = 0.0f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) t += run.v[e] + in.v[e];
+            if (__any_sync(0xffffffffu, t != t)) {
+                run = first;
+                walk.template states<true>(wpos, cpos, run, in);
+            }
+        }
     }
+    return in;
 }
 
-// The inputs of a thread's S steps of E neighbouring channels, as they lie in memory: one vector a step, or (LV = 1)
-// one element at a time where rows are not whole vectors.  `p` points at channels that exist: a thread beyond the last
-// channel reads others' (and stores nothing), `second` is where its second channel lies.
-template <typename T, int E, int LV, int S> struct Steps {
-    Pack<T, LV> q[S][E / LV];
-    template <bool FULL> __device__ __forceinline__ void load(const T* p, uint32_t stride, int live, int second)
+// Where a thread stands: its block's unit is (sequence b, strip of channels).
+template <int E> struct Place {
+    int warp, rank, chans;           // chans: channels of this thread that exist (0..E)
+    int second;                      // where the second one is read from (a channel that exists)
+    int64_t b, c, c0, read;          // c0: the strip's first channel; read: the channel that is read (c, or 0 beyond the last)
+    __device__ __forceinline__ Place(const GlrArgs& a, int cl)
+    {
+        warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
+        rank = cl > 1 ? (int)cluster_rank() : 0;
+        const int unit = blockIdx.x / cl;
+        b = unit / a.strips;
+        c0 = (unit - b * a.strips) * (32 * E);
+        c = c0 + (threadIdx.x & 31) * E;
+        chans = (int)max((int64_t)0, min((int64_t)E, a.C - c));
+        read = chans > 0 ? c : 0;
+        second = chans > 1 ? 1 : 0;
+    }
+    // bytes from a span's first step to this thread's first step and channel
+    __device__ __forceinline__ uint32_t off(int64_t stride, int64_t first, int size) const
+    {
+        return (uint32_t)(((uint32_t)first * (uint32_t)stride + (uint32_t)read) * (uint32_t)size);
+    }
+};
+
+// Inputs straight to registers: a thread's S steps, element by element (rows need not be whole vectors).  A thread beyond
+// the last channel reads another one's (and stores nothing).
+template <typename T, int E, int S> struct Direct {
+    Pack<T, 1> q[S][E];
+    // p: the block's address (the same for all its threads) of the span's first step; off: this thread's bytes from it
+    template <bool FULL> __device__ __forceinline__ void load(const T* p, uint32_t off, int64_t stride, int live, int second)
     {
 #pragma unroll
         for (int i = 0; i < S; ++i) {
-            const T* at = p + (size_t)(i * stride);
-            if (!FULL) q[i][0] = q[i][E / LV - 1] = Pack<T, LV>::zero();
-            if (FULL || i < live) {
-                q[i][0] = Pack<T, LV>::load(at);
-                if (LV < E) q[i][E / LV - 1] = Pack<T, LV>::load(at + second);
+            const T* at = reinterpret_cast<const T*>(reinterpret_cast<const char*>(p + i * stride) + off);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                if (!FULL) q[i][e] = Pack<T, 1>::zero();
+                if (FULL || i < live) q[i][e] = Pack<T, 1>::load(at + (e ? second : 0));
             }
         }
     }
     __device__ __forceinline__ F<E> get(int i) const
     {
-        float v[E];
+        F<E> r;
 #pragma unroll
-        for (int j = 0; j < E / LV; ++j) {
-            float w[LV];
-            q[i][j].unpack(w);
-#pragma unroll
-            for (int e = 0; e < LV; ++e) v[j * LV + e] = w[e];
+        for (int e = 0; e < E; ++e) {
+            float w[1];
+            q[i][e].unpack(w);
+            r.v[e] = w[0];
         }
-        return F<E>::of(v);
+        return r;
     }
 };
+
+// Inputs through shared memory, two spans ahead, in 16-byte copies: the rows of a block's 64 steps of a strip are 128
+// bytes.  Thread k copies the chunk k % 8 of the rows k / 8 and k / 8 + 32 of each array.
+constexpr int kRowBytes = 128, kTileBytes = 8 * kSteps * kRowBytes;
+struct Copier {
+    uint32_t off;                    // bytes from the block's step of an array, without the row's
+    int row;
+    bool chunk;                      // the chunk lies within the channels
+    template <typename T, int E> __device__ __forceinline__ static Copier make(const GlrArgs& a, const Place<E>& at)
+    {
+        Copier c;
+        const int k = threadIdx.x & 7;
+        c.row = threadIdx.x >> 3;
+        c.chunk = at.c0 + k * (16 / (int)sizeof(T)) < a.C;
+        c.off = (uint32_t)(at.c0 * sizeof(T)) + k * 16;
+        return c;
+    }
+    // steps: rows of this block's tile that exist
+    template <typename T> __device__ __forceinline__ void copy(uint32_t to, const T* p, int64_t stride, int steps) const
+    {
+        to += row * kRowBytes + (threadIdx.x & 7) * 16;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const char* from = reinterpret_cast<const char*>(p + j * 32 * stride) + (uint32_t)(row * (uint32_t)stride * sizeof(T)) + off;
+            if (chunk && row + j * 32 < steps)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + j * 32 * kRowBytes), "l"(from) : "memory");
+        }
+    }
+};
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+template <typename T, int E> __device__ __forceinline__ F<E> staged(const char* tile, int row)
+{
+    const Pack<T, E> q = Pack<T, E>::load(reinterpret_cast<const T*>(tile + row * kRowBytes) + (threadIdx.x & 31) * E);
+    float v[E];
+    q.unpack(v);
+    return F<E>::of(v);
+}
+
 template <typename T, int LV, int E> __device__ __forceinline__ void store_step(T* p, F<E> x, int chans)
 {
     float v[E];
@@ -428,76 +533,84 @@ __device__ __forceinline__ uint32_t cuts_of(const unsigned char* z, int live)
     return z ? __ballot_sync(0xffffffffu, lane < live && z[lane] != 0) : 0;
 }
 
-// Where a thread stands: its block's unit is (sequence b, strip of channels).
-struct Place {
-    int warp, rank, chans;           // chans: channels of this thread that exist (0..E)
-    int second;                      // where the second one is read from (a channel that exists)
-    int64_t b, c, read;              // read: the channel that is read (c, or 0 beyond the last)
-    __device__ __forceinline__ Place(const GlrArgs& a, int cl)
-    {
-        warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
-        rank = cl > 1 ? (int)cluster_rank() : 0;
-        const int unit = blockIdx.x / cl;
-        b = unit / a.strips;
-        c = (unit - b * a.strips) * (32 * E) + (threadIdx.x & 31) * E;
-        chans = (int)max((int64_t)0, min((int64_t)E, a.C - c));
-        read = chans > 0 ? c : 0;
-        second = chans > 1 ? 1 : 0;
-    }
-};
-
-// Forward: S steps a thread, W warps a block, CL blocks a cluster.
-template <typename T, int LV, int S, int W, int CL>
-__global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_forward_kernel(const GlrArgs a)
+// Forward: S steps a thread, W warps a block, CL blocks a cluster; STAGED: inputs through shared memory (W = 8), else
+// into registers.
+template <typename T, bool STAGED, int S, int W, int CL>
+__global__ void __launch_bounds__(32 * W, W == 8 ? (STAGED ? (sizeof(T) == 2 ? 3 : 4) : 2) : 1) glr_forward_kernel(const GlrArgs a)
 {
-    __shared__ Meet<W, CL> meet;
-    const Place at(a, CL);
+    constexpr int E = 4 / (int)sizeof(T);
+    constexpr int LV = STAGED ? E : 1;
+    extern __shared__ __align__(128) char tiles[];       // STAGED: [2][r, g, x] tiles
+    __shared__ Meet<E, W, CL> meet;
+    const Place<E> at(a, CL);
     constexpr int64_t SPAN = (int64_t)S * W * CL;
-    const int64_t first = ((int64_t)at.rank * W + at.warp) * S;      // this thread's first step within a span
+    const int64_t mine = (int64_t)at.rank * W * S, first = mine + at.warp * S;   // the block's and the thread's first step
     const int chans = at.chans;
     const int64_t state = at.b * a.C + at.c;
-    const T* X = reinterpret_cast<const T*>(a.x) + at.b * a.xb + at.read;
-    const T* R = reinterpret_cast<const T*>(a.r) + at.b * a.rb + at.read;
-    const T* G = reinterpret_cast<const T*>(a.g) + at.b * a.gb + at.read;
-    T* Y = reinterpret_cast<T*>(a.y) + at.b * a.T * a.C + at.c;
+    const T* X = reinterpret_cast<const T*>(a.x) + at.b * a.xb;
+    const T* R = reinterpret_cast<const T*>(a.r) + at.b * a.rb;
+    const T* G = reinterpret_cast<const T*>(a.g) + at.b * a.gb;
+    T* Y = reinterpret_cast<T*>(a.y) + at.b * a.T * a.C;
+    const uint32_t to = at.off(a.C, first, sizeof(T));
     const unsigned char* Z = a.reset ? a.reset + at.b * a.T : nullptr;
     float* K = a.kept ? a.kept + at.b * ((a.T + kSteps - 1) / kSteps) * a.C + at.c : nullptr;
 
     const F<E> lambda = each(load_f32<E>(a.decay + at.c, chans), [](float d) { return softplus_of(d); });
     const F<E> one = F<E>::all(1.0f), zero = F<E>::all(0.0f), neg = F<E>::all(-1.0f);
     F<E> run = a.h0 ? load_f32<E>(a.h0 + state, chans) : zero;
-    Steps<T, E, LV, S> qx, qr, qg;
-    uint32_t cut;
-    auto fetch = [&](int64_t t) {
-        const int live = (int)min((int64_t)S, max((int64_t)0, a.T - t));
-        if (live == S) {
-            qr.template load<true>(R + t * a.rt, (uint32_t)a.rt, S, at.second);
-            qg.template load<true>(G + t * a.gt, (uint32_t)a.gt, S, at.second);
-            qx.template load<true>(X + t * a.xt, (uint32_t)a.xt, S, at.second);
+    Direct<T, E, STAGED ? 1 : S> qx, qr, qg;
+    const Copier cp = Copier::make<T, E>(a, at);
+    uint32_t cut = 0;
+    auto fetch = [&](int64_t base, int set) {
+        const int live = (int)min((int64_t)S, max((int64_t)0, a.T - base - first));
+        if constexpr (STAGED) {
+            const int steps = (int)min((int64_t)(S * W), max((int64_t)0, a.T - base - mine));
+            const uint32_t tile = smem_addr(tiles) + set * 3 * kTileBytes;
+            cp.copy<T>(tile, R + (base + mine) * a.rt, a.rt, steps);
+            cp.copy<T>(tile + kTileBytes, G + (base + mine) * a.gt, a.gt, steps);
+            cp.copy<T>(tile + 2 * kTileBytes, X + (base + mine) * a.xt, a.xt, steps);
+            copies_commit();
+        } else if (live == S) {
+            qr.template load<true>(R + base * a.rt, at.off(a.rt, first, sizeof(T)), a.rt, S, at.second);
+            qg.template load<true>(G + base * a.gt, at.off(a.gt, first, sizeof(T)), a.gt, S, at.second);
+            qx.template load<true>(X + base * a.xt, at.off(a.xt, first, sizeof(T)), a.xt, S, at.second);
         } else {
-            qr.template load<false>(R + t * a.rt, (uint32_t)a.rt, live, at.second);
-            qg.template load<false>(G + t * a.gt, (uint32_t)a.gt, live, at.second);
-            qx.template load<false>(X + t * a.xt, (uint32_t)a.xt, live, at.second);
+            qr.template load<false>(R + base * a.rt, at.off(a.rt, first, sizeof(T)), a.rt, live, at.second);
+            qg.template load<false>(G + base * a.gt, at.off(a.gt, first, sizeof(T)), a.gt, live, at.second);
+            qx.template load<false>(X + base * a.xt, at.off(a.xt, first, sizeof(T)), a.xt, live, at.second);
         }
-        cut = cuts_of(Z + t, Z ? live : 0);
+        cut = cuts_of(Z + base + first, Z ? live : 0);
     };
-    fetch(first);
     meet_init(meet);
     bool waits = true;
+    uint32_t cut_next = 0;
+    fetch(0, 0);
+    if constexpr (STAGED) {
+        cut_next = cut;
+        fetch(SPAN, 1);                                  // (nothing beyond the end)
+        const uint32_t t = cut;
+        cut = cut_next;
+        cut_next = t;
+        copies_wait<1>();
+        __syncthreads();
+    }
 
     int n = 0;
     for (int64_t base = 0; base < a.T; base += SPAN, ++n) {
-        const int64_t t = base + first;
-        const int live = (int)min((int64_t)S, max((int64_t)0, a.T - t));
+        const int live = (int)min((int64_t)S, max((int64_t)0, a.T - base - first));
         const uint32_t cuts = cut;
+        const char* tile = tiles + (n & 1) * 3 * kTileBytes;
+        auto in_r = [&](int i) { return STAGED ? staged<T, E>(tile, at.warp * S + i) : qr.get(STAGED ? 0 : i); };
+        auto in_g = [&](int i) { return STAGED ? staged<T, E>(tile + kTileBytes, at.warp * S + i) : qg.get(STAGED ? 0 : i); };
+        auto in_x = [&](int i) { return STAGED ? staged<T, E>(tile + 2 * kTileBytes, at.warp * S + i) : qx.get(STAGED ? 0 : i); };
         F<E> fa[S], bb[S], len = zero, B = zero;
 #pragma unroll
         for (int i = 0; i < S; ++i) {
-            const F<E> y = rcp_of(one + exp_minus(qr.get(i))) * lambda;
+            const F<E> y = rcp_of(one + exp_minus(in_r(i))) * lambda;
             const F<E> rest = rest_of(y), m2 = square_rest(rest);
             // m sigmoid(g) = m^2 / sqrt(m^2 (1 + e)^2) with e = exp(-g): one rsqrt, held where m is 0
-            const F<E> q = one + exp_minus<60>(qg.get(i));
-            bb[i] = m2 * rsq_of(fma(m2 * q, q, F<E>::all(kTiny))) * qx.get(i);
+            const F<E> q = one + exp_minus<60>(in_g(i));
+            bb[i] = m2 * rsq_of(fma(m2 * q, q, F<E>::all(kTiny))) * in_x(i);
             fa[i] = one + rest * neg;
             len = len + y;
             B = fma(fa[i], B, bb[i]);
@@ -507,13 +620,12 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_forward_kernel(con
 #pragma unroll
             for (int i = 0; i < S; ++i) {
                 if (i < live) {
-                    const F<E> y = rcp_of(one + exp_minus(qr.get(i))) * lambda;
-                    len = len + y;
+                    len = len + rcp_of(one + exp_minus(in_r(i))) * lambda;
                     B = fma(fa[i], B, bb[i]);
                 }
             }
         }
-        if (base + SPAN < a.T) fetch(t + SPAN);
+        if (!STAGED && base + SPAN < a.T) fetch(base + SPAN, 0);
         if (cuts) {                                      // resets among the steps: they cut off what comes before them
             B = zero;
             len = F<E>::all(INFINITY);
@@ -523,22 +635,36 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_forward_kernel(con
                 if (i < live) B = fma(fa[i], B, bb[i]);
             }
         }
-        F<E> h = Z ? exchange<W, CL, true>(meet, n, at.warp, at.rank, len, B, run, a.status, waits)
-                   : exchange<W, CL, false>(meet, n, at.warp, at.rank, len, B, run, a.status, waits);
-        if (K && live > 0) store_f32<E>(K + (t / kSteps) * a.C, h, chans);
-        T* y = Y + t * a.C;
+        F<E> h = exchange<E, W, CL>(
+            meet, n, at.warp, at.rank, len, B, run, Z != nullptr, a.status, waits,
+            [&] {
+                if constexpr (STAGED) copies_wait<0>();  // the next span's inputs, before the barrier
+            },
+            [&] {
+                if constexpr (STAGED) {                  // all warps have read this span's tiles
+                    cut = cut_next;
+                    if (base + 2 * SPAN < a.T) {
+                        const uint32_t t = cut;
+                        fetch(base + 2 * SPAN, n & 1);
+                        cut_next = cut;
+                        cut = t;
+                    }
+                }
+            });
+        if (K && live > 0) store_f32<E>(K + ((base + first) / kSteps) * a.C, h, chans);
+        auto y = [&](int i) { return reinterpret_cast<T*>(reinterpret_cast<char*>(Y + (base + i) * a.C) + to); };
         if (live == S && !cuts) {
 #pragma unroll
             for (int i = 0; i < S; ++i) {
                 h = fma(fa[i], h, bb[i]);
-                store_step<T, LV, E>(y + (size_t)(i * (uint32_t)a.C), h, chans);
+                store_step<T, LV, E>(y(i), h, chans);
             }
         } else {
 #pragma unroll
             for (int i = 0; i < S; ++i) {
                 if (cuts >> i & 1) h = zero;
                 h = fma(fa[i], h, bb[i]);
-                if (i < live) store_step<T, LV, E>(y + (size_t)(i * (uint32_t)a.C), h, chans);
+                if (i < live) store_step<T, LV, E>(y(i), h, chans);
             }
         }
     }
@@ -546,20 +672,24 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_forward_kernel(con
 }
 
 // Backward: the same split, walked from the end of the sequence.
-template <typename T, int LV, int W, int CL>
+template <typename T, bool STAGED, int W, int CL>
 __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_backward_kernel(const GlrArgs a)
 {
     constexpr int S = kSteps;                            // a thread's steps begin at a kept state
-    __shared__ Meet<W, CL> meet;
-    const Place at(a, CL);
+    constexpr int E = 4 / (int)sizeof(T);
+    constexpr int LV = STAGED ? E : 1;
+    extern __shared__ __align__(128) char tiles[];       // STAGED: [2][r, g, x, dy] tiles
+    __shared__ Meet<E, W, CL> meet;
+    const Place<E> at(a, CL);
     constexpr int64_t SPAN = (int64_t)S * W * CL;
-    const int64_t first = ((int64_t)at.rank * W + at.warp) * S;
+    const int64_t mine = (int64_t)at.rank * W * S, first = mine + at.warp * S;
     const int chans = at.chans;
-    const int64_t state = at.b * a.C + at.c, dense = at.b * a.T * a.C + at.c;
-    const T* X = reinterpret_cast<const T*>(a.x) + at.b * a.xb + at.read;
-    const T* R = reinterpret_cast<const T*>(a.r) + at.b * a.rb + at.read;
-    const T* G = reinterpret_cast<const T*>(a.g) + at.b * a.gb + at.read;
-    const T* D = reinterpret_cast<const T*>(a.dy) + at.b * a.T * a.C + at.read;
+    const int64_t state = at.b * a.C + at.c, dense = at.b * a.T * a.C;
+    const uint32_t place = at.off(a.C, first, sizeof(T));
+    const T* X = reinterpret_cast<const T*>(a.x) + at.b * a.xb;
+    const T* R = reinterpret_cast<const T*>(a.r) + at.b * a.rb;
+    const T* G = reinterpret_cast<const T*>(a.g) + at.b * a.gb;
+    const T* D = reinterpret_cast<const T*>(a.dy) + dense;
     const unsigned char* Z = a.reset ? a.reset + at.b * a.T : nullptr;
     const float* K = a.kept + at.b * ((a.T + kSteps - 1) / kSteps) * a.C + at.c;
 
@@ -569,25 +699,66 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_backward_kernel(co
     double acc[E];                                       // sum of dL L
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.0;
+    const Copier cp = Copier::make<T, E>(a, at);
+    auto copy = [&](int64_t base, int set) {
+        const int steps = (int)min((int64_t)(S * W), max((int64_t)0, a.T - base - mine));
+        const uint32_t tile = smem_addr(tiles) + set * 4 * kTileBytes;
+        cp.copy<T>(tile, R + (base + mine) * a.rt, a.rt, steps);
+        cp.copy<T>(tile + kTileBytes, G + (base + mine) * a.gt, a.gt, steps);
+        cp.copy<T>(tile + 2 * kTileBytes, X + (base + mine) * a.xt, a.xt, steps);
+        cp.copy<T>(tile + 3 * kTileBytes, D + (base + mine) * a.C, a.C, steps);
+        copies_commit();
+    };
     meet_init(meet);
     bool waits = true;
+    const int64_t end = (a.T - 1) / SPAN * SPAN;
+    if constexpr (STAGED) {
+        copy(end, 0);
+        if (end >= SPAN) copy(end - SPAN, 1);
+        else copies_commit();
+        copies_wait<1>();
+        __syncthreads();
+    }
 
     int n = 0;
-    for (int64_t base = (a.T - 1) / SPAN * SPAN; base >= 0; base -= SPAN, ++n) {
+    for (int64_t base = end; base >= 0; base -= SPAN, ++n) {
         const int64_t t = base + first;
         const int live = (int)min((int64_t)S, max((int64_t)0, a.T - t));
-        Steps<T, E, LV, S> qx, qr, qg, qd;
-        if (live == S) {
-            qr.template load<true>(R + t * a.rt, (uint32_t)a.rt, S, at.second);
-            qg.template load<true>(G + t * a.gt, (uint32_t)a.gt, S, at.second);
-            qx.template load<true>(X + t * a.xt, (uint32_t)a.xt, S, at.second);
-            qd.template load<true>(D + t * a.C, (uint32_t)a.C, S, at.second);
-        } else {
-            qr.template load<false>(R + t * a.rt, (uint32_t)a.rt, live, at.second);
-            qg.template load<false>(G + t * a.gt, (uint32_t)a.gt, live, at.second);
-            qx.template load<false>(X + t * a.xt, (uint32_t)a.xt, live, at.second);
-            qd.template load<false>(D + t * a.C, (uint32_t)a.C, live, at.second);
+        Direct<T, E, STAGED ? 1 : S> qx, qr, qg, qd;
+        if constexpr (!STAGED) {
+            if (live == S) {
+                qr.template load<true>(R + base * a.rt, at.off(a.rt, first, sizeof(T)), a.rt, S, at.second);
+                qg.template load<true>(G + base * a.gt, at.off(a.gt, first, sizeof(T)), a.gt, S, at.second);
+                qx.template load<true>(X + base * a.xt, at.off(a.xt, first, sizeof(T)), a.xt, S, at.second);
+                qd.template load<true>(D + base * a.C, at.off(a.C, first, sizeof(T)), a.C, S, at.second);
+            } else {
+                qr.template load<false>(R + base * a.rt, at.off(a.rt, first, sizeof(T)), a.rt, live, at.second);
+                qg.template load<false>(G + base * a.gt, at.off(a.gt, first, sizeof(T)), a.gt, live, at.second);
+                qx.template load<false>(X + base * a.xt, at.off(a.xt, first, sizeof(T)), a.xt, live, at.second);
+                qd.template load<false>(D + base * a.C, at.off(a.C, first, sizeof(T)), a.C, live, at.second);
+            }
         }
+        const char* tile = tiles + (n & 1) * 4 * kTileBytes;
+        auto in_r = [&](int i) { return STAGED ? staged<T, E>(tile, at.warp * S + i) : qr.get(STAGED ? 0 : i); };
+        auto in_g = [&](int i) { return STAGED ? staged<T, E>(tile + kTileBytes, at.warp * S + i) : qg.get(STAGED ? 0 : i); };
+        auto in_x = [&](int i) { return STAGED ? staged<T, E>(tile + 2 * kTileBytes, at.warp * S + i) : qx.get(STAGED ? 0 : i); };
+        Pack<T, E> dy[S];                                // (kept packed: the tile is free after the exchange's barrier)
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+            if constexpr (STAGED) {
+                dy[i] = i < live ? Pack<T, E>::load(reinterpret_cast<const T*>(tile + 3 * kTileBytes + (at.warp * S + i) * kRowBytes) + (threadIdx.x & 31) * E)
+                                 : Pack<T, E>::zero();
+            } else {
+                float v[E];
+                qd.get(STAGED ? 0 : i).get(v);
+                dy[i] = Pack<T, E>::pack(v);
+            }
+        }
+        auto in_d = [&](int i) {
+            float v[E];
+            dy[i].unpack(v);
+            return F<E>::of(v);
+        };
         const uint32_t cut = cuts_of(Z + t, Z ? live : 0);
         F<E> h = live > 0 ? load_f32<E>(K + (t / kSteps) * a.C, chans) : zero;
         // per step: the factor, and what d multiplies in each gradient:
@@ -595,8 +766,8 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_backward_kernel(co
         F<E> fa[S], cx[S], cg[S], cl[S], cr[S], len = zero;
 #pragma unroll
         for (int i = 0; i < S; ++i) {
-            const F<E> er = exp_minus<115>(qr.get(i)), eg = exp_minus<115>(qg.get(i));
-            const F<E> s = rcp_of(one + er), sg = rcp_of(one + eg), x = qx.get(i);
+            const F<E> er = exp_minus<115>(in_r(i)), eg = exp_minus<115>(in_g(i));
+            const F<E> s = rcp_of(one + er), sg = rcp_of(one + eg), x = in_x(i);
             const F<E> y = s * lambda;
             F<E> rest;
             decay_of(y, fa[i], rest);
@@ -616,32 +787,37 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_backward_kernel(co
         F<E> B = zero;
 #pragma unroll
         for (int i = S - 1; i >= 0; --i) {
-            B = fa[i] * (B + qd.get(i));
+            B = fa[i] * (B + in_d(i));
             if (cut >> i & 1) B = zero;
         }
         if (cut) len = F<E>::all(INFINITY);
-        F<E> flow = Z ? exchange<W, CL, true>(meet, n, W - 1 - at.warp, CL - 1 - at.rank, len, B, run, a.status, waits)
-                      : exchange<W, CL, false>(meet, n, W - 1 - at.warp, CL - 1 - at.rank, len, B, run, a.status, waits);
+        F<E> flow = exchange<E, W, CL>(
+            meet, n, W - 1 - at.warp, CL - 1 - at.rank, len, B, run, Z != nullptr, a.status, waits,
+            [&] {
+                if constexpr (STAGED) copies_wait<0>();
+            },
+            [&] {
+                if constexpr (STAGED)
+                    if (base >= 2 * SPAN) copy(base - 2 * SPAN, n & 1);
+            });
         F<E> part = zero;
-        const int64_t o = dense + t * a.C;
-        T *ox = reinterpret_cast<T*>(a.dx) + o, *orr = reinterpret_cast<T*>(a.dr) + o, *og = reinterpret_cast<T*>(a.dg) + o;
+        auto to = [&](void* p, int i) {
+            return reinterpret_cast<T*>(reinterpret_cast<char*>(reinterpret_cast<T*>(p) + dense + (base + i) * a.C) + place);
+        };
 #pragma unroll
         for (int i = S - 1; i >= 0; --i) {
-            const F<E> d = flow + qd.get(i), gx = d * cx[i], gl = d * cl[i];
+            const F<E> d = flow + in_d(i), gx = d * cx[i], gl = d * cl[i];
             flow = fa[i] * d;
             if (cut >> i & 1) flow = zero;
             if (i < live) {
-                const size_t step = (size_t)(i * (uint32_t)a.C);
                 part = part + gl;
-                if (a.dx) store_step<T, LV, E>(ox + step, gx, chans);
-                if (a.dr) store_step<T, LV, E>(orr + step, gl * cr[i], chans);
-                if (a.dg) store_step<T, LV, E>(og + step, gx * cg[i], chans);
+                if (a.dx) store_step<T, LV, E>(to(a.dx, i), gx, chans);
+                if (a.dr) store_step<T, LV, E>(to(a.dr, i), gl * cr[i], chans);
+                if (a.dg) store_step<T, LV, E>(to(a.dg, i), gx * cg[i], chans);
             }
         }
-        float f[E];
-        part.get(f);
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] += (double)f[e];
+        for (int e = 0; e < E; ++e) acc[e] += (double)part.v[e];
     }
     if (a.dh0 && at.rank == 0 && at.warp == 0) store_f32<E>(a.dh0 + state, run, chans);
     if (a.part) {
@@ -686,23 +862,25 @@ kan_status validate(const kan_glr_shape* s)
     for (int64_t v : st)
         if (v < 0) return gl_fail(KAN_ERR_INVALID_ARG, "negative stride");
     for (int i = 1; i < 6; i += 2)
-        if (st[i] > ((int64_t)1 << 28)) return gl_fail(KAN_ERR_UNSUPPORTED, "a stride of steps above 2^28 elements");
-    if (s->channels > ((int64_t)1 << 24) || s->time > ((int64_t)1 << 40) || s->batch > ((int64_t)1 << 31) ||
+        if (st[i] > kMaxStride) return gl_fail(KAN_ERR_UNSUPPORTED, "a stride of steps above 2^20 elements");
+    if (s->channels > kMaxStride || s->time > ((int64_t)1 << 40) || s->batch > ((int64_t)1 << 31) ||
         s->batch * ((s->channels + 31) / 32) > ((int64_t)1 << 27))
         return gl_fail(KAN_ERR_UNSUPPORTED, "sizes too large");
     return KAN_OK;
 }
 
 // Clusters of a kernel that run at once on the current device, looked up once per device (a table per kernel).
-template <typename K> int resident(K kernel, int warps, int cluster, std::atomic<int> (&known)[64])
+template <typename K> int resident(K kernel, int warps, int cluster, size_t smem, std::atomic<int> (&known)[64])
 {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
     int n = known[dev].load(std::memory_order_relaxed);
     if (n) return n;
     cudaLaunchConfig_t cfg{};
+    if (smem && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return 0;
     cfg.gridDim = dim3(cluster);
     cfg.blockDim = dim3(32 * warps);
+    cfg.dynamicSmemBytes = smem;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = cluster;
@@ -717,11 +895,12 @@ template <typename K> int resident(K kernel, int warps, int cluster, std::atomic
     return n;
 }
 
-template <typename K> cudaError_t launch(K kernel, int warps, int cluster, const GlrArgs& a, cudaStream_t st)
+template <typename K> cudaError_t launch(K kernel, int warps, int cluster, size_t smem, const GlrArgs& a, cudaStream_t st)
 {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(a.B * a.strips * cluster));
     cfg.blockDim = dim3(32 * warps);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -736,27 +915,30 @@ template <typename K> cudaError_t launch(K kernel, int warps, int cluster, const
 
 // The kernels of one direction and operand type: blocks of 8 warps in clusters of 1 to 8, and a block of one warp for
 // sequences of at most 8 steps (and, forward, for a single one).
-template <typename T, int LV, bool BWD> struct Kernels {
+template <typename T, bool STAGED, bool BWD> struct Kernels {
+    static constexpr size_t kSmem = STAGED ? 2 * (BWD ? 4 : 3) * kTileBytes : 0;
     static void (*of(int cluster))(const GlrArgs)
     {
         if constexpr (BWD)
-            return cluster == 1 ? glr_backward_kernel<T, LV, 8, 1> : cluster == 2 ? glr_backward_kernel<T, LV, 8, 2>
-                 : cluster == 4 ? glr_backward_kernel<T, LV, 8, 4> : glr_backward_kernel<T, LV, 8, 8>;
+            return cluster == 1 ? glr_backward_kernel<T, STAGED, 8, 1> : cluster == 2 ? glr_backward_kernel<T, STAGED, 8, 2>
+                 : cluster == 4 ? glr_backward_kernel<T, STAGED, 8, 4> : glr_backward_kernel<T, STAGED, 8, 8>;
         else
-            return cluster == 1 ? glr_forward_kernel<T, LV, kSteps, 8, 1> : cluster == 2 ? glr_forward_kernel<T, LV, kSteps, 8, 2>
-                 : cluster == 4 ? glr_forward_kernel<T, LV, kSteps, 8, 4> : glr_forward_kernel<T, LV, kSteps, 8, 8>;
+            return cluster == 1 ? glr_forward_kernel<T, STAGED, kSteps, 8, 1> : cluster == 2 ? glr_forward_kernel<T, STAGED, kSteps, 8, 2>
+                 : cluster == 4 ? glr_forward_kernel<T, STAGED, kSteps, 8, 4> : glr_forward_kernel<T, STAGED, kSteps, 8, 8>;
     }
-    // Blocks of a cluster lie side by side in time: the size that needs the fewest rounds of spans on a full device.
+    // Blocks of a cluster lie side by side in time: the size that needs the fewest rounds of spans on a full device,
+    // a span costing a little more with each block whose maps are walked.
     static int cluster_for(const GlrArgs& a)
     {
         static std::atomic<int> known[4][64];
         const int64_t units = a.B * a.strips;
-        int best = 1;
+        int best = 0;
         int64_t cost = -1;
         for (int i = 0; i < 4; ++i) {
             const int cl = 1 << i;
-            const int64_t at_once = resident(of(cl), 8, cl, known[i]);
-            const int64_t c = (units + at_once - 1) / at_once * ((a.T + 8 * kSteps * cl - 1) / (8 * kSteps * cl));
+            const int64_t at_once = resident(of(cl), 8, cl, kSmem, known[i]);
+            if (at_once < 1) return 0;
+            const int64_t c = (units + at_once - 1) / at_once * ((a.T + 8 * kSteps * cl - 1) / (8 * kSteps * cl)) * (16 + cl);
             if (cost < 0 || c < cost) {
                 cost = c;
                 best = cl;
@@ -766,35 +948,40 @@ template <typename T, int LV, bool BWD> struct Kernels {
     }
     static cudaError_t run(GlrArgs& a, int& cluster, cudaStream_t st)
     {
-        cluster = 1;
-        if (a.T <= kSteps) {
-            if constexpr (BWD) return launch(glr_backward_kernel<T, LV, 1, 1>, 1, 1, a, st);
-            else if (a.T == 1) return launch(glr_forward_kernel<T, LV, 1, 1, 1>, 1, 1, a, st);
-            else return launch(glr_forward_kernel<T, LV, kSteps, 1, 1>, 1, 1, a, st);
-        }
         cluster = cluster_for(a);
-        return launch(of(cluster), 8, cluster, a, st);
+        return cluster ? launch(of(cluster), 8, cluster, kSmem, a, st) : cudaErrorInvalidValue;
     }
 };
-
-// Whole vectors of the two channels of a thread where every row of every operand begins on one.
-bool pairs(const kan_glr_shape& s, const GlrArgs& a)
+template <typename T, bool BWD> cudaError_t run_short(const GlrArgs& a, cudaStream_t st)
 {
-    const uint64_t odd = (uint64_t)(s.channels | s.x_stride_b | s.x_stride_t | s.r_stride_b | s.r_stride_t | s.g_stride_b |
-                                    s.g_stride_t) & 1;
-    const uint64_t addr = (reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.r) |
-                           reinterpret_cast<uintptr_t>(a.g) | reinterpret_cast<uintptr_t>(a.y) |
-                           reinterpret_cast<uintptr_t>(a.dy) | reinterpret_cast<uintptr_t>(a.dx) |
-                           reinterpret_cast<uintptr_t>(a.dr) | reinterpret_cast<uintptr_t>(a.dg));
-    return !odd && addr % (s.dtype == KAN_F32 ? 8 : 4) == 0;
+    if constexpr (BWD) return launch(glr_backward_kernel<T, false, 1, 1>, 1, 1, 0, a, st);
+    else if (a.T == 1) return launch(glr_forward_kernel<T, false, 1, 1, 1>, 1, 1, 0, a, st);
+    else return launch(glr_forward_kernel<T, false, kSteps, 1, 1>, 1, 1, 0, a, st);
 }
 
+// Inputs go through shared memory where their rows begin on 16 bytes and outputs on what a thread stores.
+bool staged_ok(const kan_glr_shape& s, const GlrArgs& a)
+{
+    const int esz = s.dtype == KAN_F32 ? 4 : 2;
+    const uint64_t strides = (uint64_t)(s.channels | s.x_stride_b | s.x_stride_t | s.r_stride_b | s.r_stride_t | s.g_stride_b |
+                                        s.g_stride_t) * esz;
+    const uint64_t in = (reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.r) |
+                         reinterpret_cast<uintptr_t>(a.g) | reinterpret_cast<uintptr_t>(a.dy));
+    const uint64_t out = (reinterpret_cast<uintptr_t>(a.y) | reinterpret_cast<uintptr_t>(a.dx) |
+                          reinterpret_cast<uintptr_t>(a.dr) | reinterpret_cast<uintptr_t>(a.dg));
+    return strides % 16 == 0 && in % 16 == 0 && out % 4 == 0;
+}
+
+template <typename T, bool BWD> cudaError_t run_type(const kan_glr_shape& s, GlrArgs& a, int& cluster, cudaStream_t st)
+{
+    a.strips = (int)((s.channels + 32 * (4 / sizeof(T)) - 1) / (32 * (4 / sizeof(T))));
+    cluster = 1;
+    if (a.T <= kSteps) return run_short<T, BWD>(a, st);
+    return staged_ok(s, a) ? Kernels<T, true, BWD>::run(a, cluster, st) : Kernels<T, false, BWD>::run(a, cluster, st);
+}
 template <bool BWD> cudaError_t run(const kan_glr_shape& s, GlrArgs& a, int& cluster, cudaStream_t st)
 {
-    if (s.dtype == KAN_F32)
-        return pairs(s, a) ? Kernels<float, 2, BWD>::run(a, cluster, st) : Kernels<float, 1, BWD>::run(a, cluster, st);
-    return pairs(s, a) ? Kernels<__nv_bfloat16, 2, BWD>::run(a, cluster, st)
-                       : Kernels<__nv_bfloat16, 1, BWD>::run(a, cluster, st);
+    return s.dtype == KAN_F32 ? run_type<float, BWD>(s, a, cluster, st) : run_type<__nv_bfloat16, BWD>(s, a, cluster, st);
 }
 
 void common_args(const kan_glr_shape& s, GlrArgs& a)
@@ -803,7 +990,6 @@ void common_args(const kan_glr_shape& s, GlrArgs& a)
     a.rb = s.r_stride_b, a.rt = s.r_stride_t;
     a.gb = s.g_stride_b, a.gt = s.g_stride_t;
     a.B = s.batch, a.T = s.time, a.C = s.channels;
-    a.strips = (int)((s.channels + 32 * E - 1) / (32 * E));
     a.status = device_status_ptr();
 }
 
