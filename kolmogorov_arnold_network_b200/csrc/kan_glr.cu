@@ -462,28 +462,21 @@ template <typename T, int E, int S> struct Direct {
 // bytes.  Thread k copies the chunk k % 8 of the rows k / 8 and k / 8 + 32 of each array.
 constexpr int kRowBytes = 128, kTileBytes = 8 * kSteps * kRowBytes;
 struct Copier {
-    uint32_t off;                    // bytes from the block's step of an array, without the row's
-    int row;
-    bool chunk;                      // the chunk lies within the channels
-    template <typename T, int E> __device__ __forceinline__ static Copier make(const GlrArgs& a, const Place<E>& at)
+    const char* from;                // this thread's chunk of the next span's tile
+    int64_t half, span;              // bytes to the row 32 further, to the next tile in the walk's direction
+    // p: the array at the sequence's first step; step: the tile's first step; spans: steps to the next tile (may be negative)
+    template <typename T> __device__ __forceinline__ Copier(const T* p, int64_t stride, int64_t c0, int64_t step, int64_t spans)
     {
-        Copier c;
-        const int k = threadIdx.x & 7;
-        c.row = threadIdx.x >> 3;
-        c.chunk = at.c0 + k * (16 / (int)sizeof(T)) < a.C;
-        c.off = (uint32_t)(at.c0 * sizeof(T)) + k * 16;
-        return c;
+        from = reinterpret_cast<const char*>(p + (step + (threadIdx.x >> 3)) * stride + c0) + (threadIdx.x & 7) * 16;
+        half = 32 * stride * (int64_t)sizeof(T);
+        span = spans * stride * (int64_t)sizeof(T);
     }
-    // steps: rows of this block's tile that exist
-    template <typename T> __device__ __forceinline__ void copy(uint32_t to, const T* p, int64_t stride, int steps) const
+    // rows and row 32 further: exist
+    __device__ __forceinline__ void copy(uint32_t to, bool row, bool further)
     {
-        to += row * kRowBytes + (threadIdx.x & 7) * 16;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const char* from = reinterpret_cast<const char*>(p + j * 32 * stride) + (uint32_t)(row * (uint32_t)stride * sizeof(T)) + off;
-            if (chunk && row + j * 32 < steps)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + j * 32 * kRowBytes), "l"(from) : "memory");
-        }
+        if (row) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+        if (further) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 32 * kRowBytes), "l"(from + half) : "memory");
+        from += span;
     }
 };
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -526,13 +519,6 @@ template <int E> __device__ __forceinline__ void store_f32(float* p, F<E> x, int
     for (int e = 0; e < E; ++e)
         if (e < chans) p[e] = v[e];
 }
-// Bits of the steps whose reset is set; the whole warp asks for the same steps.
-__device__ __forceinline__ uint32_t cuts_of(const unsigned char* z, int live)
-{
-    const int lane = threadIdx.x & 31;
-    return z ? __ballot_sync(0xffffffffu, lane < live && z[lane] != 0) : 0;
-}
-
 // Forward: S steps a thread, W warps a block, CL blocks a cluster; STAGED: inputs through shared memory (W = 8), else
 // into registers.
 template <typename T, bool STAGED, int S, int W, int CL>
@@ -550,25 +536,29 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? (STAGED ? (sizeof(T) == 2 ? 3
     const T* X = reinterpret_cast<const T*>(a.x) + at.b * a.xb;
     const T* R = reinterpret_cast<const T*>(a.r) + at.b * a.rb;
     const T* G = reinterpret_cast<const T*>(a.g) + at.b * a.gb;
-    T* Y = reinterpret_cast<T*>(a.y) + at.b * a.T * a.C;
-    const uint32_t to = at.off(a.C, first, sizeof(T));
+    T* Y = reinterpret_cast<T*>(a.y) + (at.b * a.T + first) * a.C + at.c;      // this thread's first output of the span
     const unsigned char* Z = a.reset ? a.reset + at.b * a.T : nullptr;
-    float* K = a.kept ? a.kept + at.b * ((a.T + kSteps - 1) / kSteps) * a.C + at.c : nullptr;
+    float* K = a.kept ? a.kept + (at.b * ((a.T + kSteps - 1) / kSteps) + first / kSteps) * a.C + at.c : nullptr;
 
     const F<E> lambda = each(load_f32<E>(a.decay + at.c, chans), [](float d) { return softplus_of(d); });
     const F<E> one = F<E>::all(1.0f), zero = F<E>::all(0.0f), neg = F<E>::all(-1.0f);
     F<E> run = a.h0 ? load_f32<E>(a.h0 + state, chans) : zero;
     Direct<T, E, STAGED ? 1 : S> qx, qr, qg;
-    const Copier cp = Copier::make<T, E>(a, at);
-    uint32_t cut = 0;
+    Copier cr(R, a.rt, at.c0, mine, SPAN), cg(G, a.gt, at.c0, mine, SPAN), cx(X, a.xt, at.c0, mine, SPAN);
+    const bool chunk = at.c0 + (threadIdx.x & 7) * (16 / (int)sizeof(T)) < a.C;      // a chunk that this thread copies exists
+    const uint32_t place = smem_addr(tiles) + threadIdx.x * 16;
+    const int lane = threadIdx.x & 31;
+    unsigned char zb = 0;                                // the reset byte of this lane's step of the next span
     auto fetch = [&](int64_t base, int set) {
         const int live = (int)min((int64_t)S, max((int64_t)0, a.T - base - first));
+        if (Z) zb = lane < live ? Z[base + first + lane] : 0;
         if constexpr (STAGED) {
-            const int steps = (int)min((int64_t)(S * W), max((int64_t)0, a.T - base - mine));
-            const uint32_t tile = smem_addr(tiles) + set * 3 * kTileBytes;
-            cp.copy<T>(tile, R + (base + mine) * a.rt, a.rt, steps);
-            cp.copy<T>(tile + kTileBytes, G + (base + mine) * a.gt, a.gt, steps);
-            cp.copy<T>(tile + 2 * kTileBytes, X + (base + mine) * a.xt, a.xt, steps);
+            const int64_t left = a.T - base - mine - (threadIdx.x >> 3);
+            const bool r0 = chunk && left > 0, r1 = chunk && left > 32;
+            const uint32_t tile = place + set * 3 * kTileBytes;
+            cr.copy(tile, r0, r1);
+            cg.copy(tile + kTileBytes, r0, r1);
+            cx.copy(tile + 2 * kTileBytes, r0, r1);
             copies_commit();
         } else if (live == S) {
             qr.template load<true>(R + base * a.rt, at.off(a.rt, first, sizeof(T)), a.rt, S, at.second);
@@ -579,18 +569,14 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? (STAGED ? (sizeof(T) == 2 ? 3
             qg.template load<false>(G + base * a.gt, at.off(a.gt, first, sizeof(T)), a.gt, live, at.second);
             qx.template load<false>(X + base * a.xt, at.off(a.xt, first, sizeof(T)), a.xt, live, at.second);
         }
-        cut = cuts_of(Z + base + first, Z ? live : 0);
     };
     meet_init(meet);
     bool waits = true;
-    uint32_t cut_next = 0;
+    unsigned char zb_now;
     fetch(0, 0);
+    zb_now = zb;
     if constexpr (STAGED) {
-        cut_next = cut;
         fetch(SPAN, 1);                                  // (nothing beyond the end)
-        const uint32_t t = cut;
-        cut = cut_next;
-        cut_next = t;
         copies_wait<1>();
         __syncthreads();
     }
@@ -598,7 +584,7 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? (STAGED ? (sizeof(T) == 2 ? 3
     int n = 0;
     for (int64_t base = 0; base < a.T; base += SPAN, ++n) {
         const int live = (int)min((int64_t)S, max((int64_t)0, a.T - base - first));
-        const uint32_t cuts = cut;
+        const uint32_t cuts = Z ? __ballot_sync(0xffffffffu, zb_now != 0) : 0;
         const char* tile = tiles + (n & 1) * 3 * kTileBytes;
         auto in_r = [&](int i) { return STAGED ? staged<T, E>(tile, at.warp * S + i) : qr.get(STAGED ? 0 : i); };
         auto in_g = [&](int i) { return STAGED ? staged<T, E>(tile + kTileBytes, at.warp * S + i) : qg.get(STAGED ? 0 : i); };
@@ -626,6 +612,7 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? (STAGED ? (sizeof(T) == 2 ? 3
             }
         }
         if (!STAGED && base + SPAN < a.T) fetch(base + SPAN, 0);
+        zb_now = zb;
         if (cuts) {                                      // resets among the steps: they cut off what comes before them
             B = zero;
             len = F<E>::all(INFINITY);
@@ -641,32 +628,34 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? (STAGED ? (sizeof(T) == 2 ? 3
                 if constexpr (STAGED) copies_wait<0>();  // the next span's inputs, before the barrier
             },
             [&] {
-                if constexpr (STAGED) {                  // all warps have read this span's tiles
-                    cut = cut_next;
-                    if (base + 2 * SPAN < a.T) {
-                        const uint32_t t = cut;
-                        fetch(base + 2 * SPAN, n & 1);
-                        cut_next = cut;
-                        cut = t;
-                    }
-                }
+                if constexpr (STAGED)                    // all warps have read this span's tiles
+                    if (base + 2 * SPAN < a.T) fetch(base + 2 * SPAN, n & 1);
             });
-        if (K && live > 0) store_f32<E>(K + ((base + first) / kSteps) * a.C, h, chans);
-        auto y = [&](int i) { return reinterpret_cast<T*>(reinterpret_cast<char*>(Y + (base + i) * a.C) + to); };
+        if (K) {
+            if (live > 0) store_f32<E>(K, h, chans);
+            K += SPAN / kSteps * a.C;
+        }
         if (live == S && !cuts) {
+            if (chans > 0) {
+                T* y = Y;
 #pragma unroll
-            for (int i = 0; i < S; ++i) {
-                h = fma(fa[i], h, bb[i]);
-                store_step<T, LV, E>(y(i), h, chans);
+                for (int i = 0; i < S; ++i) {
+                    h = fma(fa[i], h, bb[i]);
+                    store_step<T, LV, E>(y, h, STAGED ? E : chans);
+                    y += a.C;
+                }
             }
         } else {
+            T* y = Y;
 #pragma unroll
             for (int i = 0; i < S; ++i) {
                 if (cuts >> i & 1) h = zero;
                 h = fma(fa[i], h, bb[i]);
-                if (i < live) store_step<T, LV, E>(y(i), h, chans);
+                if (i < live) store_step<T, LV, E>(y, h, chans);
+                y += a.C;
             }
         }
+        Y += SPAN * a.C;
     }
     if (a.h_last && at.rank == 0 && at.warp == 0) store_f32<E>(a.h_last + state, run, chans);
 }
@@ -684,14 +673,14 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_backward_kernel(co
     constexpr int64_t SPAN = (int64_t)S * W * CL;
     const int64_t mine = (int64_t)at.rank * W * S, first = mine + at.warp * S;
     const int chans = at.chans;
-    const int64_t state = at.b * a.C + at.c, dense = at.b * a.T * a.C;
-    const uint32_t place = at.off(a.C, first, sizeof(T));
+    const int64_t state = at.b * a.C + at.c, end = (a.T - 1) / SPAN * SPAN;       // end: the last span's first step
     const T* X = reinterpret_cast<const T*>(a.x) + at.b * a.xb;
     const T* R = reinterpret_cast<const T*>(a.r) + at.b * a.rb;
     const T* G = reinterpret_cast<const T*>(a.g) + at.b * a.gb;
-    const T* D = reinterpret_cast<const T*>(a.dy) + dense;
+    const T* D = reinterpret_cast<const T*>(a.dy) + at.b * a.T * a.C;
     const unsigned char* Z = a.reset ? a.reset + at.b * a.T : nullptr;
-    const float* K = a.kept + at.b * ((a.T + kSteps - 1) / kSteps) * a.C + at.c;
+    const float* K = a.kept + (at.b * ((a.T + kSteps - 1) / kSteps) + (end + first) / kSteps) * a.C + at.c;
+    int64_t out = (at.b * a.T + end + first) * a.C + at.c;                        // this thread's first output of the span
 
     const F<E> lambda = each(load_f32<E>(a.decay + at.c, chans), [](float d) { return softplus_of(d); });
     const F<E> one = F<E>::all(1.0f), zero = F<E>::all(0.0f), neg = F<E>::all(-1.0f);
@@ -699,19 +688,32 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_backward_kernel(co
     double acc[E];                                       // sum of dL L
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.0;
-    const Copier cp = Copier::make<T, E>(a, at);
+    Copier cr(R, a.rt, at.c0, end + mine, -SPAN), cg(G, a.gt, at.c0, end + mine, -SPAN), cx(X, a.xt, at.c0, end + mine, -SPAN),
+        cd(D, a.C, at.c0, end + mine, -SPAN);
+    const bool chunk = at.c0 + (threadIdx.x & 7) * (16 / (int)sizeof(T)) < a.C;
+    const uint32_t place = smem_addr(tiles) + threadIdx.x * 16;
+    const int lane = threadIdx.x & 31;
+    unsigned char zb = 0;                                // reset byte of this lane's step, and the kept state, of the next span
+    F<E> hb = F<E>::all(0.0f);
     auto copy = [&](int64_t base, int set) {
-        const int steps = (int)min((int64_t)(S * W), max((int64_t)0, a.T - base - mine));
-        const uint32_t tile = smem_addr(tiles) + set * 4 * kTileBytes;
-        cp.copy<T>(tile, R + (base + mine) * a.rt, a.rt, steps);
-        cp.copy<T>(tile + kTileBytes, G + (base + mine) * a.gt, a.gt, steps);
-        cp.copy<T>(tile + 2 * kTileBytes, X + (base + mine) * a.xt, a.xt, steps);
-        cp.copy<T>(tile + 3 * kTileBytes, D + (base + mine) * a.C, a.C, steps);
+        const int64_t left = a.T - base - mine - (threadIdx.x >> 3);
+        const bool r0 = chunk && left > 0, r1 = chunk && left > 32;
+        const uint32_t tile = place + set * 4 * kTileBytes;
+        cr.copy(tile, r0, r1);
+        cg.copy(tile + kTileBytes, r0, r1);
+        cx.copy(tile + 2 * kTileBytes, r0, r1);
+        cd.copy(tile + 3 * kTileBytes, r0, r1);
         copies_commit();
+    };
+    auto ahead = [&](int64_t base) {                     // called once for each span, in the walk's order
+        const int live = (int)min((int64_t)S, max((int64_t)0, a.T - base - first));
+        if (Z) zb = lane < live ? Z[base + first + lane] : 0;
+        if (live > 0) hb = load_f32<E>(K, chans);
+        K -= SPAN / kSteps * a.C;
     };
     meet_init(meet);
     bool waits = true;
-    const int64_t end = (a.T - 1) / SPAN * SPAN;
+    ahead(end);
     if constexpr (STAGED) {
         copy(end, 0);
         if (end >= SPAN) copy(end - SPAN, 1);
@@ -722,8 +724,7 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_backward_kernel(co
 
     int n = 0;
     for (int64_t base = end; base >= 0; base -= SPAN, ++n) {
-        const int64_t t = base + first;
-        const int live = (int)min((int64_t)S, max((int64_t)0, a.T - t));
+        const int live = (int)min((int64_t)S, max((int64_t)0, a.T - base - first));
         Direct<T, E, STAGED ? 1 : S> qx, qr, qg, qd;
         if constexpr (!STAGED) {
             if (live == S) {
@@ -759,11 +760,12 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_backward_kernel(co
             dy[i].unpack(v);
             return F<E>::of(v);
         };
-        const uint32_t cut = cuts_of(Z + t, Z ? live : 0);
-        F<E> h = live > 0 ? load_f32<E>(K + (t / kSteps) * a.C, chans) : zero;
+        const uint32_t cut = Z ? __ballot_sync(0xffffffffu, zb != 0) : 0;
+        F<E> h = hb;
+        if (base > 0) ahead(base - SPAN);
         // per step: the factor, and what d multiplies in each gradient:
-        //   dx = d cx,  dg = dx cg,  dL L = d cl,  dr = dL L cr
-        F<E> fa[S], cx[S], cg[S], cl[S], cr[S], len = zero;
+        //   dx = d cx_,  dg = dx cg_,  dL L = d cl,  dr = dL L cr_
+        F<E> fa[S], cx_[S], cg_[S], cl[S], cr_[S], len = zero, B = zero;
 #pragma unroll
         for (int i = 0; i < S; ++i) {
             const F<E> er = exp_minus<115>(in_r(i)), eg = exp_minus<115>(in_g(i));
@@ -773,24 +775,35 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_backward_kernel(co
             decay_of(y, fa[i], rest);
             // 1 / m, held where m is 0 (there y is 0 too, and y / m goes to 0 with it)
             const F<E> m2 = square_rest(rest), rm = rsq_of(m2 + F<E>::all(kTiny));
-            if (cut >> i & 1) h = zero;
-            cx[i] = m2 * rm * sg;
-            cg[i] = x * (eg * sg);
-            cr[i] = er * s;
+            cx_[i] = m2 * rm * sg;
+            cg_[i] = x * (eg * sg);
+            cr_[i] = er * s;
+            if (cut && cut >> i & 1) h = zero;
             // a L (h - a u / m), L = -y
             cl[i] = fa[i] * y * fma(fa[i] * rm, sg * x, h * neg);
-            h = fma(fa[i], h, cx[i] * x);
-            if (live < S && i >= live) fa[i] = one;      // past the end: gamma passes (dy is 0 there)
-            else len = len + y;
+            h = fma(fa[i], h, cx_[i] * x);
+            len = len + y;
+        }
+        if (live < S) {                                  // past the end: gamma passes (dy is 0 there)
+            len = zero;
+#pragma unroll
+            for (int i = 0; i < S; ++i) {
+                if (i < live) len = len + rcp_of(one + exp_minus<115>(in_r(i))) * lambda;
+                else fa[i] = one;
+            }
         }
         // the map of these steps, from the last to the first: gamma -> a (gamma + dy)
-        F<E> B = zero;
 #pragma unroll
-        for (int i = S - 1; i >= 0; --i) {
-            B = fa[i] * (B + in_d(i));
-            if (cut >> i & 1) B = zero;
+        for (int i = S - 1; i >= 0; --i) B = fa[i] * (B + in_d(i));
+        if (cut) {
+            B = zero;
+#pragma unroll
+            for (int i = S - 1; i >= 0; --i) {
+                B = fa[i] * (B + in_d(i));
+                if (cut >> i & 1) B = zero;
+            }
+            len = F<E>::all(INFINITY);
         }
-        if (cut) len = F<E>::all(INFINITY);
         F<E> flow = exchange<E, W, CL>(
             meet, n, W - 1 - at.warp, CL - 1 - at.rank, len, B, run, Z != nullptr, a.status, waits,
             [&] {
@@ -801,21 +814,37 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_backward_kernel(co
                     if (base >= 2 * SPAN) copy(base - 2 * SPAN, n & 1);
             });
         F<E> part = zero;
-        auto to = [&](void* p, int i) {
-            return reinterpret_cast<T*>(reinterpret_cast<char*>(reinterpret_cast<T*>(p) + dense + (base + i) * a.C) + place);
-        };
+        T *ox = reinterpret_cast<T*>(a.dx) + out + S * a.C, *orr = reinterpret_cast<T*>(a.dr) + out + S * a.C,
+          *og = reinterpret_cast<T*>(a.dg) + out + S * a.C;
+        if (live == S && !cut) {
+            if (chans > 0) {
 #pragma unroll
-        for (int i = S - 1; i >= 0; --i) {
-            const F<E> d = flow + in_d(i), gx = d * cx[i], gl = d * cl[i];
-            flow = fa[i] * d;
-            if (cut >> i & 1) flow = zero;
-            if (i < live) {
-                part = part + gl;
-                if (a.dx) store_step<T, LV, E>(to(a.dx, i), gx, chans);
-                if (a.dr) store_step<T, LV, E>(to(a.dr, i), gl * cr[i], chans);
-                if (a.dg) store_step<T, LV, E>(to(a.dg, i), gx * cg[i], chans);
+                for (int i = S - 1; i >= 0; --i) {
+                    const F<E> d = flow + in_d(i), gx = d * cx_[i], gl = d * cl[i];
+                    flow = fa[i] * d;
+                    part = part + gl;
+                    ox -= a.C, orr -= a.C, og -= a.C;
+                    if (a.dx) store_step<T, LV, E>(ox, gx, STAGED ? E : chans);
+                    if (a.dr) store_step<T, LV, E>(orr, gl * cr_[i], STAGED ? E : chans);
+                    if (a.dg) store_step<T, LV, E>(og, gx * cg_[i], STAGED ? E : chans);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = S - 1; i >= 0; --i) {
+                const F<E> d = flow + in_d(i), gx = d * cx_[i], gl = d * cl[i];
+                flow = fa[i] * d;
+                if (cut >> i & 1) flow = zero;
+                ox -= a.C, orr -= a.C, og -= a.C;
+                if (i < live) {
+                    part = part + gl;
+                    if (a.dx) store_step<T, LV, E>(ox, gx, chans);
+                    if (a.dr) store_step<T, LV, E>(orr, gl * cr_[i], chans);
+                    if (a.dg) store_step<T, LV, E>(og, gx * cg_[i], chans);
+                }
             }
         }
+        out -= SPAN * a.C;
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] += (double)part.v[e];
     }
