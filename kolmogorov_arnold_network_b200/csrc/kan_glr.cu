@@ -34,6 +34,7 @@
 // reads 1/2 byte an element instead of y, and unrounded states.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "kan_device.cuh"
 #include "kan_vec.cuh"
@@ -43,7 +44,7 @@ namespace {
 
 constexpr int kSteps = 8;         // steps per thread, and the spacing of the kept states
 
-constexpr int kMaxCluster = 8;    // blocks of a cluster (the portable bound)
+constexpr int kMaxCluster = 16;   // blocks of a cluster
 constexpr int64_t kMaxStride = 1 << 20;   // elements from a step to the next: a span of 512 steps stays within 32 bits of bytes
 
 struct GlrArgs {
@@ -62,7 +63,7 @@ struct GlrArgs {
     float* dh0;                         // [B, C] or null
     double* part;                       // [B * cluster][C] partial sums for ddecay, or null
     int64_t B, T, C;
-    int strips;                         // of 128 bytes
+    int strips;                         // of 32 channels
     unsigned int* status;
 };
 
@@ -95,146 +96,148 @@ __device__ __forceinline__ float min_nan(float x, float y)
     return r;
 }
 
-// E neighbouring channels of a thread.
-template <int E> struct F {
-    float v[E];
-    __device__ __forceinline__ static F all(float x)
-    {
-        F r;
-#pragma unroll
-        for (int e = 0; e < E; ++e) r.v[e] = x;
-        return r;
-    }
-    __device__ __forceinline__ static F of(const float (&x)[E])
-    {
-        F r;
-#pragma unroll
-        for (int e = 0; e < E; ++e) r.v[e] = x[e];
-        return r;
-    }
-    __device__ __forceinline__ void get(float (&x)[E]) const
-    {
-#pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = v[e];
-    }
+// N steps of a thread's channel side by side; two of them go through the packed f32x2 instructions (two independent
+// roundings).
+template <int N> struct F {
+    float v[N];
 };
-template <int E> __device__ __forceinline__ F<E> fma(F<E> x, F<E> y, F<E> z)
+__device__ __forceinline__ uint64_t pk(F<2> x)
 {
-    F<E> r;
-#pragma unroll
-    for (int e = 0; e < E; ++e) r.v[e] = fmaf(x.v[e], y.v[e], z.v[e]);
+    uint64_t q;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(q) : "f"(x.v[0]), "f"(x.v[1]));
+    return q;
+}
+__device__ __forceinline__ F<2> unpk(uint64_t q)
+{
+    F<2> r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.v[0]), "=f"(r.v[1]) : "l"(q));
     return r;
 }
-template <int E> __device__ __forceinline__ F<E> operator*(F<E> x, F<E> y)
+__device__ __forceinline__ F<1> fma(F<1> x, F<1> y, F<1> z) { return {{fmaf(x.v[0], y.v[0], z.v[0])}}; }
+__device__ __forceinline__ F<1> operator*(F<1> x, F<1> y) { return {{x.v[0] * y.v[0]}}; }
+__device__ __forceinline__ F<2> fma(F<2> x, F<2> y, F<2> z)
 {
-    F<E> r;
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pk(x)), "l"(pk(y)), "l"(pk(z)));
+    return unpk(r);
+}
+__device__ __forceinline__ F<2> operator*(F<2> x, F<2> y)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pk(x)), "l"(pk(y)));
+    return unpk(r);
+}
+template <int N> __device__ __forceinline__ F<N> all(float c)
+{
+    F<N> r;
 #pragma unroll
-    for (int e = 0; e < E; ++e) r.v[e] = x.v[e] * y.v[e];
+    for (int e = 0; e < N; ++e) r.v[e] = c;
     return r;
 }
-template <int E> __device__ __forceinline__ F<E> operator+(F<E> x, F<E> y)
+template <int N> __device__ __forceinline__ F<N> fmac(F<N> x, F<N> y, float c) { return fma(x, y, all<N>(c)); }   // x y + c
+// with a constant factor, plain instructions take it as an immediate
+template <int N> __device__ __forceinline__ F<N> fmac(F<N> x, float k, float c)
 {
-    F<E> r;
+    F<N> r;
 #pragma unroll
-    for (int e = 0; e < E; ++e) r.v[e] = x.v[e] + y.v[e];
+    for (int e = 0; e < N; ++e) r.v[e] = fmaf(x.v[e], k, c);
     return r;
 }
-// f of each channel
-template <int E, typename Fn> __device__ __forceinline__ F<E> each(F<E> x, Fn f)
+template <int N> __device__ __forceinline__ F<N> operator*(F<N> x, float k)
 {
-    float v[E];
-    x.get(v);
+    F<N> r;
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = f(v[e]);
-    return F<E>::of(v);
+    for (int e = 0; e < N; ++e) r.v[e] = x.v[e] * k;
+    return r;
 }
-template <int E, typename Fn> __device__ __forceinline__ F<E> each(F<E> x, F<E> y, Fn f)
+template <int N> __device__ __forceinline__ F<N> operator+(F<N> x, float k)
 {
-    float v[E], w[E];
-    x.get(v);
-    y.get(w);
+    F<N> r;
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = f(v[e], w[e]);
-    return F<E>::of(v);
+    for (int e = 0; e < N; ++e) r.v[e] = x.v[e] + k;
+    return r;
+}
+template <int N> __device__ __forceinline__ F<N> operator-(float k, F<N> x)
+{
+    F<N> r;
+#pragma unroll
+    for (int e = 0; e < N; ++e) r.v[e] = k - x.v[e];
+    return r;
+}
+// f of each
+template <int N, typename Fn> __device__ __forceinline__ F<N> each(F<N> x, Fn f)
+{
+#pragma unroll
+    for (int e = 0; e < N; ++e) x.v[e] = f(x.v[e]);
+    return x;
 }
 
-// e^-x; with TOP, held at 2^TOP from above, so that what is made of it stays finite (a NaN passes).
-template <int TOP, int E> __device__ __forceinline__ F<E> exp_minus(F<E> x)
-{
-    return each(x * F<E>::all(-kLog2e), [](float t) { return ex2(min_nan(t, (float)TOP)); });
-}
-template <int E> __device__ __forceinline__ F<E> exp_minus(F<E> x)
-{
-    return each(x * F<E>::all(-kLog2e), [](float t) { return ex2(t); });
-}
-template <int E> __device__ __forceinline__ F<E> rsq_of(F<E> x)
-{
-    return each(x, [](float t) { return rsq(t); });
-}
-template <int E> __device__ __forceinline__ F<E> rcp_of(F<E> x)
+template <int N> __device__ __forceinline__ F<N> rcp_of(F<N> x)
 {
     return each(x, [](float t) { return rcp(t); });
 }
+template <int N> __device__ __forceinline__ F<N> rsq_of(F<N> x)
+{
+    return each(x, [](float t) { return rsq(t); });
+}
+// e^-x
+template <int N> __device__ __forceinline__ F<N> exp_minus(F<N> x)
+{
+    return each(x * -kLog2e, [](float t) { return ex2(t); });
+}
+// e^-x, held at 2^TOP from above, so that what is made of it stays finite (a NaN passes)
+template <int TOP, int N> __device__ __forceinline__ F<N> exp_minus_held(F<N> x)
+{
+    return each(x * -kLog2e, [](float t) { return ex2(min_nan(t, (float)TOP)); });
+}
 
 // 1 - e^-y for 0 <= y <= 1/4: y sum_{k=0..6} (-y)^k / (k+1)!; the next term is below 2^-29 of it
-template <int E> __device__ __forceinline__ F<E> rest_series(F<E> y)
+constexpr float kSmall = 0.25f;
+template <int N> __device__ __forceinline__ F<N> rest_series(F<N> y)
 {
-    F<E> s = fma(y, F<E>::all(1.0f / 5040.0f), F<E>::all(-1.0f / 720.0f));
-    s = fma(s, y, F<E>::all(1.0f / 120.0f));
-    s = fma(s, y, F<E>::all(-1.0f / 24.0f));
-    s = fma(s, y, F<E>::all(1.0f / 6.0f));
-    s = fma(s, y, F<E>::all(-0.5f));
-    return fma(s, y, F<E>::all(1.0f)) * y;
+    F<N> s = fmac(y, 1.0f / 5040.0f, -1.0f / 720.0f);
+    s = fmac(s, y, 1.0f / 120.0f);
+    s = fmac(s, y, -1.0f / 24.0f);
+    s = fmac(s, y, 1.0f / 6.0f);
+    s = fmac(s, y, -0.5f);
+    return fmac(s, y, 1.0f) * y;
 }
-template <int E> __device__ __forceinline__ F<E> exp_neg(F<E> y)
+template <int N> __device__ __forceinline__ F<N> pick_small(F<N> y, F<N> small, F<N> large)
 {
-    return each(y * F<E>::all(-kLog2e), [](float t) { return ex2(t); });
-}
-template <int E> __device__ __forceinline__ F<E> pick_small(F<E> y, F<E> small, F<E> large)
-{
-    float t[E], p[E], q[E];
-    y.get(t);
-    small.get(p);
-    large.get(q);
 #pragma unroll
-    for (int e = 0; e < E; ++e) p[e] = t[e] < 0.25f ? p[e] : q[e];
-    return F<E>::of(p);
+    for (int e = 0; e < N; ++e) small.v[e] = y.v[e] < kSmall ? small.v[e] : large.v[e];
+    return small;
 }
 // 1 - a of a step with a = e^-y (a NaN passes), and a itself to its own last bit where it is small.
-template <int E> __device__ __forceinline__ F<E> rest_of(F<E> y)
+template <int N> __device__ __forceinline__ F<N> rest_of(F<N> y) { return pick_small(y, rest_series(y), 1.0f - exp_minus(y)); }
+template <int N> __device__ __forceinline__ void decay_of(F<N> y, F<N>& av, F<N>& rest)
 {
-    return pick_small(y, rest_series(y), fma(exp_neg(y), F<E>::all(-1.0f), F<E>::all(1.0f)));
-}
-template <int E> __device__ __forceinline__ void decay_of(F<E> y, F<E>& av, F<E>& rest)
-{
-    const F<E> r = rest_series(y), big = exp_neg(y), one = F<E>::all(1.0f), neg = F<E>::all(-1.0f);
-    rest = pick_small(y, r, fma(big, neg, one));
-    av = pick_small(y, fma(r, neg, one), big);
+    const F<N> r = rest_series(y), big = exp_minus(y);
+    rest = pick_small(y, r, 1.0f - big);
+    av = pick_small(y, 1.0f - r, big);
 }
 // 1 - a^2
-template <int E> __device__ __forceinline__ F<E> square_rest(F<E> rest)
-{
-    return rest * fma(rest, F<E>::all(-1.0f), F<E>::all(2.0f));
-}
+template <int N> __device__ __forceinline__ F<N> square_rest(F<N> rest) { return rest * (2.0f - rest); }
 
-// The map h -> A h + B of many steps as h -> (k h + (p h + B)): k = 1, p = A - 1 for A above 3/4, else k = 0, p = A.
-// A reset among the steps (y is inf) gives k = 0, p = -0: B alone for every finite h, and CUTS looks at p for the others.
-template <int E> struct Map {
-    F<E> p, k, b;
+// The map h -> A h + b of many steps as h -> (k h + (p h + b)): k = 1, p = A - 1 for A above 3/4, else k = 0, p = A.
+// A reset among the steps (y is inf) gives k = 0, p = -0: b alone for every finite h, and CUTS looks at p for the others.
+struct Map {
+    float p, k, b;
 };
-template <int E> __device__ __forceinline__ Map<E> map_of(F<E> y, F<E> B)
+__device__ __forceinline__ Map map_of(float y, float b)
 {
-    Map<E> m;
-    m.p = pick_small(y, fma(rest_series(y), F<E>::all(-1.0f), F<E>::all(0.0f)), exp_neg(y));      // never -0
-    m.p = each(m.p, y, [](float p, float t) { return t == INFINITY ? -0.0f : p; });
-    m.k = each(y, [](float t) { return t < 0.25f ? 1.0f : 0.0f; });
-    m.b = B;
+    Map m;
+    const F<1> s{{y}};
+    m.p = pick_small(s, 0.0f - rest_series(s), exp_minus(s)).v[0];       // never -0
+    m.p = y == INFINITY ? -0.0f : m.p;
+    m.k = y < kSmall ? 1.0f : 0.0f;
+    m.b = b;
     return m;
 }
-template <bool CUTS, int E> __device__ __forceinline__ F<E> apply(const Map<E>& m, F<E> h)
+template <bool CUTS> __device__ __forceinline__ float apply(const Map& m, float h)
 {
-    if (CUTS) h = each(m.p, h, [](float p, float x) { return __float_as_uint(p) == 0x80000000u ? 0.0f : x; });
-    return fma(m.k, h, fma(m.p, h, m.b));
+    if (CUTS && __float_as_uint(m.p) == 0x80000000u) h = 0.0f;
+    return fmaf(m.k, h, fmaf(m.p, h, m.b));
 }
 
 __device__ __forceinline__ float softplus_of(float d) { return fmaxf(d, 0.0f) + log1pf(expf(-fabsf(d))); }
@@ -255,53 +258,23 @@ __device__ __forceinline__ uint32_t peer_addr(uint32_t local, uint32_t rank)
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(local), "r"(rank));
     return d;
 }
-// 16, 8 or 4 bytes to another block's shared memory; its mbarrier counts them as they arrive.
+// 16 bytes to another block's shared memory; its mbarrier counts them as they arrive.
 __device__ __forceinline__ void st_async(uint32_t to, uint32_t bar, float4 v)
 {
     asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%2, %3, %4, %5}, [%1];" ::"r"(to),
                  "r"(bar), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
                  : "memory");
 }
-__device__ __forceinline__ void st_async(uint32_t to, uint32_t bar, float2 v)
-{
-    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%2, %3}, [%1];" ::"r"(to),
-                 "r"(bar), "f"(v.x), "f"(v.y)
-                 : "memory");
-}
-__device__ __forceinline__ void st_async(uint32_t to, uint32_t bar, float v)
-{
-    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.f32 [%0], %2, [%1];" ::"r"(to), "r"(bar), "f"(v)
-                 : "memory");
-}
 
-template <int E> struct Vecs;
-template <> struct Vecs<1> {
-    using One = float;
-    using Two = float2;
-};
-template <> struct Vecs<2> {
-    using One = float2;
-    using Two = float4;
-};
-__device__ __forceinline__ float one_of(F<1> x) { return x.v[0]; }
-__device__ __forceinline__ float2 one_of(F<2> x) { return make_float2(x.v[0], x.v[1]); }
-__device__ __forceinline__ F<1> of_one(float x) { return {{x}}; }
-__device__ __forceinline__ F<2> of_one(float2 x) { return {{x.x, x.y}}; }
-__device__ __forceinline__ float2 two_of(F<1> x, F<1> y) { return make_float2(x.v[0], y.v[0]); }
-__device__ __forceinline__ float4 two_of(F<2> x, F<2> y) { return make_float4(x.v[0], x.v[1], y.v[0], y.v[1]); }
-__device__ __forceinline__ Map<1> of_two(float2 t, float b) { return {{{t.x}}, {{t.y}}, {{b}}}; }
-__device__ __forceinline__ Map<2> of_two(float4 t, float2 b) { return {{{t.x, t.y}}, {{t.z, t.w}}, {{b.x, b.y}}}; }
-
-// Shared memory of the exchange, two sets used by turns: maps of the block's warps and their sums of y, maps of the
+// Shared memory of the exchange, two sets used by turns: maps of the block's warps with their sums of y, maps of the
 // cluster's blocks with the mbarrier that counts them.
-template <int E, int W, int CL> struct Meet {
-    typename Vecs<E>::Two pk[2][W][32], tot_pk[2][CL][32];
-    typename Vecs<E>::One b[2][W][32], len[2][W][32], tot_b[2][CL][32];
+template <int W, int CL> struct Meet {
+    float4 warp[2][W][32];           // p, k, b, y
+    float4 block[2][CL][32];         // p, k, b, -
     uint64_t full[2];
-    static constexpr uint32_t kMapBytes = 32 * 12 * E;
 };
 
-template <int E, int W, int CL> __device__ __forceinline__ void meet_init(Meet<E, W, CL>& s)
+template <int W, int CL> __device__ __forceinline__ void meet_init(Meet<W, CL>& s)
 {
     if constexpr (CL > 1) {
         if (threadIdx.x == 0) {
@@ -313,101 +286,78 @@ template <int E, int W, int CL> __device__ __forceinline__ void meet_init(Meet<E
     }
 }
 
-// Exchange of span n of the cluster: every thread gives its map (y, B); it gets the state that enters its steps, and
-// `run` moves past the whole span.  Position 0 comes first in the direction of the scan.  One block barrier a span: a
-// set is written again only two spans later, when all warps have passed the barrier in between, and a block's maps
-// for that span are sent only after it has the whole cluster's of the span in between.  A wait that gives up is
-// recorded; the walk goes on (its results are void) and ends.
-template <int E, int W, int CL> struct Walk {
-    Meet<E, W, CL>& s;
-    int set, lane;
-    // the block's warps `from` <= w < `to`
-    template <bool CUTS> __device__ __forceinline__ F<E> warps(int from, int to, F<E> h) const
-    {
+// The state past the maps from <= i < to.
+template <bool CUTS> __device__ __forceinline__ float pass(const float4 (*maps)[32], int from, int to, float h)
+{
+    const int lane = threadIdx.x & 31;
 #pragma unroll(CUTS ? 1 : 4)
-        for (int w = from; w < to; ++w) h = apply<CUTS>(of_two(s.pk[set][w][lane], s.b[set][w][lane]), h);
-        return h;
+    for (int i = from; i < to; ++i) {
+        const float4 q = maps[i][lane];
+        h = apply<CUTS>({q.x, q.y, q.z}, h);
     }
-    // the cluster's blocks
-    template <bool CUTS> __device__ __forceinline__ F<E> blocks(int from, int to, F<E> h) const
-    {
-#pragma unroll(CUTS ? 1 : 4)
-        for (int c = from; c < to; ++c) h = apply<CUTS>(of_two(s.tot_pk[set][c][lane], s.tot_b[set][c][lane]), h);
-        return h;
-    }
-    template <bool CUTS> __device__ __forceinline__ void states(int wpos, int cpos, F<E>& run, F<E>& in) const
-    {
-        if constexpr (CL > 1) {
-            in = blocks<CUTS>(0, cpos, run);
-            run = blocks<CUTS>(cpos, CL, in);
-            in = warps<CUTS>(0, wpos, in);
-        } else {
-            in = warps<CUTS>(0, wpos, run);
-            run = warps<CUTS>(wpos, W, in);
-        }
-    }
-};
+    return h;
+}
 
-// at_barrier runs right before the block's barrier, past_barrier right after it.
-template <int E, int W, int CL, typename At, typename Past>
-__device__ __forceinline__ F<E> exchange(Meet<E, W, CL>& s, int n, int wpos, int cpos, F<E> y, F<E> B, F<E>& run, bool cuts,
-                                         unsigned int* status, bool& waits, At at_barrier, Past past_barrier)
+// Exchange of span n of the cluster: every thread gives its map (y, b); it gets the state that enters its steps, and
+// `run` moves past the whole span.  Position 0 comes first in the direction of the scan.  One block barrier a span
+// (past_barrier runs right after it): a set is written again only two spans later, when all warps have passed the
+// barrier in between, and a block's maps for that span are sent only after it has the whole cluster's of the span in
+// between.  A wait that gives up is recorded; the walk goes on (its results are void) and ends.
+template <int W, int CL, typename Past>
+__device__ __forceinline__ float exchange(Meet<W, CL>& s, int n, int wpos, int cpos, float y, float b, float& run, bool cuts,
+                                          unsigned int* status, bool& waits, Past past_barrier)
 {
     const int lane = threadIdx.x & 31, set = n & 1;
-    const Map<E> m = map_of(y, B);
-    F<E> in = run;
+    const Map m = map_of(y, b);
+    float in = run;
     if constexpr (W * CL == 1) {
         run = apply<true>(m, run);
     } else {
-        const Walk<E, W, CL> walk{s, set, lane};
-        s.pk[set][wpos][lane] = two_of(m.p, m.k);
-        s.b[set][wpos][lane] = one_of(B);
-        if constexpr (CL > 1) s.len[set][wpos][lane] = one_of(y);
-        at_barrier();
+        s.warp[set][wpos][lane] = make_float4(m.p, m.k, b, y);
         __syncthreads();
         if constexpr (CL > 1) {
             if (wpos == 0) {
-                F<E> yt = F<E>::all(0.0f);
-                const F<E> bt = cuts ? walk.template warps<true>(0, W, yt) : walk.template warps<false>(0, W, yt);
+                const float bt = cuts ? pass<true>(s.warp[set], 0, W, 0.0f) : pass<false>(s.warp[set], 0, W, 0.0f);
+                float yt = 0.0f;
 #pragma unroll
-                for (int w = 0; w < W; ++w)              // a reset cuts off a NaN before it
-                    yt = each(yt, of_one(s.len[set][w][lane]), [](float t, float l) { return l == INFINITY ? l : t + l; });
-                const Map<E> t = map_of(yt, bt);
-                const uint32_t bar = smem_addr(&s.full[set]), pk = smem_addr(&s.tot_pk[set][cpos][lane]),
-                               bb = smem_addr(&s.tot_b[set][cpos][lane]);
-                if (lane == 0) mbar_arrive_expect_tx(bar, CL * s.kMapBytes);
-#pragma unroll
-                for (int c = 0; c < CL; ++c) {
-                    const uint32_t pb = peer_addr(bar, c);
-                    st_async(peer_addr(pk, c), pb, two_of(t.p, t.k));
-                    st_async(peer_addr(bb, c), pb, one_of(t.b));
+                for (int w = 0; w < W; ++w) {            // a reset cuts off a NaN before it
+                    const float l = s.warp[set][w][lane].w;
+                    yt = l == INFINITY ? l : yt + l;
                 }
+                const Map t = map_of(yt, bt);
+                const uint32_t bar = smem_addr(&s.full[set]), to = smem_addr(&s.block[set][cpos][lane]);
+                if (lane == 0) mbar_arrive_expect_tx(bar, CL * 32 * sizeof(float4));
+#pragma unroll
+                for (int c = 0; c < CL; ++c) st_async(peer_addr(to, c), peer_addr(bar, c), make_float4(t.p, t.k, t.b, 0.0f));
             }
         }
         past_barrier();
         if constexpr (CL > 1) {
             if (waits) waits = mbar_wait(smem_addr(&s.full[set]), (n >> 1) & 1, status);
         }
-        const F<E> first = run;
-        walk.template states<false>(wpos, cpos, run, in);
-        if (cuts) {
-            // A cut map is B + 0 h: right unless h is not finite.  Then (what comes out is a NaN) once more with care.
-            float t = 0.0f;
-#pragma unroll
-            for (int e = 0; e < E; ++e) t += run.v[e] + in.v[e];
-            if (__any_sync(0xffffffffu, t != t)) {
-                run = first;
-                walk.template states<true>(wpos, cpos, run, in);
+        const float first = run;
+        auto states = [&](auto careful) {
+            constexpr bool CUTS = decltype(careful)::value;
+            if constexpr (CL > 1) {
+                in = pass<CUTS>(s.block[set], 0, cpos, first);
+                run = pass<CUTS>(s.block[set], cpos, CL, in);
+                in = pass<CUTS>(s.warp[set], 0, wpos, in);
+            } else {
+                in = pass<CUTS>(s.warp[set], 0, wpos, first);
+                run = pass<CUTS>(s.warp[set], wpos, W, in);
             }
-        }
+        };
+        states(std::false_type{});
+        // A cut map is b + 0 h: right unless h is not finite.  Then (what comes out is a NaN) once more with care.
+        if (cuts && __any_sync(0xffffffffu, run + in != run + in)) states(std::true_type{});
     }
     return in;
 }
 
-// Where a thread stands: its block's unit is (sequence b, strip of channels).
-template <int E> struct Place {
-    int warp, rank, chans;           // chans: channels of this thread that exist (0..E)
-    int second;                      // where the second one is read from (a channel that exists)
+// Where a thread stands: its block's unit is (sequence b, strip of 32 channels).
+struct Place {
+    int warp, rank;
+    bool on;                         // its channel exists
     int64_t b, c, c0, read;          // c0: the strip's first channel; read: the channel that is read (c, or 0 beyond the last)
     __device__ __forceinline__ Place(const GlrArgs& a, int cl)
     {
@@ -415,453 +365,385 @@ template <int E> struct Place {
         rank = cl > 1 ? (int)cluster_rank() : 0;
         const int unit = blockIdx.x / cl;
         b = unit / a.strips;
-        c0 = (unit - b * a.strips) * (32 * E);
-        c = c0 + (threadIdx.x & 31) * E;
-        chans = (int)max((int64_t)0, min((int64_t)E, a.C - c));
-        read = chans > 0 ? c : 0;
-        second = chans > 1 ? 1 : 0;
-    }
-    // bytes from a span's first step to this thread's first step and channel
-    __device__ __forceinline__ uint32_t off(int64_t stride, int64_t first, int size) const
-    {
-        return (uint32_t)(((uint32_t)first * (uint32_t)stride + (uint32_t)read) * (uint32_t)size);
+        c0 = (unit - b * a.strips) * 32;
+        c = c0 + (threadIdx.x & 31);
+        on = c < a.C;
+        read = on ? c : 0;
     }
 };
 
-// Inputs straight to registers: a thread's S steps, element by element (rows need not be whole vectors).  A thread beyond
-// the last channel reads another one's (and stores nothing).
-template <typename T, int E, int S> struct Direct {
-    Pack<T, 1> q[S][E];
-    // p: the block's address (the same for all its threads) of the span's first step; off: this thread's bytes from it
-    template <bool FULL> __device__ __forceinline__ void load(const T* p, uint32_t off, int64_t stride, int live, int second)
+// An array's values at a thread's S steps, straight to registers (rows need not be whole vectors).  A thread beyond the
+// last channel reads another one's (and stores nothing).
+template <typename T, int S> struct Direct {
+    Pack<T, 1> q[S];
+    const T* from;                   // this thread's first value of the next span
+    int64_t stride, span;
+    __device__ __forceinline__ Direct(const T* p, int64_t stride, int64_t read, int64_t step, int64_t spans)
+        : from(p + step * stride + read), stride(stride), span(spans * stride) {}
+    __device__ __forceinline__ void load(int live)
     {
+        const T* at = from;
+        if (live == S) {
 #pragma unroll
-        for (int i = 0; i < S; ++i) {
-            const T* at = reinterpret_cast<const T*>(reinterpret_cast<const char*>(p + i * stride) + off);
+            for (int i = 0; i < S; ++i, at += stride) q[i] = Pack<T, 1>::load(at);
+        } else {
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                if (!FULL) q[i][e] = Pack<T, 1>::zero();
-                if (FULL || i < live) q[i][e] = Pack<T, 1>::load(at + (e ? second : 0));
+            for (int i = 0; i < S; ++i, at += stride) {
+                q[i] = Pack<T, 1>::zero();
+                if (i < live) q[i] = Pack<T, 1>::load(at);
             }
         }
-    }
-    __device__ __forceinline__ F<E> get(int i) const
-    {
-        F<E> r;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            float w[1];
-            q[i][e].unpack(w);
-            r.v[e] = w[0];
-        }
-        return r;
+        from += span;
     }
 };
 
-// Inputs through shared memory, two spans ahead, in 16-byte copies: the rows of a block's 64 steps of a strip are 128
-// bytes.  Thread k copies the chunk k % 8 of the rows k / 8 and k / 8 + 32 of each array.
-constexpr int kRowBytes = 128, kTileBytes = 8 * kSteps * kRowBytes;
-struct Copier {
+// Inputs through shared memory in 16-byte copies: a block's tile of an array is its 64 steps of the strip's 32 channels.
+// A tile is read before the exchange's barrier and filled with the next span's inputs after it.
+template <typename T> struct Tile {
+    static constexpr int kRow = 32 * (int)sizeof(T), kBytes = 8 * kSteps * kRow;
+    static constexpr int kChunks = kRow / 16, kRows = 256 / kChunks;     // chunks of a row; rows of one round of the block's copies
+};
+template <typename T> struct Copier {
     const char* from;                // this thread's chunk of the next span's tile
-    int64_t half, span;              // bytes to the row 32 further, to the next tile in the walk's direction
+    int64_t more, span;              // bytes to its row of the next round, to the next tile in the walk's direction
     // p: the array at the sequence's first step; step: the tile's first step; spans: steps to the next tile (may be negative)
-    template <typename T> __device__ __forceinline__ Copier(const T* p, int64_t stride, int64_t c0, int64_t step, int64_t spans)
+    __device__ __forceinline__ Copier(const T* p, int64_t stride, int64_t c0, int64_t step, int64_t spans)
     {
-        from = reinterpret_cast<const char*>(p + (step + (threadIdx.x >> 3)) * stride + c0) + (threadIdx.x & 7) * 16;
-        half = 32 * stride * (int64_t)sizeof(T);
+        using L = Tile<T>;
+        from = reinterpret_cast<const char*>(p + (step + threadIdx.x / L::kChunks) * stride + c0) + (threadIdx.x % L::kChunks) * 16;
+        more = L::kRows * stride * (int64_t)sizeof(T);
         span = spans * stride * (int64_t)sizeof(T);
     }
-    // rows and row 32 further: exist
-    __device__ __forceinline__ void copy(uint32_t to, bool row, bool further)
+    // left: steps from this thread's first row to the sequence's end (0 where its chunk lies beyond the channels)
+    __device__ __forceinline__ void copy(uint32_t to, int64_t left)
     {
-        if (row) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-        if (further) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 32 * kRowBytes), "l"(from + half) : "memory");
+        using L = Tile<T>;
+#pragma unroll
+        for (int j = 0; j < 8 * kSteps / L::kRows; ++j)
+            if (left > j * L::kRows)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + j * L::kRows * L::kRow), "l"(from + j * more) : "memory");
         from += span;
     }
 };
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
-template <typename T, int E> __device__ __forceinline__ F<E> staged(const char* tile, int row)
+template <typename T> __device__ __forceinline__ float value(Pack<T, 1> q)
 {
-    const Pack<T, E> q = Pack<T, E>::load(reinterpret_cast<const T*>(tile + row * kRowBytes) + (threadIdx.x & 31) * E);
-    float v[E];
+    float v[1];
     q.unpack(v);
-    return F<E>::of(v);
+    return v[0];
+}
+template <typename T> __device__ __forceinline__ void put(T* p, float x)
+{
+    const float v[1] = {x};
+    Pack<T, 1>::pack(v).store(p);
 }
 
-template <typename T, int LV, int E> __device__ __forceinline__ void store_step(T* p, F<E> x, int chans)
-{
-    float v[E];
-    x.get(v);
+// The input side of both kernels: NA arrays, staged or direct, one span ahead.
+template <typename T, bool STAGED, int S, int NA> struct Inputs {
+    std::conditional_t<STAGED, Copier<T>, Direct<T, S>> a[NA];
+    uint32_t place;                  // where this thread copies to
+    int64_t row;                     // the sequence's step of its first copied row in the span at step 0; beyond the end: no chunk
+    int first;                       // the shared row of this thread's first step
+    const char* tiles;
+    __device__ __forceinline__ void load(int64_t base, int64_t T_, int live)
+    {
+        if constexpr (STAGED) {
 #pragma unroll
-    for (int j = 0; j < E / LV; ++j) {
-        if (j * LV < chans) {
-            float w[LV];
+            for (int i = 0; i < NA; ++i) a[i].copy(place + i * Tile<T>::kBytes, T_ - base - row);
+            copies_commit();
+        } else {
 #pragma unroll
-            for (int e = 0; e < LV; ++e) w[e] = v[j * LV + e];
-            Pack<T, LV>::pack(w).store(p + j * LV);
+            for (int i = 0; i < NA; ++i) a[i].load(live);
         }
     }
-}
-template <int E> __device__ __forceinline__ F<E> load_f32(const float* p, int chans)
-{
-    float v[E];
+    // before the values of a span are used
+    __device__ __forceinline__ void ready()
+    {
+        if constexpr (STAGED) {
+            copies_wait();
+            __syncthreads();
+        }
+    }
+    __device__ __forceinline__ Pack<T, 1> raw(int array, int i) const
+    {
+        if constexpr (STAGED)
+            return Pack<T, 1>::load(reinterpret_cast<const T*>(tiles + array * Tile<T>::kBytes + (first + i) * Tile<T>::kRow) + (threadIdx.x & 31));
+        else
+            return a[array].q[i];
+    }
+    template <int N> __device__ __forceinline__ F<N> get(int array, int i) const
+    {
+        F<N> r;
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = e < chans ? p[e] : 0.0f;
-    return F<E>::of(v);
-}
-template <int E> __device__ __forceinline__ void store_f32(float* p, F<E> x, int chans)
-{
-    float v[E];
-    x.get(v);
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        if (e < chans) p[e] = v[e];
-}
+        for (int e = 0; e < N; ++e) r.v[e] = value(raw(array, i + e));
+        return r;
+    }
+};
 // Forward: S steps a thread, W warps a block, CL blocks a cluster; STAGED: inputs through shared memory (W = 8), else
 // into registers.
 template <typename T, bool STAGED, int S, int W, int CL>
-__global__ void __launch_bounds__(32 * W, W == 8 ? (STAGED ? (sizeof(T) == 2 ? 3 : 4) : 2) : 1) glr_forward_kernel(const GlrArgs a)
+__global__ void __launch_bounds__(32 * W, W == 8 ? (STAGED ? 4 : 3) : 1) glr_forward_kernel(const GlrArgs a)
 {
-    constexpr int E = 4 / (int)sizeof(T);
-    constexpr int LV = STAGED ? E : 1;
-    extern __shared__ __align__(128) char tiles[];       // STAGED: [2][r, g, x] tiles
-    __shared__ Meet<E, W, CL> meet;
-    const Place<E> at(a, CL);
+    constexpr int N = S > 1 ? 2 : 1;                     // steps side by side
+    extern __shared__ __align__(128) char tiles[];       // STAGED: r, g, x
+    __shared__ Meet<W, CL> meet;
+    const Place at(a, CL);
     constexpr int64_t SPAN = (int64_t)S * W * CL;
     const int64_t mine = (int64_t)at.rank * W * S, first = mine + at.warp * S;   // the block's and the thread's first step
-    const int chans = at.chans;
     const int64_t state = at.b * a.C + at.c;
     const T* X = reinterpret_cast<const T*>(a.x) + at.b * a.xb;
     const T* R = reinterpret_cast<const T*>(a.r) + at.b * a.rb;
     const T* G = reinterpret_cast<const T*>(a.g) + at.b * a.gb;
-    T* Y = reinterpret_cast<T*>(a.y) + (at.b * a.T + first) * a.C + at.c;      // this thread's first output of the span
-    const unsigned char* Z = a.reset ? a.reset + at.b * a.T : nullptr;
+    T* Y = reinterpret_cast<T*>(a.y) + (at.b * a.T + first) * a.C + at.c;        // this thread's first output of the span
+    const unsigned char* Z = a.reset ? a.reset + at.b * a.T + first : nullptr;
     float* K = a.kept ? a.kept + (at.b * ((a.T + kSteps - 1) / kSteps) + first / kSteps) * a.C + at.c : nullptr;
-
-    const F<E> lambda = each(load_f32<E>(a.decay + at.c, chans), [](float d) { return softplus_of(d); });
-    const F<E> one = F<E>::all(1.0f), zero = F<E>::all(0.0f), neg = F<E>::all(-1.0f);
-    F<E> run = a.h0 ? load_f32<E>(a.h0 + state, chans) : zero;
-    Direct<T, E, STAGED ? 1 : S> qx, qr, qg;
-    Copier cr(R, a.rt, at.c0, mine, SPAN), cg(G, a.gt, at.c0, mine, SPAN), cx(X, a.xt, at.c0, mine, SPAN);
-    const bool chunk = at.c0 + (threadIdx.x & 7) * (16 / (int)sizeof(T)) < a.C;      // a chunk that this thread copies exists
-    const uint32_t place = smem_addr(tiles) + threadIdx.x * 16;
+    const float lambda = at.on ? softplus_of(a.decay[at.c]) : 0.0f;
+    float run = a.h0 && at.on ? a.h0[state] : 0.0f;
     const int lane = threadIdx.x & 31;
+
+    const int64_t step = STAGED ? mine : first, col = STAGED ? at.c0 : at.read;
+    Inputs<T, STAGED, S, 3> in{{{R, a.rt, col, step, SPAN}, {G, a.gt, col, step, SPAN}, {X, a.xt, col, step, SPAN}}};
+    in.place = smem_addr(tiles) + threadIdx.x * 16;
+    in.row = at.c0 + threadIdx.x % Tile<T>::kChunks * (16 / (int)sizeof(T)) < a.C ? mine + threadIdx.x / Tile<T>::kChunks : a.T;
+    in.first = at.warp * S;
+    in.tiles = tiles;
     unsigned char zb = 0;                                // the reset byte of this lane's step of the next span
-    auto fetch = [&](int64_t base, int set) {
+    auto fetch = [&](int64_t base) {
         const int live = (int)min((int64_t)S, max((int64_t)0, a.T - base - first));
-        if (Z) zb = lane < live ? Z[base + first + lane] : 0;
-        if constexpr (STAGED) {
-            const int64_t left = a.T - base - mine - (threadIdx.x >> 3);
-            const bool r0 = chunk && left > 0, r1 = chunk && left > 32;
-            const uint32_t tile = place + set * 3 * kTileBytes;
-            cr.copy(tile, r0, r1);
-            cg.copy(tile + kTileBytes, r0, r1);
-            cx.copy(tile + 2 * kTileBytes, r0, r1);
-            copies_commit();
-        } else if (live == S) {
-            qr.template load<true>(R + base * a.rt, at.off(a.rt, first, sizeof(T)), a.rt, S, at.second);
-            qg.template load<true>(G + base * a.gt, at.off(a.gt, first, sizeof(T)), a.gt, S, at.second);
-            qx.template load<true>(X + base * a.xt, at.off(a.xt, first, sizeof(T)), a.xt, S, at.second);
-        } else {
-            qr.template load<false>(R + base * a.rt, at.off(a.rt, first, sizeof(T)), a.rt, live, at.second);
-            qg.template load<false>(G + base * a.gt, at.off(a.gt, first, sizeof(T)), a.gt, live, at.second);
-            qx.template load<false>(X + base * a.xt, at.off(a.xt, first, sizeof(T)), a.xt, live, at.second);
+        if (Z) {
+            zb = lane < live ? Z[lane] : 0;
+            Z += SPAN;
         }
+        in.load(base, a.T, live);
     };
     meet_init(meet);
     bool waits = true;
-    unsigned char zb_now;
-    fetch(0, 0);
-    zb_now = zb;
-    if constexpr (STAGED) {
-        fetch(SPAN, 1);                                  // (nothing beyond the end)
-        copies_wait<1>();
-        __syncthreads();
-    }
+    fetch(0);
 
     int n = 0;
     for (int64_t base = 0; base < a.T; base += SPAN, ++n) {
         const int live = (int)min((int64_t)S, max((int64_t)0, a.T - base - first));
-        const uint32_t cuts = Z ? __ballot_sync(0xffffffffu, zb_now != 0) : 0;
-        const char* tile = tiles + (n & 1) * 3 * kTileBytes;
-        auto in_r = [&](int i) { return STAGED ? staged<T, E>(tile, at.warp * S + i) : qr.get(STAGED ? 0 : i); };
-        auto in_g = [&](int i) { return STAGED ? staged<T, E>(tile + kTileBytes, at.warp * S + i) : qg.get(STAGED ? 0 : i); };
-        auto in_x = [&](int i) { return STAGED ? staged<T, E>(tile + 2 * kTileBytes, at.warp * S + i) : qx.get(STAGED ? 0 : i); };
-        F<E> fa[S], bb[S], len = zero, B = zero;
+        const uint32_t cuts = a.reset ? __ballot_sync(0xffffffffu, zb != 0) : 0;
+        in.ready();
+        float fa[S], bb[S], len = 0.0f, B = 0.0f;
 #pragma unroll
-        for (int i = 0; i < S; ++i) {
-            const F<E> y = rcp_of(one + exp_minus(in_r(i))) * lambda;
-            const F<E> rest = rest_of(y), m2 = square_rest(rest);
+        for (int i = 0; i < S; i += N) {
+            const F<N> y = rcp_of(exp_minus(in.template get<N>(0, i)) + 1.0f) * lambda;
+            const F<N> rest = rest_of(y), m2 = square_rest(rest);
             // m sigmoid(g) = m^2 / sqrt(m^2 (1 + e)^2) with e = exp(-g): one rsqrt, held where m is 0
-            const F<E> q = one + exp_minus<60>(in_g(i));
-            bb[i] = m2 * rsq_of(fma(m2 * q, q, F<E>::all(kTiny))) * in_x(i);
-            fa[i] = one + rest * neg;
-            len = len + y;
-            B = fma(fa[i], B, bb[i]);
+            const F<N> q = exp_minus_held<60>(in.template get<N>(1, i)) + 1.0f;
+            const F<N> b = m2 * rsq_of(fmac(m2 * q, q, kTiny)) * in.template get<N>(2, i), f = 1.0f - rest;
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                fa[i + e] = f.v[e];
+                bb[i + e] = b.v[e];
+                len += y.v[e];
+                B = fmaf(f.v[e], B, b.v[e]);
+            }
         }
         if (live < S) {                                  // past the end: a = 1, nothing comes in
-            len = B = zero;
+            len = B = 0.0f;
 #pragma unroll
             for (int i = 0; i < S; ++i) {
                 if (i < live) {
-                    len = len + rcp_of(one + exp_minus(in_r(i))) * lambda;
-                    B = fma(fa[i], B, bb[i]);
+                    len += (rcp_of(exp_minus(in.template get<1>(0, i)) + 1.0f) * lambda).v[0];
+                    B = fmaf(fa[i], B, bb[i]);
                 }
             }
         }
-        if (!STAGED && base + SPAN < a.T) fetch(base + SPAN, 0);
-        zb_now = zb;
+        if (!STAGED && base + SPAN < a.T) fetch(base + SPAN);
         if (cuts) {                                      // resets among the steps: they cut off what comes before them
-            B = zero;
-            len = F<E>::all(INFINITY);
+            B = 0.0f;
+            len = INFINITY;
 #pragma unroll
             for (int i = 0; i < S; ++i) {
-                if (cuts >> i & 1) B = zero;
-                if (i < live) B = fma(fa[i], B, bb[i]);
+                if (cuts >> i & 1) B = 0.0f;
+                if (i < live) B = fmaf(fa[i], B, bb[i]);
             }
         }
-        F<E> h = exchange<E, W, CL>(
-            meet, n, at.warp, at.rank, len, B, run, Z != nullptr, a.status, waits,
-            [&] {
-                if constexpr (STAGED) copies_wait<0>();  // the next span's inputs, before the barrier
-            },
-            [&] {
-                if constexpr (STAGED)                    // all warps have read this span's tiles
-                    if (base + 2 * SPAN < a.T) fetch(base + 2 * SPAN, n & 1);
-            });
+        float h = exchange<W, CL>(meet, n, at.warp, at.rank, len, B, run, a.reset != nullptr, a.status, waits, [&] {
+            if constexpr (STAGED)                        // all warps have read this span's tiles
+                if (base + SPAN < a.T) fetch(base + SPAN);
+        });
         if (K) {
-            if (live > 0) store_f32<E>(K, h, chans);
+            if (live > 0 && at.on) *K = h;
             K += SPAN / kSteps * a.C;
         }
-        if (live == S && !cuts) {
-            if (chans > 0) {
-                T* y = Y;
+        if (at.on) {
+            T* y = Y;
+            if (live == S && !cuts) {
 #pragma unroll
                 for (int i = 0; i < S; ++i) {
-                    h = fma(fa[i], h, bb[i]);
-                    store_step<T, LV, E>(y, h, STAGED ? E : chans);
+                    h = fmaf(fa[i], h, bb[i]);
+                    put(y, h);
                     y += a.C;
                 }
-            }
-        } else {
-            T* y = Y;
+            } else {
 #pragma unroll
-            for (int i = 0; i < S; ++i) {
-                if (cuts >> i & 1) h = zero;
-                h = fma(fa[i], h, bb[i]);
-                if (i < live) store_step<T, LV, E>(y, h, chans);
-                y += a.C;
+                for (int i = 0; i < S; ++i) {
+                    if (cuts >> i & 1) h = 0.0f;
+                    h = fmaf(fa[i], h, bb[i]);
+                    if (i < live) put(y, h);
+                    y += a.C;
+                }
             }
         }
         Y += SPAN * a.C;
     }
-    if (a.h_last && at.rank == 0 && at.warp == 0) store_f32<E>(a.h_last + state, run, chans);
+    if (a.h_last && at.on && at.rank == 0 && at.warp == 0) a.h_last[state] = run;
 }
 
 // Backward: the same split, walked from the end of the sequence.
 template <typename T, bool STAGED, int W, int CL>
-__global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_backward_kernel(const GlrArgs a)
+__global__ void __launch_bounds__(32 * W, W == 8 ? (STAGED ? 3 : 2) : 1) glr_backward_kernel(const GlrArgs a)
 {
-    constexpr int S = kSteps;                            // a thread's steps begin at a kept state
-    constexpr int E = 4 / (int)sizeof(T);
-    constexpr int LV = STAGED ? E : 1;
-    extern __shared__ __align__(128) char tiles[];       // STAGED: [2][r, g, x, dy] tiles
-    __shared__ Meet<E, W, CL> meet;
-    const Place<E> at(a, CL);
+    constexpr int S = kSteps, N = 2;                     // a thread's steps begin at a kept state
+    extern __shared__ __align__(128) char tiles[];       // STAGED: r, g, x, dy
+    __shared__ Meet<W, CL> meet;
+    const Place at(a, CL);
     constexpr int64_t SPAN = (int64_t)S * W * CL;
     const int64_t mine = (int64_t)at.rank * W * S, first = mine + at.warp * S;
-    const int chans = at.chans;
-    const int64_t state = at.b * a.C + at.c, end = (a.T - 1) / SPAN * SPAN;       // end: the last span's first step
+    const int64_t state = at.b * a.C + at.c, end = (a.T - 1) / SPAN * SPAN;      // end: the last span's first step
     const T* X = reinterpret_cast<const T*>(a.x) + at.b * a.xb;
     const T* R = reinterpret_cast<const T*>(a.r) + at.b * a.rb;
     const T* G = reinterpret_cast<const T*>(a.g) + at.b * a.gb;
     const T* D = reinterpret_cast<const T*>(a.dy) + at.b * a.T * a.C;
-    const unsigned char* Z = a.reset ? a.reset + at.b * a.T : nullptr;
-    const float* K = a.kept + (at.b * ((a.T + kSteps - 1) / kSteps) + (end + first) / kSteps) * a.C + at.c;
-    int64_t out = (at.b * a.T + end + first) * a.C + at.c;                        // this thread's first output of the span
-
-    const F<E> lambda = each(load_f32<E>(a.decay + at.c, chans), [](float d) { return softplus_of(d); });
-    const F<E> one = F<E>::all(1.0f), zero = F<E>::all(0.0f), neg = F<E>::all(-1.0f);
-    F<E> run = a.dh_last ? load_f32<E>(a.dh_last + state, chans) : zero;
-    double acc[E];                                       // sum of dL L
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.0;
-    Copier cr(R, a.rt, at.c0, end + mine, -SPAN), cg(G, a.gt, at.c0, end + mine, -SPAN), cx(X, a.xt, at.c0, end + mine, -SPAN),
-        cd(D, a.C, at.c0, end + mine, -SPAN);
-    const bool chunk = at.c0 + (threadIdx.x & 7) * (16 / (int)sizeof(T)) < a.C;
-    const uint32_t place = smem_addr(tiles) + threadIdx.x * 16;
+    const unsigned char* Z = a.reset ? a.reset + at.b * a.T + end + first : nullptr;
+    const float* K = a.kept + (at.b * ((a.T + kSteps - 1) / kSteps) + (end + first) / kSteps) * a.C + at.read;
+    int64_t out = (at.b * a.T + end + first) * a.C + at.c;                       // this thread's first output of the span
+    const float lambda = at.on ? softplus_of(a.decay[at.c]) : 0.0f;
+    float run = a.dh_last && at.on ? a.dh_last[state] : 0.0f;
+    double acc = 0.0;                                    // sum of dL L
     const int lane = threadIdx.x & 31;
+
+    const int64_t step = end + (STAGED ? mine : first), col = STAGED ? at.c0 : at.read;
+    Inputs<T, STAGED, S, 4> in{{{R, a.rt, col, step, -SPAN}, {G, a.gt, col, step, -SPAN}, {X, a.xt, col, step, -SPAN}, {D, a.C, col, step, -SPAN}}};
+    in.place = smem_addr(tiles) + threadIdx.x * 16;
+    in.row = at.c0 + threadIdx.x % Tile<T>::kChunks * (16 / (int)sizeof(T)) < a.C ? mine + threadIdx.x / Tile<T>::kChunks : a.T;
+    in.first = at.warp * S;
+    in.tiles = tiles;
     unsigned char zb = 0;                                // reset byte of this lane's step, and the kept state, of the next span
-    F<E> hb = F<E>::all(0.0f);
-    auto copy = [&](int64_t base, int set) {
-        const int64_t left = a.T - base - mine - (threadIdx.x >> 3);
-        const bool r0 = chunk && left > 0, r1 = chunk && left > 32;
-        const uint32_t tile = place + set * 4 * kTileBytes;
-        cr.copy(tile, r0, r1);
-        cg.copy(tile + kTileBytes, r0, r1);
-        cx.copy(tile + 2 * kTileBytes, r0, r1);
-        cd.copy(tile + 3 * kTileBytes, r0, r1);
-        copies_commit();
-    };
-    auto ahead = [&](int64_t base) {                     // called once for each span, in the walk's order
+    float hb = 0.0f;
+    auto fetch = [&](int64_t base) {
         const int live = (int)min((int64_t)S, max((int64_t)0, a.T - base - first));
-        if (Z) zb = lane < live ? Z[base + first + lane] : 0;
-        if (live > 0) hb = load_f32<E>(K, chans);
+        if (Z) {
+            zb = lane < live ? Z[lane] : 0;
+            Z -= SPAN;
+        }
+        if (live > 0) hb = *K;
         K -= SPAN / kSteps * a.C;
+        in.load(base, a.T, live);
     };
     meet_init(meet);
     bool waits = true;
-    ahead(end);
-    if constexpr (STAGED) {
-        copy(end, 0);
-        if (end >= SPAN) copy(end - SPAN, 1);
-        else copies_commit();
-        copies_wait<1>();
-        __syncthreads();
-    }
+    fetch(end);
 
     int n = 0;
     for (int64_t base = end; base >= 0; base -= SPAN, ++n) {
         const int live = (int)min((int64_t)S, max((int64_t)0, a.T - base - first));
-        Direct<T, E, STAGED ? 1 : S> qx, qr, qg, qd;
-        if constexpr (!STAGED) {
-            if (live == S) {
-                qr.template load<true>(R + base * a.rt, at.off(a.rt, first, sizeof(T)), a.rt, S, at.second);
-                qg.template load<true>(G + base * a.gt, at.off(a.gt, first, sizeof(T)), a.gt, S, at.second);
-                qx.template load<true>(X + base * a.xt, at.off(a.xt, first, sizeof(T)), a.xt, S, at.second);
-                qd.template load<true>(D + base * a.C, at.off(a.C, first, sizeof(T)), a.C, S, at.second);
-            } else {
-                qr.template load<false>(R + base * a.rt, at.off(a.rt, first, sizeof(T)), a.rt, live, at.second);
-                qg.template load<false>(G + base * a.gt, at.off(a.gt, first, sizeof(T)), a.gt, live, at.second);
-                qx.template load<false>(X + base * a.xt, at.off(a.xt, first, sizeof(T)), a.xt, live, at.second);
-                qd.template load<false>(D + base * a.C, at.off(a.C, first, sizeof(T)), a.C, live, at.second);
-            }
-        }
-        const char* tile = tiles + (n & 1) * 4 * kTileBytes;
-        auto in_r = [&](int i) { return STAGED ? staged<T, E>(tile, at.warp * S + i) : qr.get(STAGED ? 0 : i); };
-        auto in_g = [&](int i) { return STAGED ? staged<T, E>(tile + kTileBytes, at.warp * S + i) : qg.get(STAGED ? 0 : i); };
-        auto in_x = [&](int i) { return STAGED ? staged<T, E>(tile + 2 * kTileBytes, at.warp * S + i) : qx.get(STAGED ? 0 : i); };
-        Pack<T, E> dy[S];                                // (kept packed: the tile is free after the exchange's barrier)
-#pragma unroll
-        for (int i = 0; i < S; ++i) {
-            if constexpr (STAGED) {
-                dy[i] = i < live ? Pack<T, E>::load(reinterpret_cast<const T*>(tile + 3 * kTileBytes + (at.warp * S + i) * kRowBytes) + (threadIdx.x & 31) * E)
-                                 : Pack<T, E>::zero();
-            } else {
-                float v[E];
-                qd.get(STAGED ? 0 : i).get(v);
-                dy[i] = Pack<T, E>::pack(v);
-            }
-        }
-        auto in_d = [&](int i) {
-            float v[E];
-            dy[i].unpack(v);
-            return F<E>::of(v);
-        };
-        const uint32_t cut = Z ? __ballot_sync(0xffffffffu, zb != 0) : 0;
-        F<E> h = hb;
-        if (base > 0) ahead(base - SPAN);
+        const uint32_t cut = a.reset ? __ballot_sync(0xffffffffu, zb != 0) : 0;
+        in.ready();
+        float h = hb;
         // per step: the factor, and what d multiplies in each gradient:
-        //   dx = d cx_,  dg = dx cg_,  dL L = d cl,  dr = dL L cr_
-        F<E> fa[S], cx_[S], cg_[S], cl[S], cr_[S], len = zero, B = zero;
+        //   dx = d cx,  dg = dx cg,  dL L = d cl,  dr = dL L cr
+        float fa[S], cx[S], cg[S], cl[S], cr[S], dy[S], len = 0.0f, B = 0.0f;
 #pragma unroll
-        for (int i = 0; i < S; ++i) {
-            const F<E> er = exp_minus<115>(in_r(i)), eg = exp_minus<115>(in_g(i));
-            const F<E> s = rcp_of(one + er), sg = rcp_of(one + eg), x = in_x(i);
-            const F<E> y = s * lambda;
-            F<E> rest;
-            decay_of(y, fa[i], rest);
+        for (int i = 0; i < S; i += N) {
+            const F<N> er = exp_minus_held<115>(in.template get<N>(0, i)), eg = exp_minus_held<115>(in.template get<N>(1, i));
+            const F<N> s = rcp_of(er + 1.0f), sg = rcp_of(eg + 1.0f), x = in.template get<N>(2, i);
+            const F<N> y = s * lambda;
+            F<N> av, rest;
+            decay_of(y, av, rest);
             // 1 / m, held where m is 0 (there y is 0 too, and y / m goes to 0 with it)
-            const F<E> m2 = square_rest(rest), rm = rsq_of(m2 + F<E>::all(kTiny));
-            cx_[i] = m2 * rm * sg;
-            cg_[i] = x * (eg * sg);
-            cr_[i] = er * s;
-            if (cut && cut >> i & 1) h = zero;
-            // a L (h - a u / m), L = -y
-            cl[i] = fa[i] * y * fma(fa[i] * rm, sg * x, h * neg);
-            h = fma(fa[i], h, cx_[i] * x);
-            len = len + y;
+            const F<N> m2 = square_rest(rest), rm = rsq_of(m2 + kTiny), w = m2 * rm * sg, b = w * x;
+            const F<N> xg = x * (eg * sg), rr = er * s, ay = av * y, au = av * rm * (sg * x);
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                if (cut && cut >> (i + e) & 1) h = 0.0f;
+                fa[i + e] = av.v[e];
+                cx[i + e] = w.v[e];
+                cg[i + e] = xg.v[e];
+                cr[i + e] = rr.v[e];
+                cl[i + e] = ay.v[e] * (au.v[e] - h);     // a L (h - a u / m), L = -y
+                h = fmaf(av.v[e], h, b.v[e]);
+                len += y.v[e];
+            }
         }
-        if (live < S) {                                  // past the end: gamma passes (dy is 0 there)
-            len = zero;
+#pragma unroll
+        for (int i = 0; i < S; ++i) dy[i] = value(in.raw(3, i));
+        if (live < S) {                                  // past the end: gamma passes
+            len = 0.0f;
 #pragma unroll
             for (int i = 0; i < S; ++i) {
-                if (i < live) len = len + rcp_of(one + exp_minus<115>(in_r(i))) * lambda;
-                else fa[i] = one;
+                if (i < live) {
+                    len += (rcp_of(exp_minus_held<115>(in.template get<1>(0, i)) + 1.0f) * lambda).v[0];
+                } else {
+                    fa[i] = 1.0f;
+                    dy[i] = 0.0f;
+                }
             }
         }
         // the map of these steps, from the last to the first: gamma -> a (gamma + dy)
 #pragma unroll
-        for (int i = S - 1; i >= 0; --i) B = fa[i] * (B + in_d(i));
+        for (int i = S - 1; i >= 0; --i) B = fa[i] * (B + dy[i]);
         if (cut) {
-            B = zero;
+            B = 0.0f;
 #pragma unroll
             for (int i = S - 1; i >= 0; --i) {
-                B = fa[i] * (B + in_d(i));
-                if (cut >> i & 1) B = zero;
+                B = fa[i] * (B + dy[i]);
+                if (cut >> i & 1) B = 0.0f;
             }
-            len = F<E>::all(INFINITY);
+            len = INFINITY;
         }
-        F<E> flow = exchange<E, W, CL>(
-            meet, n, W - 1 - at.warp, CL - 1 - at.rank, len, B, run, Z != nullptr, a.status, waits,
-            [&] {
-                if constexpr (STAGED) copies_wait<0>();
-            },
-            [&] {
-                if constexpr (STAGED)
-                    if (base >= 2 * SPAN) copy(base - 2 * SPAN, n & 1);
-            });
-        F<E> part = zero;
-        T *ox = reinterpret_cast<T*>(a.dx) + out + S * a.C, *orr = reinterpret_cast<T*>(a.dr) + out + S * a.C,
-          *og = reinterpret_cast<T*>(a.dg) + out + S * a.C;
-        if (live == S && !cut) {
-            if (chans > 0) {
+        if (!STAGED && base > 0) fetch(base - SPAN);
+        float flow = exchange<W, CL>(meet, n, W - 1 - at.warp, CL - 1 - at.rank, len, B, run, a.reset != nullptr, a.status, waits, [&] {
+            if constexpr (STAGED)
+                if (base > 0) fetch(base - SPAN);
+        });
+        float part = 0.0f;
+        if (at.on) {
+            T *ox = reinterpret_cast<T*>(a.dx) + out, *orr = reinterpret_cast<T*>(a.dr) + out, *og = reinterpret_cast<T*>(a.dg) + out;
+            const uint32_t step_bytes = (uint32_t)a.C * (uint32_t)sizeof(T);
+            auto row = [&](T* p, int i) { return reinterpret_cast<T*>(reinterpret_cast<char*>(p) + (uint64_t)step_bytes * (uint32_t)i); };
+            if (live == S && !cut) {
 #pragma unroll
                 for (int i = S - 1; i >= 0; --i) {
-                    const F<E> d = flow + in_d(i), gx = d * cx_[i], gl = d * cl[i];
+                    const float d = flow + dy[i], gx = d * cx[i], gl = d * cl[i];
                     flow = fa[i] * d;
-                    part = part + gl;
-                    ox -= a.C, orr -= a.C, og -= a.C;
-                    if (a.dx) store_step<T, LV, E>(ox, gx, STAGED ? E : chans);
-                    if (a.dr) store_step<T, LV, E>(orr, gl * cr_[i], STAGED ? E : chans);
-                    if (a.dg) store_step<T, LV, E>(og, gx * cg_[i], STAGED ? E : chans);
+                    part += gl;
+                    if (a.dx) put(row(ox, i), gx);
+                    if (a.dr) put(row(orr, i), gl * cr[i]);
+                    if (a.dg) put(row(og, i), gx * cg[i]);
                 }
-            }
-        } else {
+            } else {
 #pragma unroll
-            for (int i = S - 1; i >= 0; --i) {
-                const F<E> d = flow + in_d(i), gx = d * cx_[i], gl = d * cl[i];
-                flow = fa[i] * d;
-                if (cut >> i & 1) flow = zero;
-                ox -= a.C, orr -= a.C, og -= a.C;
-                if (i < live) {
-                    part = part + gl;
-                    if (a.dx) store_step<T, LV, E>(ox, gx, chans);
-                    if (a.dr) store_step<T, LV, E>(orr, gl * cr_[i], chans);
-                    if (a.dg) store_step<T, LV, E>(og, gx * cg_[i], chans);
+                for (int i = S - 1; i >= 0; --i) {
+                    const float d = flow + dy[i], gx = d * cx[i], gl = d * cl[i];
+                    flow = fa[i] * d;
+                    if (cut >> i & 1) flow = 0.0f;
+                    if (i < live) {
+                        part += gl;
+                        if (a.dx) put(row(ox, i), gx);
+                        if (a.dr) put(row(orr, i), gl * cr[i]);
+                        if (a.dg) put(row(og, i), gx * cg[i]);
+                    }
                 }
             }
         }
         out -= SPAN * a.C;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] += (double)part.v[e];
+        acc += (double)part;
     }
-    if (a.dh0 && at.rank == 0 && at.warp == 0) store_f32<E>(a.dh0 + state, run, chans);
+    if (a.dh0 && at.on && at.rank == 0 && at.warp == 0) a.dh0[state] = run;
     if (a.part) {
-        __shared__ double red[W][E][32];
-        const int lane = threadIdx.x & 31;
-#pragma unroll
-        for (int e = 0; e < E; ++e) red[at.warp][e][lane] = acc[e];
+        __shared__ double red[W][32];
+        red[at.warp][lane] = acc;
         __syncthreads();
-        if (at.warp == 0) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                double v = 0.0;
-                for (int w = 0; w < W; ++w) v += red[w][e][lane];
-                if (e < chans) a.part[(at.b * CL + at.rank) * a.C + at.c + e] = v;
-            }
+        if (at.warp == 0 && at.on) {
+            double v = 0.0;
+            for (int w = 0; w < W; ++w) v += red[w][lane];
+            a.part[(at.b * CL + at.rank) * a.C + at.c] = v;
         }
     }
 }
@@ -906,7 +788,9 @@ template <typename K> int resident(K kernel, int warps, int cluster, size_t smem
     int n = known[dev].load(std::memory_order_relaxed);
     if (n) return n;
     cudaLaunchConfig_t cfg{};
-    if (smem && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return 0;
+    if ((smem && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) ||
+        (cluster > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess))
+        return 0;
     cfg.gridDim = dim3(cluster);
     cfg.blockDim = dim3(32 * warps);
     cfg.dynamicSmemBytes = smem;
@@ -942,32 +826,40 @@ template <typename K> cudaError_t launch(K kernel, int warps, int cluster, size_
     return e;
 }
 
-// The kernels of one direction and operand type: blocks of 8 warps in clusters of 1 to 8, and a block of one warp for
+// The kernels of one direction and operand type: blocks of 8 warps in clusters of 1 to 16, and a block of one warp for
 // sequences of at most 8 steps (and, forward, for a single one).
 template <typename T, bool STAGED, bool BWD> struct Kernels {
-    static constexpr size_t kSmem = STAGED ? 2 * (BWD ? 4 : 3) * kTileBytes : 0;
+    static constexpr size_t kSmem = STAGED ? (BWD ? 4 : 3) * Tile<T>::kBytes : 0;
     static void (*of(int cluster))(const GlrArgs)
     {
         if constexpr (BWD)
             return cluster == 1 ? glr_backward_kernel<T, STAGED, 8, 1> : cluster == 2 ? glr_backward_kernel<T, STAGED, 8, 2>
-                 : cluster == 4 ? glr_backward_kernel<T, STAGED, 8, 4> : glr_backward_kernel<T, STAGED, 8, 8>;
+                 : cluster == 4 ? glr_backward_kernel<T, STAGED, 8, 4> : cluster == 8 ? glr_backward_kernel<T, STAGED, 8, 8>
+                 : glr_backward_kernel<T, STAGED, 8, 16>;
         else
             return cluster == 1 ? glr_forward_kernel<T, STAGED, kSteps, 8, 1> : cluster == 2 ? glr_forward_kernel<T, STAGED, kSteps, 8, 2>
-                 : cluster == 4 ? glr_forward_kernel<T, STAGED, kSteps, 8, 4> : glr_forward_kernel<T, STAGED, kSteps, 8, 8>;
+                 : cluster == 4 ? glr_forward_kernel<T, STAGED, kSteps, 8, 4> : cluster == 8 ? glr_forward_kernel<T, STAGED, kSteps, 8, 8>
+                 : glr_forward_kernel<T, STAGED, kSteps, 8, 16>;
     }
-    // Blocks of a cluster lie side by side in time: the size that needs the fewest rounds of spans on a full device,
-    // a span costing a little more with each block whose maps are walked.
+    // Blocks of a cluster lie side by side in time.  The size for which the SMs are done first: a wave of blocks takes
+    // its spans times the blocks that share an SM (one alone hides little of its latencies: it counts for two), and a
+    // span a little more with each block whose maps are walked.
     static int cluster_for(const GlrArgs& a)
     {
-        static std::atomic<int> known[4][64];
-        const int64_t units = a.B * a.strips;
+        static std::atomic<int> known[5][64];
+        const int64_t units = a.B * a.strips, sms = 148;
         int best = 0;
         int64_t cost = -1;
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 5; ++i) {
             const int cl = 1 << i;
             const int64_t at_once = resident(of(cl), 8, cl, kSmem, known[i]);
-            if (at_once < 1) return 0;
-            const int64_t c = (units + at_once - 1) / at_once * ((a.T + 8 * kSteps * cl - 1) / (8 * kSteps * cl)) * (16 + cl);
+            if (at_once < 1) {
+                if (cl > 8) break;
+                return 0;
+            }
+            auto shared = [&](int64_t clusters) { return clusters ? std::max<int64_t>(2, (clusters * cl + sms - 1) / sms) : 0; };
+            const int64_t rounds = units / at_once * shared(at_once) + shared(units % at_once);
+            const int64_t c = rounds * ((a.T + 8 * kSteps * cl - 1) / (8 * kSteps * cl)) * (16 + cl);
             if (cost < 0 || c < cost) {
                 cost = c;
                 best = cl;
@@ -988,7 +880,7 @@ template <typename T, bool BWD> cudaError_t run_short(const GlrArgs& a, cudaStre
     else return launch(glr_forward_kernel<T, false, kSteps, 1, 1>, 1, 1, 0, a, st);
 }
 
-// Inputs go through shared memory where their rows begin on 16 bytes and outputs on what a thread stores.
+// Inputs go through shared memory where their rows begin on 16 bytes.
 bool staged_ok(const kan_glr_shape& s, const GlrArgs& a)
 {
     const int esz = s.dtype == KAN_F32 ? 4 : 2;
@@ -996,14 +888,12 @@ bool staged_ok(const kan_glr_shape& s, const GlrArgs& a)
                                         s.g_stride_t) * esz;
     const uint64_t in = (reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.r) |
                          reinterpret_cast<uintptr_t>(a.g) | reinterpret_cast<uintptr_t>(a.dy));
-    const uint64_t out = (reinterpret_cast<uintptr_t>(a.y) | reinterpret_cast<uintptr_t>(a.dx) |
-                          reinterpret_cast<uintptr_t>(a.dr) | reinterpret_cast<uintptr_t>(a.dg));
-    return strides % 16 == 0 && in % 16 == 0 && out % 4 == 0;
+    return strides % 16 == 0 && in % 16 == 0;
 }
 
 template <typename T, bool BWD> cudaError_t run_type(const kan_glr_shape& s, GlrArgs& a, int& cluster, cudaStream_t st)
 {
-    a.strips = (int)((s.channels + 32 * (4 / sizeof(T)) - 1) / (32 * (4 / sizeof(T))));
+    a.strips = (int)((s.channels + 31) / 32);
     cluster = 1;
     if (a.T <= kSteps) return run_short<T, BWD>(a, st);
     return staged_ok(s, a) ? Kernels<T, true, BWD>::run(a, cluster, st) : Kernels<T, false, BWD>::run(a, cluster, st);
