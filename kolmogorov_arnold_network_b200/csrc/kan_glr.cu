@@ -300,12 +300,12 @@ template <bool CUTS> __device__ __forceinline__ float pass(const float4 (*maps)[
 
 // Exchange of span n of the cluster: every thread gives its map (y, b); it gets the state that enters its steps, and
 // `run` moves past the whole span.  Position 0 comes first in the direction of the scan.  One block barrier a span
-// (past_barrier runs right after it): a set is written again only two spans later, when all warps have passed the
+// (at_barrier runs right before it, past_barrier right after it): a set is written again only two spans later, when all warps have passed the
 // barrier in between, and a block's maps for that span are sent only after it has the whole cluster's of the span in
 // between.  A wait that gives up is recorded; the walk goes on (its results are void) and ends.
-template <int W, int CL, typename Past>
+template <int W, int CL, typename At, typename Past>
 __device__ __forceinline__ float exchange(Meet<W, CL>& s, int n, int wpos, int cpos, float y, float b, float& run, bool cuts,
-                                          unsigned int* status, bool& waits, Past past_barrier)
+                                          unsigned int* status, bool& waits, At at_barrier, Past past_barrier)
 {
     const int lane = threadIdx.x & 31, set = n & 1;
     const Map m = map_of(y, b);
@@ -314,6 +314,7 @@ __device__ __forceinline__ float exchange(Meet<W, CL>& s, int n, int wpos, int c
         run = apply<true>(m, run);
     } else {
         s.warp[set][wpos][lane] = make_float4(m.p, m.k, b, y);
+        at_barrier();
         __syncthreads();
         if constexpr (CL > 1) {
             if (wpos == 0) {
@@ -398,7 +399,8 @@ template <typename T, int S> struct Direct {
 };
 
 // Inputs through shared memory in 16-byte copies: a block's tile of an array is its 64 steps of the strip's 32 channels.
-// A tile is read before the exchange's barrier and filled with the next span's inputs after it.
+// Two sets of tiles: a span's tiles are read before the exchange's barrier, behind which they are filled with the inputs of
+// the span after the next; the next span's are waited for right before that barrier.
 template <typename T> struct Tile {
     static constexpr int kRow = 32 * (int)sizeof(T), kBytes = 8 * kSteps * kRow;
     static constexpr int kChunks = kRow / 16, kRows = 256 / kChunks;     // chunks of a row; rows of one round of the block's copies
@@ -447,22 +449,22 @@ template <typename T, bool STAGED, int S, int NA> struct Inputs {
     int64_t row;                     // the sequence's step of its first copied row in the span at step 0; beyond the end: no chunk
     int first;                       // the shared row of this thread's first step
     const char* tiles;
-    __device__ __forceinline__ void load(int64_t base, int64_t T_, int live)
+    static constexpr int kSet = NA * Tile<T>::kBytes;
+    __device__ __forceinline__ void load(int64_t base, int64_t T_, int live, int set)
     {
         if constexpr (STAGED) {
 #pragma unroll
-            for (int i = 0; i < NA; ++i) a[i].copy(place + i * Tile<T>::kBytes, T_ - base - row);
+            for (int i = 0; i < NA; ++i) a[i].copy(place + set * kSet + i * Tile<T>::kBytes, base < 0 ? 0 : T_ - base - row);
             copies_commit();
         } else {
 #pragma unroll
             for (int i = 0; i < NA; ++i) a[i].load(live);
         }
     }
-    // before the values of a span are used
-    __device__ __forceinline__ void ready()
+    __device__ __forceinline__ void first_ready()
     {
         if constexpr (STAGED) {
-            copies_wait();
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
             __syncthreads();
         }
     }
@@ -484,7 +486,7 @@ template <typename T, bool STAGED, int S, int NA> struct Inputs {
 // Forward: S steps a thread, W warps a block, CL blocks a cluster; STAGED: inputs through shared memory (W = 8), else
 // into registers.
 template <typename T, bool STAGED, int S, int W, int CL>
-__global__ void __launch_bounds__(32 * W, W == 8 ? (STAGED ? 4 : 3) : 1) glr_forward_kernel(const GlrArgs a)
+__global__ void __launch_bounds__(32 * W, W == 8 ? (STAGED && sizeof(T) == 2 ? 4 : 3) : 1) glr_forward_kernel(const GlrArgs a)
 {
     constexpr int N = S > 1 ? 2 : 1;                     // steps side by side
     extern __shared__ __align__(128) char tiles[];       // STAGED: r, g, x
@@ -509,24 +511,27 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? (STAGED ? 4 : 3) : 1) glr_for
     in.row = at.c0 + threadIdx.x % Tile<T>::kChunks * (16 / (int)sizeof(T)) < a.C ? mine + threadIdx.x / Tile<T>::kChunks : a.T;
     in.first = at.warp * S;
     in.tiles = tiles;
-    unsigned char zb = 0;                                // the reset byte of this lane's step of the next span
-    auto fetch = [&](int64_t base) {
+    unsigned char zb = 0, zb_next = 0;                   // the reset byte of this lane's step of the span, of the next one
+    auto fetch = [&](int64_t base, int set) {
         const int live = (int)min((int64_t)S, max((int64_t)0, a.T - base - first));
         if (Z) {
-            zb = lane < live ? Z[lane] : 0;
+            zb_next = lane < live ? Z[lane] : 0;
             Z += SPAN;
         }
-        in.load(base, a.T, live);
+        in.load(base, a.T, live, set);
     };
     meet_init(meet);
     bool waits = true;
-    fetch(0);
+    fetch(0, 0);
+    zb = zb_next;
+    if constexpr (STAGED) fetch(SPAN, 1);
+    in.first_ready();
 
     int n = 0;
     for (int64_t base = 0; base < a.T; base += SPAN, ++n) {
         const int live = (int)min((int64_t)S, max((int64_t)0, a.T - base - first));
         const uint32_t cuts = a.reset ? __ballot_sync(0xffffffffu, zb != 0) : 0;
-        in.ready();
+        if constexpr (STAGED) in.tiles = tiles + (n & 1) * in.kSet;
         float fa[S], bb[S], len = 0.0f, B = 0.0f;
 #pragma unroll
         for (int i = 0; i < S; i += N) {
@@ -553,7 +558,8 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? (STAGED ? 4 : 3) : 1) glr_for
                 }
             }
         }
-        if (!STAGED && base + SPAN < a.T) fetch(base + SPAN);
+        if (!STAGED && base + SPAN < a.T) fetch(base + SPAN, 0);
+        zb = zb_next;
         if (cuts) {                                      // resets among the steps: they cut off what comes before them
             B = 0.0f;
             len = INFINITY;
@@ -563,10 +569,14 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? (STAGED ? 4 : 3) : 1) glr_for
                 if (i < live) B = fmaf(fa[i], B, bb[i]);
             }
         }
-        float h = exchange<W, CL>(meet, n, at.warp, at.rank, len, B, run, a.reset != nullptr, a.status, waits, [&] {
-            if constexpr (STAGED)                        // all warps have read this span's tiles
-                if (base + SPAN < a.T) fetch(base + SPAN);
-        });
+        float h = exchange<W, CL>(meet, n, at.warp, at.rank, len, B, run, a.reset != nullptr, a.status, waits,
+            [&] {
+                if constexpr (STAGED) copies_wait();
+            },
+            [&] {
+                if constexpr (STAGED)                    // all warps have read this span's tiles
+                    if (base + SPAN < a.T) fetch(base + 2 * SPAN, n & 1);
+            });
         if (K) {
             if (live > 0 && at.on) *K = h;
             K += SPAN / kSteps * a.C;
@@ -597,7 +607,7 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? (STAGED ? 4 : 3) : 1) glr_for
 
 // Backward: the same split, walked from the end of the sequence.
 template <typename T, bool STAGED, int W, int CL>
-__global__ void __launch_bounds__(32 * W, W == 8 ? (STAGED ? 3 : 2) : 1) glr_backward_kernel(const GlrArgs a)
+__global__ void __launch_bounds__(32 * W, W == 8 ? (STAGED && sizeof(T) == 2 ? 3 : 2) : 1) glr_backward_kernel(const GlrArgs a)
 {
     constexpr int S = kSteps, N = 2;                     // a thread's steps begin at a kept state
     extern __shared__ __align__(128) char tiles[];       // STAGED: r, g, x, dy
@@ -624,27 +634,30 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? (STAGED ? 3 : 2) : 1) glr_bac
     in.row = at.c0 + threadIdx.x % Tile<T>::kChunks * (16 / (int)sizeof(T)) < a.C ? mine + threadIdx.x / Tile<T>::kChunks : a.T;
     in.first = at.warp * S;
     in.tiles = tiles;
-    unsigned char zb = 0;                                // reset byte of this lane's step, and the kept state, of the next span
-    float hb = 0.0f;
-    auto fetch = [&](int64_t base) {
-        const int live = (int)min((int64_t)S, max((int64_t)0, a.T - base - first));
+    unsigned char zb = 0, zb_next = 0;                   // reset byte of this lane's step, and the kept state: of the span,
+    float hb = 0.0f, hb_next = 0.0f;                     // of the next one
+    auto fetch = [&](int64_t base, int set) {            // (a span before the first one: base < 0)
+        const int live = base < 0 ? 0 : (int)min((int64_t)S, max((int64_t)0, a.T - base - first));
         if (Z) {
-            zb = lane < live ? Z[lane] : 0;
+            zb_next = lane < live ? Z[lane] : 0;
             Z -= SPAN;
         }
-        if (live > 0) hb = *K;
+        if (live > 0) hb_next = *K;
         K -= SPAN / kSteps * a.C;
-        in.load(base, a.T, live);
+        in.load(base, a.T, live, set);
     };
     meet_init(meet);
     bool waits = true;
-    fetch(end);
+    fetch(end, 0);
+    zb = zb_next, hb = hb_next;
+    if constexpr (STAGED) fetch(end - SPAN, 1);
+    in.first_ready();
 
     int n = 0;
     for (int64_t base = end; base >= 0; base -= SPAN, ++n) {
         const int live = (int)min((int64_t)S, max((int64_t)0, a.T - base - first));
         const uint32_t cut = a.reset ? __ballot_sync(0xffffffffu, zb != 0) : 0;
-        in.ready();
+        if constexpr (STAGED) in.tiles = tiles + (n & 1) * in.kSet;
         float h = hb;
         // per step: the factor, and what d multiplies in each gradient:
         //   dx = d cx,  dg = dx cg,  dL L = d cl,  dr = dL L cr
@@ -697,11 +710,16 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? (STAGED ? 3 : 2) : 1) glr_bac
             }
             len = INFINITY;
         }
-        if (!STAGED && base > 0) fetch(base - SPAN);
-        float flow = exchange<W, CL>(meet, n, W - 1 - at.warp, CL - 1 - at.rank, len, B, run, a.reset != nullptr, a.status, waits, [&] {
-            if constexpr (STAGED)
-                if (base > 0) fetch(base - SPAN);
-        });
+        if (!STAGED && base > 0) fetch(base - SPAN, 0);
+        zb = zb_next, hb = hb_next;
+        float flow = exchange<W, CL>(meet, n, W - 1 - at.warp, CL - 1 - at.rank, len, B, run, a.reset != nullptr, a.status, waits,
+            [&] {
+                if constexpr (STAGED) copies_wait();
+            },
+            [&] {
+                if constexpr (STAGED)
+                    if (base > 0) fetch(base - 2 * SPAN, n & 1);
+            });
         float part = 0.0f;
         if (at.on) {
             T *ox = reinterpret_cast<T*>(a.dx) + out, *orr = reinterpret_cast<T*>(a.dr) + out, *og = reinterpret_cast<T*>(a.dg) + out;
@@ -829,7 +847,7 @@ template <typename K> cudaError_t launch(K kernel, int warps, int cluster, size_
 // The kernels of one direction and operand type: blocks of 8 warps in clusters of 1 to 16, and a block of one warp for
 // sequences of at most 8 steps (and, forward, for a single one).
 template <typename T, bool STAGED, bool BWD> struct Kernels {
-    static constexpr size_t kSmem = STAGED ? (BWD ? 4 : 3) * Tile<T>::kBytes : 0;
+    static constexpr size_t kSmem = STAGED ? 2 * (BWD ? 4 : 3) * Tile<T>::kBytes : 0;
     static void (*of(int cluster))(const GlrArgs)
     {
         if constexpr (BWD)
