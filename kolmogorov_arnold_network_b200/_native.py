@@ -246,8 +246,7 @@ def kan_input_range(n, x, dtype, minmax, workspace, ws_bytes, stream):
 
 
 def make_embed_shape(tokens, rows, dim, padding_idx, scale, dtype, grad_dtype, id_bytes) -> kan_embed_shape:
-    return kan_embed_shape(int(tokens), int(rows), int(dim), int(padding_idx), float(scale), int(dtype),
-                           int(grad_dtype), int(id_bytes))
+    return kan_embed_shape(tokens, rows, dim, padding_idx, scale, dtype, grad_dtype, id_bytes)
 
 
 def kan_embed_workspace_size(shape: kan_embed_shape) -> int:

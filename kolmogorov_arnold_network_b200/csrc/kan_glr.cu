@@ -486,7 +486,7 @@ template <typename T, bool STAGED, int S, int NA> struct Inputs {
 // Forward: S steps a thread, W warps a block, CL blocks a cluster; STAGED: inputs through shared memory (W = 8), else
 // into registers.
 template <typename T, bool STAGED, int S, int W, int CL>
-__global__ void __launch_bounds__(32 * W, W == 8 ? (STAGED && sizeof(T) == 2 ? 4 : 3) : 1) glr_forward_kernel(const GlrArgs a)
+__global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 1) glr_forward_kernel(const GlrArgs a)
 {
     constexpr int N = S > 1 ? 2 : 1;                     // steps side by side
     extern __shared__ __align__(128) char tiles[];       // STAGED: r, g, x
@@ -607,7 +607,7 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? (STAGED && sizeof(T) == 2 ? 4
 
 // Backward: the same split, walked from the end of the sequence.
 template <typename T, bool STAGED, int W, int CL>
-__global__ void __launch_bounds__(32 * W, W == 8 ? (STAGED && sizeof(T) == 2 ? 3 : 2) : 1) glr_backward_kernel(const GlrArgs a)
+__global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_backward_kernel(const GlrArgs a)
 {
     constexpr int S = kSteps, N = 2;                     // a thread's steps begin at a kept state
     extern __shared__ __align__(128) char tiles[];       // STAGED: r, g, x, dy

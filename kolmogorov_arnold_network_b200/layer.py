@@ -7,6 +7,7 @@ of the layer itself runs in libkan_b200.so.
 """
 from __future__ import annotations
 
+import contextlib
 import math
 
 import torch
@@ -381,43 +382,66 @@ class UKANLayer(torch.nn.Module):
 
 # ---------------------------------------------------------------------------
 # Sequence operators around the layers: embedding, gated linear recurrence, distillation loss
-def _same_device(ref, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"{name} is on {t.device}, expected {ref.device}")
+_NO_SWITCH = contextlib.nullcontext()
+
+
+def _on(device: int):
+    """The library works on the current device: a switch to the operands' device where it is another one (these calls are
+    often small, so the usual case costs nothing)."""
+    return _NO_SWITCH if device == torch._C._cuda_getDevice() else torch.cuda.device(device)
+
+
+def _raw_stream(device: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
+def _is(t, dtype, shape, device: int) -> bool:
+    """A dense CUDA tensor of this dtype, shape and device."""
+    return t.dtype is dtype and t.get_device() == device and t.shape == shape and t.is_contiguous()
+
+
+def _need(t, name, dtype, shape, device: int):
+    """_is, with the reason where it is not; None passes."""
+    if t is None or _is(t, dtype, shape, device):
+        return
+    _check(t, name, dtype, shape)
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
 
 
 def _id_bytes(ids, name="ids"):
-    if ids.dtype not in (torch.int32, torch.int64):
+    if ids.dtype is torch.int64:
+        return 8
+    if ids.dtype is not torch.int32:
         raise TypeError(f"{name} has dtype {ids.dtype}, expected int32 or int64")
-    return 4 if ids.dtype == torch.int32 else 8
+    return 4
 
 
 def embed_forward(ids, weight, scale=1.0, y=None):
     """y[..., :] = scale * weight[ids[...], :]; ids int32 or int64 of any shape, weight [rows, dim].  An id outside the
     table gives a row of zeros and is reported by the device status (``_native.kan_sync_status``)."""
+    dtype, code, dev = weight.dtype, _code(weight), weight.get_device()
     _check(weight, "weight")
-    _check(ids, "ids")
     if weight.dim() != 2:
         raise ValueError("weight must be [rows, dim]")
     rows, dim = weight.shape
-    code = _code(weight)
+    _need(ids, "ids", ids.dtype, ids.shape, dev)
     s = N.make_embed_shape(ids.numel(), rows, dim, -1, scale, code, code, _id_bytes(ids))
     if y is None:
-        y = torch.empty((*ids.shape, dim), dtype=weight.dtype, device=weight.device)
-    _check(y, "y", weight.dtype, (*ids.shape, dim))
-    _same_device(weight, ids=ids, y=y)
-    with torch.cuda.device(weight.device):
-        N.kan_embed_forward(s, _p(ids), _p(weight), _p(y), _stream(weight))
+        y = weight.new_empty((*ids.shape, dim))
+    else:
+        _need(y, "y", dtype, (*ids.shape, dim), dev)
+    with _on(dev):
+        N.kan_embed_forward(s, ids.data_ptr(), weight.data_ptr(), y.data_ptr(), _raw_stream(dev))
     return y
 
 
 def embed_backward(ids, dY, rows, scale=1.0, padding_idx=None, grad_dtype=torch.float32, out=None, ws=None):
     """dW [rows, dim] = scale * the sum of dY's rows by id, in one fixed order (tokens sorted by id); ``grad_dtype``
     float32 or bfloat16 (rounded once).  The row ``padding_idx`` and rows without a token are 0."""
-    _check(ids, "ids")
+    dev = dY.get_device()
     _check(dY, "dY")
-    if dY.dim() < 1 or tuple(dY.shape[:-1]) != tuple(ids.shape):
+    _need(ids, "ids", ids.dtype, ids.shape, dev)
+    if dY.dim() < 1 or dY.shape[:-1] != ids.shape:
         raise ValueError(f"dY has shape {tuple(dY.shape)}, expected {tuple(ids.shape)} and the row length")
     dim = dY.shape[-1]
     if out is not None:
@@ -428,12 +452,14 @@ def embed_backward(ids, dY, rows, scale=1.0, padding_idx=None, grad_dtype=torch.
                            _DT[grad_dtype], _id_bytes(ids))
     if out is None:
         out = torch.empty((rows, dim), dtype=grad_dtype, device=dY.device)
-    _check(out, "out", grad_dtype, (rows, dim))
-    _same_device(dY, ids=ids, out=out, ws=ws)
-    with torch.cuda.device(dY.device):
+    else:
+        _need(out, "out", grad_dtype, (rows, dim), dev)
+    with _on(dev):
         if ws is None:
             ws = torch.empty(max(16, N.kan_embed_workspace_size(s)), dtype=torch.uint8, device=dY.device)
-        N.kan_embed_backward(s, _p(ids), _p(dY), _p(out), _p(ws), ws.numel(), _stream(dY))
+        else:
+            _need(ws, "ws", torch.uint8, ws.shape, dev)
+        N.kan_embed_backward(s, ids.data_ptr(), dY.data_ptr(), out.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(dev))
     return out
 
 
@@ -480,21 +506,24 @@ def _glr_operand(t, name, x):
         raise TypeError(f"{name} has dtype {t.dtype}, expected {x.dtype}")
     if t.shape != x.shape or t.dim() != 3:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [batch, time, channels] as x")
-    sb, st, sc = t.stride()
-    if sc != 1 and t.shape[2] > 1:
+    if t.stride(2) != 1 and t.shape[2] > 1:
         raise ValueError(f"{name}'s channels must be contiguous")
-    return sb, st
 
 
 def _glr_shape(x, r, g, decay, reset):
-    strides = [_glr_operand(t, nm, x) for t, nm in ((x, "x"), (r, "r"), (g, "g"))]
-    B, T, C = x.shape
-    _check(decay, "decay", torch.float32, (C,))
-    if reset is not None and reset.dtype not in (torch.bool, torch.uint8):
-        raise TypeError(f"reset has dtype {reset.dtype}, expected bool or uint8")
-    _check(reset, "reset", None, (B, T))
-    _same_device(x, decay=decay, reset=reset)
-    return N.make_glr_shape(B, T, C, *strides, _code(x))
+    shape, dev = x.shape, x.get_device()
+    sx, sr, sg = x.stride(), r.stride(), g.stride()
+    if not (len(shape) == 3 and dev >= 0 and r.shape == shape == g.shape and r.dtype is x.dtype is g.dtype
+            and r.get_device() == dev == g.get_device() and sx[2] == sr[2] == sg[2] == 1):
+        for t, nm in ((x, "x"), (r, "r"), (g, "g")):
+            _glr_operand(t, nm, x)
+    B, T, C = shape
+    _need(decay, "decay", torch.float32, (C,), dev)
+    if reset is not None:
+        if reset.dtype not in (torch.bool, torch.uint8):
+            raise TypeError(f"reset has dtype {reset.dtype}, expected bool or uint8")
+        _need(reset, "reset", reset.dtype, (B, T), dev)
+    return N.make_glr_shape(B, T, C, sx[:2], sr[:2], sg[:2], _code(x))
 
 
 def glr_forward(x, r, g, decay, h0=None, reset=None, keep=False, y=None, h_last=None):
@@ -504,18 +533,21 @@ def glr_forward(x, r, g, decay, h0=None, reset=None, keep=False, y=None, h_last=
     set the state starts from 0 again.  With ``keep`` the states for ``glr_backward`` come in ``kept``, else None.
     For one new token pass time = 1 and h_last=h0 to update the state in place."""
     s = _glr_shape(x, r, g, decay, reset)
+    dev = x.get_device()
     B, T, C = x.shape
     if y is None:
-        y = torch.empty((B, T, C), dtype=x.dtype, device=x.device)
+        y = x.new_empty((B, T, C))
+    else:
+        _need(y, "y", x.dtype, (B, T, C), dev)
+    _need(h0, "h0", torch.float32, (B, C), dev)
     if h_last is None:
-        h_last = torch.empty((B, C), dtype=torch.float32, device=x.device)
-    kept = (torch.empty((B, -(-T // N.KAN_GLR_STEPS), C), dtype=torch.float32, device=x.device) if keep else None)
-    _check(h0, "h0", torch.float32, (B, C))
-    _check(y, "y", x.dtype, (B, T, C))
-    _check(h_last, "h_last", torch.float32, (B, C))
-    _same_device(x, h0=h0, y=y, h_last=h_last)
-    with torch.cuda.device(x.device):
-        N.kan_glr_forward(s, _p(x), _p(r), _p(g), _p(decay), _p(reset), _p(h0), _p(y), _p(h_last), _p(kept), _stream(x))
+        h_last = decay.new_empty((B, C))
+    elif h_last is not h0:
+        _need(h_last, "h_last", torch.float32, (B, C), dev)
+    kept = decay.new_empty((B, -(-T // N.KAN_GLR_STEPS), C)) if keep else None
+    with _on(dev):
+        N.kan_glr_forward(s, x.data_ptr(), r.data_ptr(), g.data_ptr(), decay.data_ptr(), _p(reset), _p(h0), y.data_ptr(),
+                          h_last.data_ptr(), _p(kept), _raw_stream(dev))
     return y, h_last, kept
 
 
@@ -523,19 +555,22 @@ def glr_backward(x, r, g, decay, kept, dY, reset=None, dh_last=None, need=(True,
     """(dx, dr, dg, ddecay, dh0) for upstream dY [batch, time, channels] and dh_last [batch, channels] (None: 0), from
     the states ``kept`` by ``glr_forward``; ``need`` says which are wanted (None is returned for the others)."""
     s = _glr_shape(x, r, g, decay, reset)
+    dev = x.get_device()
     B, T, C = x.shape
-    _check(kept, "kept", torch.float32, (B, -(-T // N.KAN_GLR_STEPS), C))
-    _check(dY, "dY", x.dtype, (B, T, C))
-    _check(dh_last, "dh_last", torch.float32, (B, C))
-    _same_device(x, kept=kept, dY=dY, dh_last=dh_last, ws=ws)
-    dx, dr, dg = (torch.empty((B, T, C), dtype=x.dtype, device=x.device) if n else None for n in need[:3])
-    ddecay = torch.empty_like(decay) if need[3] else None
-    dh0 = torch.empty((B, C), dtype=torch.float32, device=x.device) if need[4] else None
-    with torch.cuda.device(x.device):
+    _need(kept, "kept", torch.float32, (B, -(-T // N.KAN_GLR_STEPS), C), dev)
+    _need(dY, "dY", x.dtype, (B, T, C), dev)
+    _need(dh_last, "dh_last", torch.float32, (B, C), dev)
+    dx, dr, dg = (x.new_empty((B, T, C)) if n else None for n in need[:3])
+    ddecay = decay.new_empty(C) if need[3] else None
+    dh0 = decay.new_empty((B, C)) if need[4] else None
+    with _on(dev):
         if ws is None and ddecay is not None:
             ws = torch.empty(max(16, N.kan_glr_workspace_size(s)), dtype=torch.uint8, device=x.device)
-        N.kan_glr_backward(s, _p(x), _p(r), _p(g), _p(decay), _p(reset), _p(kept), _p(dY), _p(dh_last), _p(dx), _p(dr),
-                           _p(dg), _p(ddecay), _p(dh0), _p(ws), 0 if ws is None else ws.numel(), _stream(x))
+        elif ws is not None:
+            _need(ws, "ws", torch.uint8, ws.shape, dev)
+        N.kan_glr_backward(s, x.data_ptr(), r.data_ptr(), g.data_ptr(), decay.data_ptr(), _p(reset), kept.data_ptr(),
+                           dY.data_ptr(), _p(dh_last), _p(dx), _p(dr), _p(dg), _p(ddecay), _p(dh0), _p(ws),
+                           0 if ws is None else ws.numel(), _raw_stream(dev))
     return dx, dr, dg, ddecay, dh0
 
 
@@ -600,20 +635,18 @@ def _rows_of(t, name):
 
 
 def _distill_shape(z, ids, teacher, temperature, weight, dz=None):
-    ld = _rows_of(z, "logits")
+    ld, dev = _rows_of(z, "logits"), z.get_device()
     n, vocab = z.shape
-    _check(ids, "ids")
-    _check(teacher, "teacher", torch.float32)
+    _need(ids, "ids", ids.dtype, ids.shape, dev)
     if ids.dim() != 2 or ids.shape[0] != n:
         raise ValueError(f"ids has shape {tuple(ids.shape)}, expected [{n}, entries]")
-    _check(teacher, "teacher", torch.float32, tuple(ids.shape))
-    _check(weight, "weight", torch.float32, (n,))
+    _need(teacher, "teacher", torch.float32, ids.shape, dev)
+    _need(weight, "weight", torch.float32, (n,), dev)
     ld_grad = vocab
     if dz is not None:
         ld_grad = _rows_of(dz, "dlogits")
-        if dz.dtype != z.dtype or dz.shape != z.shape:
-            raise ValueError("dlogits must have the logits' shape and dtype")
-    _same_device(z, ids=ids, teacher=teacher, weight=weight, dlogits=dz)
+        if dz.dtype != z.dtype or dz.shape != z.shape or dz.get_device() != dev:
+            raise ValueError("dlogits must have the logits' shape, dtype and device")
     return N.make_distill_shape(n, vocab, ld, ld_grad, ids.shape[1], _id_bytes(ids), temperature, _code(z))
 
 
@@ -623,10 +656,11 @@ def distill_forward(logits, ids, teacher, temperature=1.0, weight=None):
     negative id is an empty place): loss[n] = weight[n] T^2 KL(softmax(teacher / T) || softmax(logits / T)), the teacher's
     distribution over its entries, the student's over the vocabulary.  ``stats`` goes to ``distill_backward``."""
     s = _distill_shape(logits, ids, teacher, temperature, weight)
-    loss = torch.empty(s.rows, dtype=torch.float32, device=logits.device)
-    stats = torch.empty((s.rows, 2), dtype=torch.float32, device=logits.device)
-    with torch.cuda.device(logits.device):
-        N.kan_distill_forward(s, _p(logits), _p(ids), _p(teacher), _p(weight), _p(loss), _p(stats), _stream(logits))
+    dev = logits.get_device()
+    loss, stats = teacher.new_empty(s.rows), teacher.new_empty((s.rows, 2))
+    with _on(dev):
+        N.kan_distill_forward(s, logits.data_ptr(), ids.data_ptr(), teacher.data_ptr(), _p(weight), loss.data_ptr(),
+                              stats.data_ptr(), _raw_stream(dev))
     return loss, stats
 
 
@@ -635,12 +669,12 @@ def distill_backward(logits, ids, teacher, stats, temperature=1.0, weight=None, 
     if dlogits is None:
         dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
     s = _distill_shape(logits, ids, teacher, temperature, weight, dlogits)
-    _check(stats, "stats", torch.float32, (s.rows, 2))
-    _check(dloss, "dloss", torch.float32, (s.rows,))
-    _same_device(logits, stats=stats, dloss=dloss)
-    with torch.cuda.device(logits.device):
-        N.kan_distill_backward(s, _p(logits), _p(ids), _p(teacher), _p(weight), _p(stats), _p(dloss), _p(dlogits),
-                               _stream(logits))
+    dev = logits.get_device()
+    _need(stats, "stats", torch.float32, (s.rows, 2), dev)
+    _need(dloss, "dloss", torch.float32, (s.rows,), dev)
+    with _on(dev):
+        N.kan_distill_backward(s, logits.data_ptr(), ids.data_ptr(), teacher.data_ptr(), _p(weight), stats.data_ptr(),
+                               _p(dloss), dlogits.data_ptr(), _raw_stream(dev))
     return dlogits
 
 
@@ -650,11 +684,11 @@ def distill_loss_grad(logits, ids, teacher, temperature=1.0, weight=None, dlogit
     if dlogits is None:
         dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
     s = _distill_shape(logits, ids, teacher, temperature, weight, dlogits)
-    loss = torch.empty(s.rows, dtype=torch.float32, device=logits.device)
-    stats = torch.empty((s.rows, 2), dtype=torch.float32, device=logits.device)
-    with torch.cuda.device(logits.device):
-        N.kan_distill_loss_grad(s, _p(logits), _p(ids), _p(teacher), _p(weight), _p(loss), _p(stats), _p(dlogits),
-                                _stream(logits))
+    dev = logits.get_device()
+    loss, stats = teacher.new_empty(s.rows), teacher.new_empty((s.rows, 2))
+    with _on(dev):
+        N.kan_distill_loss_grad(s, logits.data_ptr(), ids.data_ptr(), teacher.data_ptr(), _p(weight), loss.data_ptr(),
+                                stats.data_ptr(), dlogits.data_ptr(), _raw_stream(dev))
     return loss, dlogits
 
 
