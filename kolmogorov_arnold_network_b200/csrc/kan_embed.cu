@@ -9,19 +9,22 @@
 // distinct row read).
 //
 // Backward, without atomic adds and with one fixed order of summation:
-//   1. embed_sort_kernel orders the tokens by id, stably.  Block p owns the
-//      ids with id % P == p (P a power of two): neighbouring ids, whose
-//      frequencies are alike in a vocabulary, fall to different blocks.
-//      Every block reads all ids twice (they stay in L2); the first reading
-//      counts, per warp, the tokens of each owned id and all tokens of the
-//      blocks before it, which gives the block's place in the order without
-//      any exchange between blocks; the second one places its tokens.  The
-//      block also writes the zero rows of its ids that no token has.
-//   2. embed_sum_kernel cuts the ordered list into chunks of kChunk tokens;
-//      a thread keeps one vector of columns and adds the chunk's rows in
-//      order.  Runs that lie within a chunk are written at once, the pieces
-//      of runs that cross a border go to the workspace as fp32 partials:
-//      the work is even however often a token occurs.
+//   1. The tokens are ordered by id, stably.  A sort block owns the ids that
+//      are alike modulo P (a power of two, 256 at least): neighbouring ids, whose frequencies are
+//      alike in a vocabulary, fall to different blocks.
+//      Few tokens: every block reads all ids twice (they stay in L2); the
+//      first reading counts, per warp, the tokens of each owned id and all
+//      tokens of the blocks before it, which gives the block's place in the
+//      order without any exchange between blocks; the second one places its
+//      tokens.  Many tokens: embed_split_kernel first groups each piece of
+//      2048 tokens by owner, and a sort block reads its own tokens only.
+//   2. embed_sum_kernel cuts the ordered list into chunks; a thread keeps some
+//      vectors of columns and adds the chunk's rows in order.  Runs that lie
+//      within a chunk are written at once, the pieces of runs that cross a
+//      border go to the workspace as fp32 partials: the work is even however
+//      often a token occurs.  Further blocks of the same launch write the zero
+//      rows of the ids that no token has, the larger part of the traffic where
+//      the vocabulary is large.
 //   3. embed_join_kernel adds the partials of each such run in chunk order.
 // Sums are fp32 and rounded once, when the row of dW is written.
 #include <algorithm>
@@ -36,8 +39,15 @@ constexpr int kSegVecs = 128;     // forward: vectors of a row that one warp cop
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxBins = 1536;    // ids per sort block (their per-warp counts lie in shared memory)
-constexpr int kChunk = 64;        // tokens per chunk of the ordered list
-constexpr int kJoinRows = 4;      // partials that a block of the join adds side by side
+constexpr int kMaxChunk = 64;     // tokens per chunk of the ordered list, at most
+constexpr int kJoinRows = 4;     // partials that a block of the join adds side by side
+constexpr int kPiece = 2048;      // tokens that a block of the split groups by owner
+constexpr int kBatch = 8;          // ids that a thread of the sort reads at once
+constexpr int kSplitShift = 8;    // owners of the split: 256 (more sort blocks share an owner's tokens)
+
+// A kernel launched while the one before it still runs waits here for its end.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 template <typename I> __device__ __forceinline__ int64_t id_at(const void* ids, int64_t t)
 {
@@ -78,50 +88,153 @@ __global__ void __launch_bounds__(128) embed_forward_kernel(const void* __restri
 }
 
 // ---- backward: the order ----
+// The sort block of an id: by its low 8 bits (the owner), and by the next bits where there are more than 256 blocks.
+__device__ __forceinline__ int sort_block(int id, int shift)
+{
+    const int more = shift - kSplitShift;
+    return (id & ((1 << kSplitShift) - 1)) << more | (id >> kSplitShift & ((1 << more) - 1));
+}
+
 struct SortArgs {
     const void* ids;
-    int32_t* perm;       // [tokens] token numbers, ordered by (block, id), ascending within an id
+    int32_t* perm;       // [tokens] token numbers, ordered by (sort block, id), ascending within an id
     int32_t* key;        // [tokens] their ids
     int32_t* count;      // [1] tokens that take part
-    void* dW;
+    uint8_t* present;    // [P][bins] whether a token has the id
+    int2* grouped;       // [tokens] (token, id) of each piece, grouped by owner
+    int32_t* start;      // [pieces][257] where each owner's tokens begin in the piece
     int64_t tokens, rows, pad;
-    int64_t row_bytes;
     int shift;           // log2 P
     int bins;            // ids per block
-    int wide;            // dW's rows are whole 16-byte vectors
+    int pieces;          // 0: the blocks read the ids themselves
     unsigned int* status;
 };
 
-template <typename I>
+// Groups a piece of tokens by owner (id % 256), stably: counts per warp and owner, their running sums, then each token
+// to its place.
+template <typename I> __global__ void __launch_bounds__(kSortThreads) embed_split_kernel(const SortArgs a)
+{
+    constexpr int P = 1 << kSplitShift, PER = kPiece / kSortThreads;
+    __shared__ int32_t cnt[kSortWarps][P];
+    __shared__ int32_t wsum[8];
+    let_next_start();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    for (int i = tid; i < kSortWarps * P; i += kSortThreads) (&cnt[0][0])[i] = 0;
+    const int64_t t0 = (int64_t)blockIdx.x * kPiece + warp * (32 * PER) + lane;
+    int id[PER], rank[PER];
+    bool bad = false;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {                      // a warp's tokens in their order, 32 at a time
+        const int64_t t = t0 + 32 * k;
+        const int64_t v = t < a.tokens ? id_at<I>(a.ids, t) : a.pad;
+        const bool in = v >= 0 && v < a.rows;
+        bad |= t < a.tokens && !in;
+        id[k] = in && v != a.pad && t < a.tokens ? (int)v : -1;
+        const int o = id[k] & (P - 1);
+        const unsigned act = __ballot_sync(0xffffffffu, id[k] >= 0);
+        rank[k] = 0;
+        if (id[k] >= 0) {
+            const unsigned same = __match_any_sync(act, o);
+            rank[k] = cnt[warp][o] + __popc(same & ((1u << lane) - 1));
+            __syncwarp(act);
+            if ((same & ((1u << lane) - 1)) == 0) cnt[warp][o] += __popc(same);
+        }
+        __syncwarp();
+    }
+    if (bad) record_status(a.status, KAN_ERR_DEVICE_CHECK);
+    __syncthreads();
+    int n = 0, s = 0;
+    if (tid < P) {
+        for (int w = 0; w < kSortWarps; ++w) {
+            const int c = cnt[w][tid];
+            cnt[w][tid] = n;
+            n += c;
+        }
+        s = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += u;
+        }
+        if (lane == 31) wsum[warp] = s;
+    }
+    __syncthreads();
+    if (tid < P) {
+        int before = 0;
+        for (int w = 0; w < warp; ++w) before += wsum[w];
+        const int at = before + s - n;
+        a.start[(int64_t)blockIdx.x * (P + 1) + tid] = at;
+        if (tid == P - 1) a.start[(int64_t)blockIdx.x * (P + 1) + P] = at + n;
+        for (int w = 0; w < kSortWarps; ++w) cnt[w][tid] += at;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < PER; ++k)
+        if (id[k] >= 0)
+            a.grouped[(int64_t)blockIdx.x * kPiece + cnt[warp][id[k] & (P - 1)] + rank[k]] = make_int2((int)(t0 + 32 * k), id[k]);
+}
+
+template <typename I, bool SPLIT>
 __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const SortArgs a)
 {
     extern __shared__ int32_t cnt[];                // [kSortWarps][bins] counts, then next places
-    int32_t* total = cnt + (size_t)kSortWarps * a.bins;   // [bins] tokens of each id
     __shared__ int32_t wsum[kSortWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int p = blockIdx.x;
-    const int64_t mask = ((int64_t)1 << a.shift) - 1;
+    let_next_start();
     for (int i = tid; i < kSortWarps * a.bins; i += kSortThreads) cnt[i] = 0;
     __syncthreads();
 
-    // tokens of this warp: a contiguous piece, whole 32-token steps
+    // this warp's tokens: a contiguous part of the list (SPLIT: of the pieces)
     const int64_t piece = ((a.tokens + kSortThreads - 1) / kSortThreads) * 32;
-    const int64_t t0 = min(a.tokens, piece * warp), t1 = min(a.tokens, t0 + piece);
+    const int64_t t0 = SPLIT ? (int64_t)a.pieces * warp / kSortWarps : min(a.tokens, piece * warp);
+    const int64_t t1 = SPLIT ? (int64_t)a.pieces * (warp + 1) / kSortWarps : min(a.tokens, t0 + piece);
     int32_t* mine = cnt + (size_t)warp * a.bins;
+    const int owner = p >> (a.shift - kSplitShift);
     int below = 0;
-    bool bad = false;
-#pragma unroll 4
-    for (int64_t t = t0 + lane; t < t1; t += 32) {
-        const int64_t id = id_at<I>(a.ids, t);
-        const bool in = id >= 0 && id < a.rows;
-        bad |= !in;
-        if (in && id != a.pad) {
-            const int o = (int)(id & mask);
-            below += o < p;
-            if (o == p) atomicAdd(&mine[id >> a.shift], 1);   // an integer count: no order
+    // SPLIT: begin and end of the owner's tokens in the warp's next 32 pieces, a lane each
+    int from = 0, to = 0;
+    auto bounds = [&](int64_t q0) {
+        const bool has = q0 + lane < t1;
+        const int32_t* st = a.start + (q0 + lane) * ((1 << kSplitShift) + 1) + owner;
+        from = has ? st[0] : 0;
+        to = has ? st[1] : 0;
+    };
+    if constexpr (SPLIT) {
+        wait_for_previous();
+        for (int64_t q0 = t0; q0 < t1; q0 += 32) {
+            bounds(q0);
+            below += from;                          // the owners before this one
+            for (int k = 0; k < 32 && q0 + k < t1; ++k) {
+                const int f = __shfl_sync(0xffffffffu, from, k), l = __shfl_sync(0xffffffffu, to, k);
+                for (int j = f + lane; j < l; j += 32) {
+                    const int id = a.grouped[(q0 + k) * kPiece + j].y;
+                    const int o = sort_block(id, a.shift);
+                    below += o < p;
+                    if (o == p) atomicAdd(&mine[id >> a.shift], 1);   // an integer count: no order
+                }
+            }
         }
+    } else {
+        bool bad = false;
+        for (int64_t t = t0 + lane; t < t1; t += 32 * kBatch) {
+            int64_t id[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) id[k] = t + 32 * k < t1 ? id_at<I>(a.ids, t + 32 * k) : a.pad;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const bool in = id[k] >= 0 && id[k] < a.rows;
+                bad |= !in && t + 32 * k < t1;
+                if (in && id[k] != a.pad && t + 32 * k < t1) {
+                    const int o = sort_block((int)id[k], a.shift);
+                    below += o < p;
+                    if (o == p) atomicAdd(&mine[id[k] >> a.shift], 1);   // an integer count: no order
+                }
+            }
+        }
+        if (p == 0 && bad) record_status(a.status, KAN_ERR_DEVICE_CHECK);
     }
-    if (p == 0 && bad) record_status(a.status, KAN_ERR_DEVICE_CHECK);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) below += __shfl_xor_sync(0xffffffffu, below, o);
     if (lane == 0) wsum[warp] = below;
@@ -131,7 +244,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const SortArgs
     for (int w = 0; w < kSortWarps; ++w) base += wsum[w];
     __syncthreads();
 
-    // places: ids ascending, and within an id the warps' pieces in order
+    // places: ids ascending, and within an id the warps' parts in order
     int carry = base;
     for (int b0 = 0; b0 < a.bins; b0 += kSortThreads) {
         const int b = b0 + tid;
@@ -152,7 +265,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const SortArgs
             all += wsum[w];
         }
         if (b < a.bins) {
-            total[b] = n;
+            a.present[(int64_t)p * a.bins + b] = n != 0;
             int at = carry + before + s - n;
             for (int w = 0; w < kSortWarps; ++w) {
                 int32_t& c = cnt[(size_t)w * a.bins + b];
@@ -164,37 +277,43 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const SortArgs
         carry += all;
         __syncthreads();
     }
-    if (p == (int)mask && tid == 0) *a.count = carry;
+    if (p == (1 << a.shift) - 1 && tid == 0) *a.count = carry;
 
     // second reading: every token to its place
-    for (int64_t t = t0; t < t1; t += 32) {
-        const int64_t tl = t + lane;
-        const int64_t id = tl < t1 ? id_at<I>(a.ids, tl) : -1;
-        const bool own = id >= 0 && id < a.rows && id != a.pad && (int)(id & mask) == p;
+    auto place = [&](bool own, int token, int id) {
         const unsigned act = __ballot_sync(0xffffffffu, own);
-        if (act == 0) continue;
+        if (act == 0) return;
         if (own) {
-            const int b = (int)(id >> a.shift);
+            const int b = id >> a.shift;
             const unsigned same = __match_any_sync(act, b);
             const int rank = __popc(same & ((1u << lane) - 1));
             const int at = mine[b];
             __syncwarp(act);
             if (rank == 0) mine[b] = at + __popc(same);
-            a.perm[at + rank] = (int32_t)tl;
-            a.key[at + rank] = (int32_t)id;
+            a.perm[at + rank] = token;
+            a.key[at + rank] = id;
         }
         __syncwarp();
-    }
-
-    // rows that no token has
-    for (int b = warp; b < a.bins; b += kSortWarps) {
-        const int64_t id = ((int64_t)b << a.shift) + p;
-        if (id >= a.rows || total[b] != 0) continue;
-        char* row = reinterpret_cast<char*>(a.dW) + id * a.row_bytes;
-        if (a.wide) {
-            for (int64_t i = (int64_t)lane * 16; i < a.row_bytes; i += 512) *reinterpret_cast<uint4*>(row + i) = uint4{};
-        } else {
-            for (int64_t i = (int64_t)lane * 2; i < a.row_bytes; i += 64) *reinterpret_cast<uint16_t*>(row + i) = 0;
+    };
+    if constexpr (SPLIT) {
+        for (int64_t q0 = t0; q0 < t1; q0 += 32) {
+            if (t1 - t0 > 32) bounds(q0);           // (32 pieces at most: still there)
+            for (int k = 0; k < 32 && q0 + k < t1; ++k) {
+                const int f = __shfl_sync(0xffffffffu, from, k), l = __shfl_sync(0xffffffffu, to, k);
+                for (int j0 = f; j0 < l; j0 += 32) {
+                    const int2 g = j0 + lane < l ? a.grouped[(q0 + k) * kPiece + j0 + lane] : make_int2(0, -1);
+                    place(g.y >= 0 && sort_block(g.y, a.shift) == p, g.x, g.y);
+                }
+            }
+        }
+    } else {
+        for (int64_t t = t0 + lane; t - lane < t1; t += 32 * kBatch) {
+            int64_t id[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) id[k] = t + 32 * k < t1 ? id_at<I>(a.ids, t + 32 * k) : -1;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+                place(id[k] >= 0 && id[k] < a.rows && id[k] != a.pad && sort_block((int)id[k], a.shift) == p, (int)(t + 32 * k), (int)id[k]);
         }
     }
 }
@@ -206,9 +325,13 @@ struct SumArgs {
     const int32_t* perm;
     const int32_t* key;
     const int32_t* count;
-    float* part;         // [chunks][2][dim]: a chunk's first piece (of a run that began before it), its last piece
-    int64_t dim;
+    const uint8_t* present;
+    float* part;         // [chunks][2][part_dim]: a chunk's first piece (of a run that began before it), its last piece
+    int64_t dim, rows, row_bytes, part_dim;
     float scale;
+    int chunk;           // tokens per chunk
+    int shift, bins;     // as the sort's
+    int64_t chunks, zero_blocks;
 };
 
 template <typename T, typename O, int N>
@@ -225,96 +348,168 @@ __device__ __forceinline__ void store_row(O* p, const float (&acc)[N], float sca
     }
 }
 
-template <typename T, typename O, int N>
+// The zero rows of the ids that no token has: a warp a row.
+template <typename V> __device__ __forceinline__ void zero_row(char* row, int64_t bytes)
+{
+    for (int64_t i = (threadIdx.x & 31) * sizeof(V); i < bytes; i += 32 * sizeof(V)) *reinterpret_cast<V*>(row + i) = V{};
+}
+__device__ __forceinline__ void zero_rows(const SumArgs& a, int64_t block)
+{
+    const int warps = blockDim.x >> 5;
+    for (int64_t id = block * warps + (threadIdx.x >> 5); id < a.rows; id += a.zero_blocks * warps) {
+        if (a.present[(int64_t)sort_block((int)id, a.shift) * a.bins + (id >> a.shift)]) continue;
+        char* row = reinterpret_cast<char*>(a.dW) + id * a.row_bytes;
+        if (a.row_bytes % 16 == 0) zero_row<uint4>(row, a.row_bytes);
+        else if (a.row_bytes % 4 == 0) zero_row<uint32_t>(row, a.row_bytes);
+        else zero_row<uint16_t>(row, a.row_bytes);
+    }
+}
+
+// NV vectors of N elements per thread, blockDim apart.
+template <typename T, typename O, int N, int NV>
 __global__ void __launch_bounds__(256) embed_sum_kernel(const SumArgs a)
 {
-    __shared__ int32_t sp[kChunk], sk[kChunk + 2];       // token numbers; ids with the neighbours' on both sides
+    constexpr int U = NV > 1 ? 4 : 8;                    // rows in flight
+    __shared__ int32_t sp[kMaxChunk], sk[kMaxChunk + 2]; // token numbers; ids with the neighbours' on both sides
+    let_next_start();
+    wait_for_previous();
+    if ((int64_t)blockIdx.x >= a.chunks) {
+        if (blockIdx.y == 0) zero_rows(a, blockIdx.x - a.chunks);
+        return;
+    }
     const int m = *a.count;
-    const int64_t c0 = (int64_t)blockIdx.x * kChunk;
+    const int64_t c0 = (int64_t)blockIdx.x * a.chunk;
     if (c0 >= m) return;
-    const int len = (int)min((int64_t)kChunk, m - c0);
+    const int len = (int)min((int64_t)a.chunk, m - c0);
     for (int i = threadIdx.x; i < len; i += blockDim.x) sp[i] = a.perm[c0 + i];
     for (int i = threadIdx.x; i < len + 2; i += blockDim.x) {
         const int64_t j = c0 + i - 1;
         sk[i] = j >= 0 && j < m ? a.key[j] : -1;
     }
     __syncthreads();
-    const int64_t v = (int64_t)blockIdx.y * blockDim.x + threadIdx.x;
-    if (v * N >= a.dim) return;
-    const T* src = reinterpret_cast<const T*>(a.dY) + v * N;
-    O* dst = reinterpret_cast<O*>(a.dW) + v * N;
-    float* part = a.part + (int64_t)blockIdx.x * 2 * a.dim + v * N;
+    // bits of the rows at which a run, or the chunk, ends
+    const int lane = threadIdx.x & 31;
+    auto ends_at = [&](int i) { return i < len && (i + 1 == len || sk[i + 2] != sk[i + 1]); };
+    const uint64_t ends = (uint64_t)__ballot_sync(0xffffffffu, ends_at(lane)) | (uint64_t)__ballot_sync(0xffffffffu, ends_at(lane + 32)) << 32;
+
+    const int64_t v0 = (int64_t)blockIdx.y * blockDim.x * NV + threadIdx.x, vecs = a.dim / N;
+    if (v0 >= vecs) return;
+    const int step = blockDim.x * N;                     // elements between a thread's vectors
+    bool on[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) on[k] = v0 + (int64_t)k * blockDim.x < vecs;
+    const T* src = reinterpret_cast<const T*>(a.dY) + v0 * N;
+    O* dst = reinterpret_cast<O*>(a.dW) + v0 * N;
+    float* part = a.part + (int64_t)blockIdx.x * 2 * a.part_dim + v0 * N;
     bool from_before = sk[1] == sk[0];
-    float acc[N];
+    float acc[NV][N];
+    auto clear = [&] {
 #pragma unroll
-    for (int e = 0; e < N; ++e) acc[e] = 0.0f;
-    constexpr int U = 8;
-    for (int i0 = 0; i0 < len; i0 += U) {
-        Pack<T, N> q[U];
+        for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (i0 + u < len) q[u] = Pack<T, N>::load(src + (int64_t)sp[i0 + u] * a.dim);
+            for (int e = 0; e < N; ++e) acc[k][e] = 0.0f;
+    };
+    clear();
+    Pack<T, N> q[U][NV];
+    auto load = [&](int i0) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int i = i0 + u;
-            if (i < len) {
-                float f[N];
-                q[u].unpack(f);
+            if (i0 + u < len) {
+                const T* row = src + (int64_t)sp[i0 + u] * a.dim;
 #pragma unroll
-                for (int e = 0; e < N; ++e) acc[e] += f[e];
-                const int id = sk[i + 1];
-                const bool last = i + 1 == len;
-                if (last || sk[i + 2] != id) {           // the run's end, or the chunk's
+                for (int k = 0; k < NV; ++k)
+                    if (on[k]) q[u][k] = Pack<T, N>::load(row + k * step);
+            }
+        }
+    };
+    load(0);
+    for (int i0 = 0; i0 < len; i0 += U) {
+        Pack<T, N> now[U][NV];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int k = 0; k < NV; ++k) now[u][k] = q[u][k];
+        load(i0 + U);
+        const uint32_t e4 = (uint32_t)(ends >> i0) & ((1u << U) - 1);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (i0 + u < len) {
+#pragma unroll
+                for (int k = 0; k < NV; ++k) {
+                    float f[N];
+                    now[u][k].unpack(f);
+#pragma unroll
+                    for (int e = 0; e < N; ++e) acc[k][e] += f[e];
+                }
+                if (e4 >> u & 1) {
+                    const int i = i0 + u, id = sk[i + 1];
                     const bool goes_on = sk[i + 2] == id;
-                    if (!from_before && !goes_on) store_row<T, O, N>(dst + (int64_t)id * a.dim, acc, a.scale);
-                    else store_row<T, float, N>(part + (from_before ? 0 : a.dim), acc, 1.0f);
-                    from_before = false;
 #pragma unroll
-                    for (int e = 0; e < N; ++e) acc[e] = 0.0f;
+                    for (int k = 0; k < NV; ++k) {
+                        if (!on[k]) continue;
+                        if (!from_before && !goes_on) store_row<T, O, N>(dst + (int64_t)id * a.dim + k * step, acc[k], a.scale);
+                        else store_row<T, float, N>(part + (from_before ? 0 : a.part_dim) + k * step, acc[k], 1.0f);
+                    }
+                    from_before = false;
+                    clear();
                 }
             }
         }
     }
 }
 
-// A run that crosses chunk borders is joined by the block of the chunk where
-// it begins: that chunk's last piece and the first pieces of the chunks after
-// it, kJoinRows sums side by side, added in a fixed order at the end.
+// A run that crosses chunk borders is joined by the block of the chunk where it begins: that chunk's last piece and the
+// first pieces of the chunks after it, kJoinRows sums side by side, added in a fixed order at the end.  A block takes
+// 256 columns (the partials' rows are whole float4).
 template <typename O>
 __global__ void __launch_bounds__(64 * kJoinRows) embed_join_kernel(const SumArgs a)
 {
+    let_next_start();
+    wait_for_previous();
     const int m = *a.count;
-    const int64_t c = blockIdx.x, end = (c + 1) * kChunk;
+    const int64_t c = blockIdx.x, end = (c + 1) * a.chunk;
     if (end >= m) return;
     const int id = a.key[end - 1];
     if (a.key[end] != id) return;
     // it begins here if the chunk's first token is another id's, or the run's very first one
-    const int64_t c0 = c * kChunk;
+    const int64_t c0 = c * a.chunk;
     if (a.key[c0] == id && c0 > 0 && a.key[c0 - 1] == id) return;
     // the chunks after it whose first token is still of the run (equal ids lie side by side)
     int64_t last_chunk = c;
     for (;;) {
-        const int64_t at = (last_chunk + 1 + threadIdx.x) * kChunk;
+        const int64_t at = (last_chunk + 1 + threadIdx.x) * a.chunk;
         const int n = __syncthreads_count(at < m && a.key[at] == id);
         last_chunk += n;
         if (n < (int)blockDim.x) break;
     }
-    __shared__ float red[kJoinRows][64];
+    __shared__ float4 red[kJoinRows][64];
     const int col = threadIdx.x & 63, row = threadIdx.x >> 6;
-    const int64_t d = (int64_t)blockIdx.y * 64 + col;
-    float acc = 0.0f;
-    if (d < a.dim) {
-        if (row == 0) acc = a.part[(c * 2 + 1) * a.dim + d];
-        for (int64_t k = c + 1 + row; k <= last_chunk; k += kJoinRows) acc += a.part[k * 2 * a.dim + d];
+    const int64_t d = ((int64_t)blockIdx.y * 64 + col) * 4;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (d < a.part_dim) {
+        auto add = [&](int64_t piece) {
+            const float4 q = *reinterpret_cast<const float4*>(a.part + piece * a.part_dim + d);
+            acc.x += q.x, acc.y += q.y, acc.z += q.z, acc.w += q.w;
+        };
+        if (row == 0) add(c * 2 + 1);
+#pragma unroll 4
+        for (int64_t k = c + 1 + row; k <= last_chunk; k += kJoinRows) add(k * 2);
     }
     red[row][col] = acc;
     __syncthreads();
-    if (row == 0 && d < a.dim) {
-        float s = red[0][col];
+    if (row == 0) {
 #pragma unroll
-        for (int r = 1; r < kJoinRows; ++r) s += red[r][col];
-        const float f[1] = {s * a.scale};
-        Pack<O, 1>::pack(f).store(reinterpret_cast<O*>(a.dW) + (int64_t)id * a.dim + d);
+        for (int r = 1; r < kJoinRows; ++r) {
+            const float4 q = red[r][col];
+            acc.x += q.x, acc.y += q.y, acc.z += q.z, acc.w += q.w;
+        }
+        const float v[4] = {acc.x, acc.y, acc.z, acc.w};
+        O* out = reinterpret_cast<O*>(a.dW) + (int64_t)id * a.dim;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float f[1] = {v[e] * a.scale};
+            if (d + e < a.dim) Pack<O, 1>::pack(f).store(out + d + e);
+        }
     }
 }
 
@@ -340,27 +535,84 @@ kan_status validate(const kan_embed_shape* s)
 // Sort blocks: 256 (all resident at once on 148 SMs), more for tables of more than 256 * kMaxBins rows.
 int sort_shift(const kan_embed_shape& s)
 {
-    int sh = 8;
+    int sh = kSplitShift;
     while (((s.rows - 1) >> sh) + 1 > kMaxBins) ++sh;
     return sh;
 }
 
+// Tokens per chunk: small enough that the chunks fill the SMs, 16 to 64 (fewer tokens a chunk, more partials).
+int chunk_of(const kan_embed_shape& s)
+{
+    int c = kMaxChunk;
+    while (c > 16 && s.tokens / c < 4 * 148) c /= 2;
+    return c;
+}
+// Above this many tokens the sort blocks read what embed_split_kernel has grouped for them, below it the ids themselves.
+constexpr int64_t kSplitFrom = 8192;
+
 struct Layout {
-    size_t perm, key, count, part, bytes;
-    int64_t chunks;
+    size_t perm, key, count, present, grouped, start, part, bytes;
+    int64_t chunks, pieces, part_dim;
+    int chunk, shift, bins;
 };
 
 Layout layout_of(const kan_embed_shape& s)
 {
     auto up = [](size_t n) { return (n + 255) / 256 * 256; };
     Layout L{};
-    L.chunks = (s.tokens + kChunk - 1) / kChunk;
+    L.chunk = chunk_of(s);
+    L.chunks = (s.tokens + L.chunk - 1) / L.chunk;
+    L.pieces = s.tokens > kSplitFrom ? (s.tokens + kPiece - 1) / kPiece : 0;
+    L.shift = sort_shift(s);
+    L.bins = (int)(((s.rows - 1) >> L.shift) + 1);
     L.perm = 0;
     L.key = L.perm + up((size_t)s.tokens * 4);
     L.count = L.key + up((size_t)s.tokens * 4);
-    L.part = L.count + 256;
-    L.bytes = L.part + up((size_t)L.chunks * 2 * s.dim * 4);
+    L.present = L.count + 256;
+    L.grouped = L.present + up((size_t)L.bins << L.shift);
+    L.start = L.grouped + (L.pieces ? up((size_t)s.tokens * 8) : 0);
+    L.part = L.start + up((size_t)L.pieces * ((1 << kSplitShift) + 1) * 4);
+    L.part_dim = (s.dim + 3) / 4 * 4;
+    L.bytes = L.part + up((size_t)L.chunks * 2 * L.part_dim * 4);
     return L;
+}
+
+// A launch whose blocks may be set up while the kernel before it ends (it waits for that end itself).
+template <typename K, typename A> cudaError_t launch_after(K kernel, dim3 grid, int threads, size_t smem, const A& a, cudaStream_t st)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
+    if (e == cudaSuccess) count_launch();
+    return e;
+}
+
+template <typename I> cudaError_t launch_sort(const SortArgs& o, cudaStream_t st)
+{
+    const size_t smem = (size_t)kSortWarps * o.bins * 4;
+    const dim3 grid(1u << o.shift);
+    cudaError_t e;
+    if (o.pieces) {
+        e = cudaFuncSetAttribute(embed_sort_kernel<I, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        embed_split_kernel<I><<<(unsigned)o.pieces, kSortThreads, 0, st>>>(o);
+        count_launch();
+        e = cudaGetLastError();
+        return e == cudaSuccess ? launch_after(embed_sort_kernel<I, true>, grid, kSortThreads, smem, o, st) : e;
+    }
+    e = cudaFuncSetAttribute(embed_sort_kernel<I, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    embed_sort_kernel<I, false><<<grid, kSortThreads, smem, st>>>(o);
+    count_launch();
+    return cudaGetLastError();
 }
 
 template <typename T, int N>
@@ -389,28 +641,27 @@ cudaError_t forward_of(const kan_embed_shape& s, const void* ids, const void* W,
 }
 
 template <typename T, typename O, int N>
-cudaError_t launch_sum(const kan_embed_shape& s, const SumArgs& a, int64_t chunks, cudaStream_t st)
+cudaError_t launch_sum(const kan_embed_shape& s, SumArgs a, cudaStream_t st)
 {
-    const int64_t vecs = s.dim / N;
+    // narrow vectors come four to a thread, so that a row's bookkeeping is shared by as many loads
+    constexpr int NV = N * (int)sizeof(T) <= 4 ? 4 : 1;
+    const int64_t vecs = (s.dim / N + NV - 1) / NV;
     const int64_t slices = (vecs + 255) / 256;
     const int threads = (int)(((vecs + slices - 1) / slices + 31) / 32 * 32);
-    embed_sum_kernel<T, O, N><<<dim3((unsigned)chunks, (unsigned)slices), threads, 0, st>>>(a);
-    count_launch();
-    cudaError_t e = cudaGetLastError();
+    a.zero_blocks = std::min<int64_t>((s.rows + threads / 32 - 1) / (threads / 32), 148 * 16);
+    const cudaError_t e = launch_after(embed_sum_kernel<T, O, N, NV>, dim3((unsigned)(a.chunks + a.zero_blocks), (unsigned)slices), threads, 0, a, st);
     if (e != cudaSuccess) return e;
-    embed_join_kernel<O><<<dim3((unsigned)chunks, (unsigned)((s.dim + 63) / 64)), 64 * kJoinRows, 0, st>>>(a);
-    count_launch();
-    return cudaGetLastError();
+    return launch_after(embed_join_kernel<O>, dim3((unsigned)a.chunks, (unsigned)((s.dim + 255) / 256)), 64 * kJoinRows, 0, a, st);
 }
 
 template <typename T, typename O>
-cudaError_t sum_of(const kan_embed_shape& s, const SumArgs& a, int64_t chunks, cudaStream_t st)
+cudaError_t sum_of(const kan_embed_shape& s, const SumArgs& a, cudaStream_t st)
 {
     switch (common_vector_bytes((uint64_t)s.dim * sizeof(T)) / (int)sizeof(T)) {
-    case 8: if constexpr (sizeof(T) == 2) return launch_sum<T, O, 8>(s, a, chunks, st);
-    case 4: return launch_sum<T, O, 4>(s, a, chunks, st);
-    case 2: return launch_sum<T, O, 2>(s, a, chunks, st);
-    default: return launch_sum<T, O, 1>(s, a, chunks, st);
+    case 8: if constexpr (sizeof(T) == 2) return launch_sum<T, O, 8>(s, a, st);
+    case 4: return launch_sum<T, O, 4>(s, a, st);
+    case 2: return launch_sum<T, O, 2>(s, a, st);
+    default: return launch_sum<T, O, 1>(s, a, st);
     }
 }
 
@@ -466,26 +717,17 @@ kan_status kan_embed_backward(const kan_embed_shape* s, const void* ids, const v
     o.perm = reinterpret_cast<int32_t*>(ws + L.perm);
     o.key = reinterpret_cast<int32_t*>(ws + L.key);
     o.count = reinterpret_cast<int32_t*>(ws + L.count);
-    o.dW = dW;
     o.tokens = s->tokens;
     o.rows = s->rows;
     o.pad = s->padding_idx;
-    o.row_bytes = row_bytes;
-    o.shift = sort_shift(*s);
-    o.bins = (int)(((s->rows - 1) >> o.shift) + 1);
-    o.wide = row_bytes % 16 == 0;
+    o.present = reinterpret_cast<uint8_t*>(ws + L.present);
+    o.grouped = reinterpret_cast<int2*>(ws + L.grouped);
+    o.start = reinterpret_cast<int32_t*>(ws + L.start);
+    o.shift = L.shift;
+    o.bins = L.bins;
+    o.pieces = (int)L.pieces;
     o.status = device_status_ptr();
-    const size_t smem = (size_t)(kSortWarps + 1) * o.bins * 4;
-    const void* fn = s->id_bytes == 8 ? reinterpret_cast<const void*>(&embed_sort_kernel<int64_t>)
-                                      : reinterpret_cast<const void*>(&embed_sort_kernel<int32_t>);
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess) {
-        const unsigned P = 1u << o.shift;
-        if (s->id_bytes == 8) embed_sort_kernel<int64_t><<<P, kSortThreads, smem, cs>>>(o);
-        else embed_sort_kernel<int32_t><<<P, kSortThreads, smem, cs>>>(o);
-        count_launch();
-        e = cudaGetLastError();
-    }
+    cudaError_t e = s->id_bytes == 8 ? launch_sort<int64_t>(o, cs) : launch_sort<int32_t>(o, cs);
     if (e == cudaSuccess) {
         SumArgs a{};
         a.dY = dY;
@@ -494,14 +736,22 @@ kan_status kan_embed_backward(const kan_embed_shape* s, const void* ids, const v
         a.key = o.key;
         a.count = o.count;
         a.part = reinterpret_cast<float*>(ws + L.part);
+        a.present = o.present;
         a.dim = s->dim;
+        a.rows = s->rows;
+        a.row_bytes = row_bytes;
+        a.part_dim = L.part_dim;
         a.scale = s->scale;
+        a.chunk = L.chunk;
+        a.shift = L.shift;
+        a.bins = L.bins;
+        a.chunks = L.chunks;
         const bool g32 = s->grad_dtype == KAN_F32;
         if (s->dtype == KAN_F32)
-            e = g32 ? sum_of<float, float>(*s, a, L.chunks, cs) : sum_of<float, __nv_bfloat16>(*s, a, L.chunks, cs);
+            e = g32 ? sum_of<float, float>(*s, a, cs) : sum_of<float, __nv_bfloat16>(*s, a, cs);
         else
-            e = g32 ? sum_of<__nv_bfloat16, float>(*s, a, L.chunks, cs)
-                    : sum_of<__nv_bfloat16, __nv_bfloat16>(*s, a, L.chunks, cs);
+            e = g32 ? sum_of<__nv_bfloat16, float>(*s, a, cs)
+                    : sum_of<__nv_bfloat16, __nv_bfloat16>(*s, a, cs);
     }
     return e == cudaSuccess ? KAN_OK : em_fail(KAN_ERR_CUDA, cudaGetErrorString(e));
 }

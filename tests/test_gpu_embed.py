@@ -86,7 +86,7 @@ GRAD = [
     # n, rows, dim, ids
     (1, 1, 1, "uniform"), (1, 300, 768, "uniform"), (64, 64, 64, "one"), (65, 1000, 771, "one"), (129, 5, 8, "uniform"),
     (1000, 50257, 24, "zipf"), (8192, 5000, 96, "zipf"), (4097, 3, 130, "uniform"), (20000, 700, 33, "zipf"),
-    (33000, 2, 12, "one"), (640, 10, 1030, "uniform"),
+    (33000, 2, 12, "one"), (640, 10, 1030, "uniform"), (8193, 300, 40, "zipf"), (2, 4, 3000, "one"),
 ]
 
 
@@ -103,7 +103,7 @@ def test_gradient(dt, gdt, case):
     assert N.kan_sync_status(None) == 0
 
 
-@pytest.mark.parametrize("n,rows", [(300, 400_001), (5000, 700_000)])
+@pytest.mark.parametrize("n,rows", [(300, 400_001), (5000, 700_000), (9000, 800_003), (20000, 400_001)])
 def test_gradient_large_table(n, rows):
     """More rows than 256 sort blocks hold bins for."""
     ids = _ids(n, rows, "uniform", 3)
