@@ -41,7 +41,9 @@ constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxBins = 1536;    // ids per sort block (their per-warp counts lie in shared memory)
 constexpr int kMaxChunk = 64;     // tokens per chunk of the ordered list, at most
 constexpr int kJoinRows = 4;     // partials that a block of the join adds side by side
+constexpr int kShortRun = 4;      // a run of at most so many further pieces is joined by one block
 constexpr int kPiece = 2048;      // tokens that a block of the split groups by owner
+constexpr int kFound = 32;        // tokens that a warp of the sort keeps from its first reading
 constexpr int kBatch = 8;          // ids that a thread of the sort reads at once
 constexpr int kSplitShift = 8;    // owners of the split: 256 (more sort blocks share an owner's tokens)
 
@@ -180,6 +182,8 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const SortArgs
 {
     extern __shared__ int32_t cnt[];                // [kSortWarps][bins] counts, then next places
     __shared__ int32_t wsum[kSortWarps];
+    __shared__ int2 kept[SPLIT ? 1 : kSortWarps][kFound];
+    int found = 0;                                  // tokens of this block in the warp's part
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int p = blockIdx.x;
     let_next_start();
@@ -218,18 +222,24 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const SortArgs
         }
     } else {
         bool bad = false;
-        for (int64_t t = t0 + lane; t < t1; t += 32 * kBatch) {
+        for (int64_t t = t0 + lane; t - lane < t1; t += 32 * kBatch) {
             int64_t id[kBatch];
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) id[k] = t + 32 * k < t1 ? id_at<I>(a.ids, t + 32 * k) : a.pad;
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
-                const bool in = id[k] >= 0 && id[k] < a.rows;
-                bad |= !in && t + 32 * k < t1;
-                if (in && id[k] != a.pad && t + 32 * k < t1) {
-                    const int o = sort_block((int)id[k], a.shift);
-                    below += o < p;
-                    if (o == p) atomicAdd(&mine[id[k] >> a.shift], 1);   // an integer count: no order
+                const bool in = id[k] >= 0 && id[k] < a.rows, live = t + 32 * k < t1;
+                bad |= !in && live;
+                const int o = in && live && id[k] != a.pad ? sort_block((int)id[k], a.shift) : p + 1;
+                below += o < p;
+                const unsigned act = __ballot_sync(0xffffffffu, o == p);
+                if (act) {                          // few tokens are this block's: kept for the second reading
+                    if (o == p) {
+                        atomicAdd(&mine[id[k] >> a.shift], 1);   // an integer count: no order
+                        const int at = found + __popc(act & ((1u << lane) - 1));
+                        if (at < kFound) kept[warp][at] = make_int2((int)(t + 32 * k), (int)id[k]);
+                    }
+                    found += __popc(act);
                 }
             }
         }
@@ -305,6 +315,11 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const SortArgs
                     place(g.y >= 0 && sort_block(g.y, a.shift) == p, g.x, g.y);
                 }
             }
+        }
+    } else if (found <= kFound) {
+        for (int j = lane; j - lane < found; j += 32) {
+            const int2 g = j < found ? kept[warp][j] : make_int2(0, -1);
+            place(g.y >= 0, g.x, g.y);
         }
     } else {
         for (int64_t t = t0 + lane; t - lane < t1; t += 32 * kBatch) {
@@ -466,50 +481,56 @@ __global__ void __launch_bounds__(64 * kJoinRows) embed_join_kernel(const SumArg
 {
     let_next_start();
     wait_for_previous();
-    const int m = *a.count;
-    const int64_t c = blockIdx.x, end = (c + 1) * a.chunk;
-    if (end >= m) return;
-    const int id = a.key[end - 1];
-    if (a.key[end] != id) return;
+    const int64_t c = blockIdx.x, c0 = c * a.chunk, end = c0 + a.chunk;
+    // (all at once: a.key has room for whole chunks and one more)
+    const int m = *a.count, id = a.key[end - 1], next = a.key[end], first = a.key[c0], before = a.key[max(c0 - 1, (int64_t)0)];
+    if (end >= m || next != id) return;
     // it begins here if the chunk's first token is another id's, or the run's very first one
-    const int64_t c0 = c * a.chunk;
-    if (a.key[c0] == id && c0 > 0 && a.key[c0 - 1] == id) return;
+    if (first == id && c0 > 0 && before == id) return;
     // the chunks after it whose first token is still of the run (equal ids lie side by side)
     int64_t last_chunk = c;
     for (;;) {
         const int64_t at = (last_chunk + 1 + threadIdx.x) * a.chunk;
-        const int n = __syncthreads_count(at < m && a.key[at] == id);
+        const int n = __syncthreads_count(at < m && a.key[min(at, (int64_t)m)] == id);
         last_chunk += n;
         if (n < (int)blockDim.x) break;
+    }
+    auto get = [&](int64_t piece, int64_t d) { return *reinterpret_cast<const float4*>(a.part + piece * a.part_dim + d); };
+    auto put = [&](float4 acc, int64_t d) {
+        const float v[4] = {acc.x, acc.y, acc.z, acc.w};
+        O* out = reinterpret_cast<O*>(a.dW) + (int64_t)id * a.dim + d;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float f[1] = {v[e] * a.scale};
+            if (d + e < a.dim) Pack<O, 1>::pack(f).store(out + e);
+        }
+    };
+    auto plus = [](float4 x, float4 y) { return make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w); };
+    if (last_chunk - c <= kShortRun) {               // few pieces: one block takes all columns
+        if (blockIdx.y) return;
+        for (int64_t d = threadIdx.x * 4; d < a.part_dim; d += 4 * blockDim.x) {
+            float4 acc = get(c * 2 + 1, d);
+#pragma unroll 2
+            for (int64_t k = c + 1; k <= last_chunk; ++k) acc = plus(acc, get(k * 2, d));
+            put(acc, d);
+        }
+        return;
     }
     __shared__ float4 red[kJoinRows][64];
     const int col = threadIdx.x & 63, row = threadIdx.x >> 6;
     const int64_t d = ((int64_t)blockIdx.y * 64 + col) * 4;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (d < a.part_dim) {
-        auto add = [&](int64_t piece) {
-            const float4 q = *reinterpret_cast<const float4*>(a.part + piece * a.part_dim + d);
-            acc.x += q.x, acc.y += q.y, acc.z += q.z, acc.w += q.w;
-        };
-        if (row == 0) add(c * 2 + 1);
-#pragma unroll 4
-        for (int64_t k = c + 1 + row; k <= last_chunk; k += kJoinRows) add(k * 2);
+        if (row == 0) acc = get(c * 2 + 1, d);
+#pragma unroll 8
+        for (int64_t k = c + 1 + row; k <= last_chunk; k += kJoinRows) acc = plus(acc, get(k * 2, d));
     }
     red[row][col] = acc;
     __syncthreads();
     if (row == 0) {
 #pragma unroll
-        for (int r = 1; r < kJoinRows; ++r) {
-            const float4 q = red[r][col];
-            acc.x += q.x, acc.y += q.y, acc.z += q.z, acc.w += q.w;
-        }
-        const float v[4] = {acc.x, acc.y, acc.z, acc.w};
-        O* out = reinterpret_cast<O*>(a.dW) + (int64_t)id * a.dim;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float f[1] = {v[e] * a.scale};
-            if (d + e < a.dim) Pack<O, 1>::pack(f).store(out + d + e);
-        }
+        for (int r = 1; r < kJoinRows; ++r) acc = plus(acc, red[r][col]);
+        put(acc, d);
     }
 }
 
@@ -567,7 +588,7 @@ Layout layout_of(const kan_embed_shape& s)
     L.bins = (int)(((s.rows - 1) >> L.shift) + 1);
     L.perm = 0;
     L.key = L.perm + up((size_t)s.tokens * 4);
-    L.count = L.key + up((size_t)s.tokens * 4);
+    L.count = L.key + up((size_t)(L.chunks * L.chunk + 1) * 4);      // (the join reads whole chunks)
     L.present = L.count + 256;
     L.grouped = L.present + up((size_t)L.bins << L.shift);
     L.start = L.grouped + (L.pieces ? up((size_t)s.tokens * 8) : 0);
