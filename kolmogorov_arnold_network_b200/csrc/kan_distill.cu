@@ -12,6 +12,7 @@
 // next to the maximum, and a row that a mask fills with its type's lowest value
 // stays finite.
 #include <algorithm>
+#include <atomic>
 
 #include "kan_device.cuh"
 #include "kan_vec.cuh"
@@ -292,6 +293,401 @@ template <typename T> __global__ void __launch_bounds__(kThreads) distill_backwa
     subtract_teacher<T>(a, t, zk, out, st, c);
 }
 
+// ---- both in one pass ----
+// A cluster of CL blocks takes a row at a time, a block a slice of it, which lies in its shared memory from the load to the
+// store: the logits are read once and the gradient is written in their place there.  Two buffers: while a row is worked
+// on, the next one is loaded and the last one stored, in bulk copies of whole 16-byte chunks (the elements of a row's or
+// slice's broken chunks go by plain loads and stores).  The blocks of a cluster exchange the slices' (maximum, sum) and
+// the logits at the teacher's tokens (for the loss, which block 0 writes) through st.async and an mbarrier.
+struct FusedArgs {
+    DistArgs d;
+    int per;                      // elements of a slice (the last one may be shorter): whole chunks
+    int buf;                      // bytes of a buffer
+    int kp;                       // teacher entries, rounded up to 4
+};
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync_all()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_addr(uint32_t local, uint32_t rank)
+{
+    uint32_t d;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(local), "r"(rank));
+    return d;
+}
+__device__ __forceinline__ void st_async(uint32_t to, uint32_t bar, float2 v)
+{
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%2, %3}, [%1];" ::"r"(to), "r"(bar),
+                 "f"(v.x), "f"(v.y)
+                 : "memory");
+}
+__device__ __forceinline__ void st_async(uint32_t to, uint32_t bar, float v)
+{
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.f32 [%0], %2, [%1];" ::"r"(to), "r"(bar), "f"(v)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_load(uint32_t to, const void* from, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to), "l"(from),
+                 "r"(bytes), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_store(void* to, uint32_t from, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to), "r"(from), "r"(bytes) : "memory");
+}
+
+// (m, s) of two parts: sums relative to the larger maximum.  A part without elements is (-inf, 0).
+__device__ __forceinline__ float2 both(float2 a, float2 b, float k)
+{
+    const float m = fmaxf(a.x, b.x);
+    const float s = (a.x == neg_inf() ? a.y : a.y * term(a.x, m, k)) + (b.x == neg_inf() ? b.y : b.y * term(b.x, m, k));
+    return make_float2(m, s);
+}
+
+template <typename T, int CL, int NT>
+__global__ void __launch_bounds__(NT, NT == 512 ? 2 : 6) distill_fused_kernel(const FusedArgs f)
+{
+    constexpr int N = 16 / (int)sizeof(T), WARPS = NT / 32, J = 2;       // at most J entries a thread
+    extern __shared__ __align__(128) unsigned char smem[];
+    const DistArgs& a = f.d;
+    int32_t* const tid_ = reinterpret_cast<int32_t*>(smem + 2 * (size_t)f.buf);      // [kp] ids of the entries, -1: none
+    float* const te = reinterpret_cast<float*>(tid_ + f.kp);                         // [kp] exp((t - max) / T)
+    float* const zk = te + f.kp;                                                     // [2][kp] block 0: logits at the entries
+    __shared__ float2 wstat[WARPS], cstat[2][CL];
+    __shared__ float wmax[WARPS], wsum[WARPS], wloss[WARPS];
+    __shared__ uint64_t full[2], met[2];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = CL > 1 ? (int)cluster_rank() : 0;
+    const int64_t clusters = gridDim.x / CL;
+    const int64_t v0 = (int64_t)rank * f.per;
+    const int len = (int)min((int64_t)f.per, a.vocab - v0);
+    const int warps_k = min(WARPS, (a.k + 31) / 32);                     // warps that hold entries
+    if (tid == 0) {
+        mbar_init(smem_addr(&full[0]), 1);
+        mbar_init(smem_addr(&full[1]), 1);
+        mbar_init(smem_addr(&met[0]), 1);
+        mbar_init(smem_addr(&met[1]), 1);
+        fence_barrier_init();
+    }
+    if constexpr (CL > 1) cluster_sync_all();
+    else __syncthreads();
+
+    const T* const Z = reinterpret_cast<const T*>(a.z) + v0;
+    T* const G = reinterpret_cast<T*>(a.dz) + v0;
+    // element e of the slice lies at buffer[off + e]
+    auto off_of = [&](int64_t n) { return (int)((reinterpret_cast<uintptr_t>(Z + n * a.ld) & 15u) / sizeof(T)); };
+    // chunks of the buffer that a bulk copy may load: not those that reach beyond the row
+    auto load_chunks = [&](int off, int& ca, int& cb) {
+        ca = rank == 0 && off > 0 ? 1 : 0;
+        const int64_t in_row = ((int64_t)off + (a.vocab - v0)) / N;
+        cb = (int)min((int64_t)((off + len + N - 1) / N), in_row);
+        if (cb < ca) cb = ca;
+    };
+    // the broken chunks' elements of row n: thread < 2 N; index in the slice, or -1
+    auto edge_of = [&](int off, int ca, int cb) {
+        const int head = min(len, max(0, ca * N - off)), tail = max(head, cb * N - off);
+        if (tid < N) return tid < head ? tid : -1;
+        if (tid < 2 * N) return tail + tid - N < len ? tail + tid - N : -1;
+        return -1;
+    };
+    auto load = [&](int64_t n, int b) {                                  // thread 0: row n into buffer b
+        const int off = off_of(n);
+        int ca, cb;
+        load_chunks(off, ca, cb);
+        const uint32_t bar = smem_addr(&full[b]);
+        const uint32_t bytes = (uint32_t)(cb - ca) * 16;
+        mbar_arrive_expect_tx(bar, bytes);
+        if (bytes) bulk_load(smem_addr(smem + (size_t)b * f.buf) + ca * 16, Z + n * a.ld - off + ca * N, bytes, bar);
+    };
+    auto edge_load = [&](int64_t n, int& at) {                           // thread < 2 N: its broken chunk's element
+        const int off = off_of(n);
+        int ca, cb;
+        load_chunks(off, ca, cb);
+        at = edge_of(off, ca, cb);
+        const float v = at >= 0 ? elem(Z + n * a.ld + at) : 0.0f;
+        at += off;
+        return v;
+    };
+    auto edge_put = [&](int b, int64_t n, int at, float v) {
+        if (at >= off_of(n)) {
+            const float x[1] = {v};
+            Pack<T, 1>::pack(x).store(reinterpret_cast<T*>(smem + (size_t)b * f.buf) + at);
+        }
+    };
+    // a row's teacher entries of this thread
+    int id_next[J];
+    float t_next[J];
+    float w_next = 0.0f;
+    auto teacher = [&](int64_t n) {
+        w_next = a.weight ? a.weight[n] : 1.0f;
+#pragma unroll
+        for (int q = 0; q < J; ++q) {
+            const int j = tid + q * NT;
+            id_next[q] = -1;
+            t_next[q] = neg_inf();
+            if (j < a.k) {
+                const int64_t at = n * a.k + j;
+                const int64_t id = a.id_bytes == 8 ? reinterpret_cast<const int64_t*>(a.ids)[at]
+                                                   : (int64_t)reinterpret_cast<const int32_t*>(a.ids)[at];
+                const float t = a.teacher[at];
+                if (id >= a.vocab && w_next != 0.0f) record_status(a.status, KAN_ERR_DEVICE_CHECK);
+                if (id >= 0 && id < a.vocab && t != neg_inf()) {
+                    id_next[q] = (int)id;
+                    t_next[q] = t;
+                }
+            }
+        }
+    };
+
+    const int64_t n0 = blockIdx.x / CL;
+    if (n0 < a.n) {
+        int at;
+        float v;
+        if (tid < 2 * N) {
+            v = edge_load(n0, at);
+            edge_put(0, n0, at, v);
+            if (n0 + clusters < a.n) {
+                v = edge_load(n0 + clusters, at);
+                edge_put(1, n0 + clusters, at, v);
+            }
+        }
+        if (tid == 0) {
+            load(n0, 0);
+            if (n0 + clusters < a.n) load(n0 + clusters, 1);
+        }
+        teacher(n0);
+    }
+    __syncthreads();
+    bool waits = true;
+    int it = 0, ex = 0;                                                  // rows so far; exchanges so far
+    for (int64_t n = n0; n < a.n; n += clusters, ++it) {
+        const int b = it & 1;
+        const int64_t after = n + clusters;
+        T* const buf = reinterpret_cast<T*>(smem + (size_t)b * f.buf);
+        const int off = off_of(n), chunks = (off + len + N - 1) / N;
+        int id[J];
+        float t[J], z[J];
+        const float w = w_next;
+        bool any = false;
+#pragma unroll
+        for (int q = 0; q < J; ++q) {
+            id[q] = id_next[q];
+            t[q] = t_next[q];
+            any |= id[q] >= 0;
+        }
+        if (after < a.n) teacher(after);
+        // the row after next goes where the last one was; its broken chunks' elements, ahead
+        const bool refill = it > 0 && after < a.n;
+        int edge_at = -1;
+        float edge_v = 0.0f;
+        if (refill && tid < 2 * N) edge_v = edge_load(after, edge_at);
+        if (waits) waits = mbar_wait(smem_addr(&full[b]), (it >> 1) & 1, a.status);
+
+        // maximum and sum of the slice, each thread's own at first
+        float2 st = make_float2(neg_inf(), 0.0f);
+        if (w != 0.0f) {
+            auto add = [&](const float (&x)[N], float vm) {
+                if (vm > st.x) {
+                    st.y *= term(st.x, vm, a.scale2);                    // 0 for the first one
+                    st.x = vm;
+                }
+                const float ref = st.x == neg_inf() ? 0.0f : st.x;
+                float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+                for (int e = 0; e < N; e += 2) {
+                    s0 += term(x[e], ref, a.scale2);
+                    s1 += term(x[e + 1], ref, a.scale2);
+                }
+                st.y += s0 + s1;
+            };
+            for (int c = tid; c < chunks; c += NT) {
+                float x[N];
+                Pack<T, N>::load(buf + c * N).unpack(x);
+                if (c == 0 || c == chunks - 1) {
+#pragma unroll
+                    for (int e = 0; e < N; ++e) {
+                        const int i = c * N - off + e;
+                        if (i < 0 || i >= len) x[e] = neg_inf();
+                    }
+                }
+                float vm = x[0];
+#pragma unroll
+                for (int e = 1; e < N; ++e) vm = fmaxf(vm, x[e]);
+                add(x, vm);
+            }
+        }
+        float mt = neg_inf();
+#pragma unroll
+        for (int q = 0; q < J; ++q) {
+            const int64_t i = (int64_t)id[q] - v0;
+            z[q] = id[q] >= 0 && i >= 0 && i < len ? elem(buf + off + i) : 0.0f;
+            mt = fmaxf(mt, t[q]);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            const float2 y = make_float2(__shfl_xor_sync(0xffffffffu, st.x, o), __shfl_xor_sync(0xffffffffu, st.y, o));
+            st = both(st, y, a.scale2);
+            mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+        }
+        if (lane == 0) {
+            wstat[warp] = st;
+            wmax[warp] = mt;
+        }
+        // (the row before is stored by now or soon: its buffer takes the row after)
+        if (refill && warp == 0) {
+            if (lane == 0) bulk_wait_read<0>();
+            __syncwarp();
+            if (tid < 2 * N) edge_put(b ^ 1, after, edge_at, edge_v);
+            if (lane == 0) load(after, b ^ 1);
+        }
+        any = __syncthreads_or(any);                                     // 1: partial results are there
+        const bool counts = any && w != 0.0f;
+        float cq = 0.0f, M = 0.0f, S = 1.0f, c = 0.0f, E = 1.0f;
+        if (counts) {
+            const int set = ex & 1;
+            mt = wmax[0];
+            for (int i = 1; i < warps_k; ++i) mt = fmaxf(mt, wmax[i]);
+            if (warp == 0) {                                             // the slice's (m, s) to every block
+                st = lane < WARPS ? wstat[lane] : make_float2(neg_inf(), 0.0f);
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    const float2 y = make_float2(__shfl_xor_sync(0xffffffffu, st.x, o), __shfl_xor_sync(0xffffffffu, st.y, o));
+                    st = both(st, y, a.scale2);
+                }
+                if constexpr (CL > 1) {
+                    if (lane < CL) st_async(peer_addr(smem_addr(&cstat[set][rank]), lane), peer_addr(smem_addr(&met[set]), lane), st);
+                } else {
+                    if (lane == 0) cstat[0][0] = st;
+                }
+            }
+            // the teacher's weights, and the logits at its tokens to block 0
+            float e[J], es = 0.0f;
+            int valid = 0;
+#pragma unroll
+            for (int q = 0; q < J; ++q) {
+                const int j = tid + q * NT;
+                e[q] = id[q] < 0 ? 0.0f : expf((t[q] - mt) * a.inv_temp);
+                es += e[q];
+                valid += id[q] >= 0;
+                if (j < a.k) {
+                    tid_[j] = id[q];
+                    te[j] = e[q];
+                    if constexpr (CL > 1) {
+                        const int64_t i = (int64_t)id[q] - v0;
+                        if (id[q] >= 0 && i >= 0 && i < len)
+                            st_async(peer_addr(smem_addr(zk + set * f.kp + j), 0), peer_addr(smem_addr(&met[set]), 0), z[q]);
+                    }
+                }
+            }
+            if (warp < warps_k) {
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) es += __shfl_xor_sync(0xffffffffu, es, o);
+                if (lane == 0) wsum[warp] = es;
+            }
+            if constexpr (CL > 1) {
+                if (rank == 0) {
+                    const int all = __syncthreads_count(valid & 1) + 2 * __syncthreads_count(valid & 2);
+                    if (tid == 0) mbar_arrive_expect_tx(smem_addr(&met[set]), CL * (int)sizeof(float2) + all * 4);
+                } else if (tid == 0) {
+                    mbar_arrive_expect_tx(smem_addr(&met[set]), CL * (int)sizeof(float2));
+                }
+                if (waits) waits = mbar_wait(smem_addr(&met[set]), (ex >> 1) & 1, a.status);
+            }
+            __syncthreads();                                             // 2: the teacher's entries (and, alone, the sums)
+            float2 tot = cstat[CL > 1 ? set : 0][0];
+#pragma unroll
+            for (int i = 1; i < CL; ++i) tot = both(tot, cstat[set][i], a.scale2);
+            M = tot.x;
+            S = M == neg_inf() ? __int_as_float(0x7fc00000) : tot.y;     // a row of -inf alone has no distribution
+            E = wsum[0];
+            for (int i = 1; i < warps_k; ++i) E += wsum[i];
+            c = w * a.temp;
+            cq = c / S;
+            if (rank == 0) {
+                float l = 0.0f;
+                const float le = logf(E), ls = logf(S);
+#pragma unroll
+                for (int q = 0; q < J; ++q) {
+                    const int j = tid + q * NT;
+                    const float p = e[q] / E;
+                    if (id[q] >= 0 && !(p == 0.0f)) {
+                        const float zj = CL > 1 ? zk[set * f.kp + j] : z[q];
+                        l += p * ((t[q] - mt) * a.inv_temp - le - ((zj - M) * a.inv_temp - ls));
+                    }
+                }
+                if (warp < warps_k) {
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+                    if (lane == 0) wloss[warp] = l;
+                }
+            }
+            ++ex;
+        }
+        // the gradient in the logits' place
+        for (int k = tid; k < chunks; k += NT) {
+            float x[N];
+            Pack<T, N>::load(buf + k * N).unpack(x);
+#pragma unroll
+            for (int e = 0; e < N; ++e) x[e] = counts ? cq * term(x[e], M, a.scale2) : 0.0f;
+            Pack<T, N>::pack(x).store(buf + k * N);
+        }
+        // an entry of this slice that is the first with its id: the sum over the entries with this id
+        float p[J];
+#pragma unroll
+        for (int q = 0; q < J; ++q) {
+            const int j = tid + q * NT;
+            const int64_t i = (int64_t)id[q] - v0;
+            p[q] = -1.0f;
+            if (counts && id[q] >= 0 && i >= 0 && i < len) {
+                float sum = 0.0f;
+                bool first = true;
+                for (int o = 0; o < a.k; ++o) {
+                    if (tid_[o] == id[q]) {
+                        first &= o >= j;
+                        sum += te[o];
+                    }
+                }
+                if (first) p[q] = sum / E;
+            }
+        }
+        __syncthreads();                                                 // 3: the slice is written
+#pragma unroll
+        for (int q = 0; q < J; ++q) {
+            if (!(p[q] == -1.0f)) {
+                const float x[1] = {c * (term(z[q], M, a.scale2) / S - p[q])};
+                Pack<T, 1>::pack(x).store(buf + off + (id[q] - v0));
+            }
+        }
+        if (tid == 0 && rank == 0) {
+            float l = 0.0f;
+            if (counts)
+                for (int i = 0; i < warps_k; ++i) l += wloss[i];
+            a.loss[n] = counts ? w * a.temp * a.temp * l : 0.0f;
+            a.stats[n] = make_float2(counts ? M : 0.0f, counts ? S : 1.0f);
+        }
+        fence_async_smem();
+        __syncthreads();                                                 // 4: the teacher's part too
+        T* const out = G + n * a.ld_grad;
+        const int sa = off > 0 ? 1 : 0, sb = max(sa, (off + len) / N);   // whole chunks of the slice
+        if (tid == 0) {
+            if (sb > sa) bulk_store(out - off + sa * N, smem_addr(buf) + sa * 16, (uint32_t)(sb - sa) * 16);
+            bulk_commit();
+        }
+        const int i = edge_of(off, sa, sb);
+        if (i >= 0) Pack<T, 1>::load(buf + off + i).store(out + i);
+    }
+    if (tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if constexpr (CL > 1) cluster_sync_all();                            // no block leaves while another's logits may arrive
+}
+
 kan_status di_fail(kan_status st, const char* msg) { return set_last_error(st, msg); }
 
 kan_status validate(const kan_distill_shape* s)
@@ -347,6 +743,84 @@ template <typename F32, typename B16> cudaError_t by_type(const kan_distill_shap
     return cudaGetLastError();
 }
 
+// The fused kernel's shape: the fewest blocks a row whose two buffers let two blocks share an SM, else one block an SM;
+// none (0) if not even 8 slices fit, or if the gradient's rows do not begin where the logits' do within 16 bytes.
+struct FusedPlan {
+    int cluster, per, buf, kp;
+    size_t smem;
+};
+FusedPlan plan_of(const kan_distill_shape& s, const void* z, const void* dz)
+{
+    FusedPlan P{};
+    const int64_t esz = s.dtype == KAN_F32 ? 4 : 2, n = 16 / esz;
+    if ((reinterpret_cast<uintptr_t>(z) - reinterpret_cast<uintptr_t>(dz)) % 16 || (s.ld - s.ld_grad) * esz % 16) return P;
+    P.kp = (s.entries + 3) / 4 * 4;
+    for (size_t limit : {(size_t)112 << 10, (size_t)224 << 10}) {
+        for (int cl = 1; cl <= 8; cl *= 2) {
+            const int64_t per = ((s.vocab + cl - 1) / cl + n - 1) / n * n;
+            const int64_t buf = per * esz + 16;
+            const size_t smem = 2 * (size_t)buf + 16 * (size_t)P.kp;
+            if (smem <= limit && per * (cl - 1) < s.vocab) {
+                P.cluster = cl;
+                P.per = (int)per;
+                P.buf = (int)buf;
+                P.smem = smem;
+                return P;
+            }
+        }
+    }
+    return P;
+}
+
+template <typename T, int CL, int NT> cudaError_t launch_fused(const FusedArgs& f, const FusedPlan& P, cudaStream_t st)
+{
+    // clusters that run at once, looked up again when the shared memory or the device differs from the last call's
+    static std::atomic<uint64_t> known{0};
+    auto kernel = distill_fused_kernel<T, CL, NT>;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.blockDim = dim3(NT);
+    cfg.dynamicSmemBytes = P.smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = CL;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const uint64_t key = (uint64_t)P.smem << 8 | (uint64_t)(dev & 0xff);
+    uint64_t got = known.load(std::memory_order_relaxed);
+    int n = (int)(got >> 48);
+    if (!n || (got & 0xffffffffffffull) != key) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 << 10);
+        if (e != cudaSuccess) return e;
+        cfg.gridDim = dim3(CL);
+        e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+        if (e != cudaSuccess) return e;
+        n = std::min(std::max(n, 1), 0x7fff);
+        known.store((uint64_t)n << 48 | key, std::memory_order_relaxed);
+    }
+    cfg.gridDim = dim3((unsigned)(std::min<int64_t>(n, f.d.n) * CL));
+    cfg.numAttrs = CL > 1 ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, kernel, f);
+    if (e == cudaSuccess) count_launch();
+    return e;
+}
+
+template <typename T> cudaError_t fused_of(const FusedArgs& f, const FusedPlan& P, cudaStream_t st)
+{
+    // short rows: more and smaller blocks on an SM, so that other rows' phases fill the barriers of one
+    if (P.cluster == 1 && P.buf <= 16 << 10 && f.d.k <= 256) return launch_fused<T, 1, 128>(f, P, st);
+    switch (P.cluster) {
+    case 1: return launch_fused<T, 1, 512>(f, P, st);
+    case 2: return launch_fused<T, 2, 512>(f, P, st);
+    case 4: return launch_fused<T, 4, 512>(f, P, st);
+    default: return launch_fused<T, 8, 512>(f, P, st);
+    }
+}
+
 }  // namespace
 }  // namespace kan
 
@@ -392,11 +866,26 @@ kan_status kan_distill_loss_grad(const kan_distill_shape* s, const void* z, cons
 {
     kan_status st = validate(s);
     if (st != KAN_OK) return st;
-    if (s->rows > 0 && !dz) return di_fail(KAN_ERR_INVALID_ARG, "a null pointer");
-    if (misaligned(*s, {dz}, nullptr, {})) return di_fail(KAN_ERR_UNSUPPORTED, "operands must be aligned to their elements, stats to 8 bytes");
-    st = kan_distill_forward(s, z, ids, teacher, weight, loss, stats, stream);
-    if (st != KAN_OK) return st;
-    return kan_distill_backward(s, z, ids, teacher, weight, stats, nullptr, dz, stream);
+    if (s->rows == 0) return KAN_OK;
+    if (!z || !ids || !teacher || !loss || !stats || !dz) return di_fail(KAN_ERR_INVALID_ARG, "a null pointer");
+    if (misaligned(*s, {z, dz}, ids, {teacher, weight, loss}) || reinterpret_cast<uintptr_t>(stats) % 8)
+        return di_fail(KAN_ERR_UNSUPPORTED, "operands must be aligned to their elements, stats to 8 bytes");
+    const FusedPlan P = plan_of(*s, z, dz);
+    if (!P.cluster) {
+        st = kan_distill_forward(s, z, ids, teacher, weight, loss, stats, stream);
+        return st == KAN_OK ? kan_distill_backward(s, z, ids, teacher, weight, stats, nullptr, dz, stream) : st;
+    }
+    FusedArgs f{};
+    f.d = args_of(*s, z, ids, teacher, weight);
+    f.d.loss = loss;
+    f.d.stats = reinterpret_cast<float2*>(stats);
+    f.d.dz = dz;
+    f.per = P.per;
+    f.buf = P.buf;
+    f.kp = P.kp;
+    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = s->dtype == KAN_F32 ? fused_of<float>(f, P, cs) : fused_of<__nv_bfloat16>(f, P, cs);
+    return e == cudaSuccess ? KAN_OK : di_fail(KAN_ERR_CUDA, cudaGetErrorString(e));
 }
 
 }  // extern "C"
