@@ -304,6 +304,7 @@ struct FusedArgs {
     int per;                      // elements of a slice (the last one may be shorter): whole chunks
     int buf;                      // bytes of a buffer
     int kp;                       // teacher entries, rounded up to 4
+    int kpow;                     // and to a power of two, at most the block's threads
 };
 
 __device__ __forceinline__ uint32_t cluster_rank()
@@ -344,13 +345,111 @@ __device__ __forceinline__ void bulk_store(void* to, uint32_t from, uint32_t byt
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to), "r"(from), "r"(bytes) : "memory");
 }
 
-// (m, s) of two parts: sums relative to the larger maximum.  A part without elements is (-inf, 0).
-__device__ __forceinline__ float2 both(float2 a, float2 b, float k)
+// A sum kept relative to its own maximum m, relative to M instead (nothing to scale where there is no element).
+__device__ __forceinline__ float rescale(float2 st, float M, float k) { return st.x == neg_inf() ? st.y : st.y * term(st.x, M, k); }
+// (m, s) of the lanes together, in every lane
+template <int LANES> __device__ __forceinline__ float2 join_lanes(float2 st, float k)
 {
-    const float m = fmaxf(a.x, b.x);
-    const float s = (a.x == neg_inf() ? a.y : a.y * term(a.x, m, k)) + (b.x == neg_inf() ? b.y : b.y * term(b.x, m, k));
-    return make_float2(m, s);
+    float M = st.x;
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float s = rescale(st, M, k);
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return make_float2(M, s);
 }
+
+// Two fp32 values in the packed f32x2 instructions.
+__device__ __forceinline__ uint64_t two(float x, float y)
+{
+    uint64_t q;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(q) : "f"(x), "f"(y));
+    return q;
+}
+__device__ __forceinline__ void halves(uint64_t q, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(q)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+__device__ __forceinline__ uint64_t ex2_2(uint64_t q)
+{
+    float x, y;
+    halves(q, x, y);
+    return two(ex2(x), ex2(y));
+}
+// Element pair i of a chunk.
+__device__ __forceinline__ uint64_t pair(const Pack<float, 4>& c, int i) { return two(__uint_as_float(c.word(2 * i)), __uint_as_float(c.word(2 * i + 1))); }
+__device__ __forceinline__ uint64_t pair(const Pack<__nv_bfloat16, 8>& c, int i)
+{
+    return two(__uint_as_float(c.word(i) << 16), __uint_as_float(c.word(i) & 0xFFFF0000u));
+}
+// The largest element (a NaN is passed over; the sums see it).
+__device__ __forceinline__ float chunk_max(const Pack<float, 4>& c)
+{
+    return fmaxf(fmaxf(__uint_as_float(c.q.x), __uint_as_float(c.q.y)), fmaxf(__uint_as_float(c.q.z), __uint_as_float(c.q.w)));
+}
+__device__ __forceinline__ float chunk_max(const Pack<__nv_bfloat16, 8>& c)
+{
+    auto h = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
+    const __nv_bfloat162 m = __hmax2(__hmax2(h(c.q.x), h(c.q.y)), __hmax2(h(c.q.z), h(c.q.w)));
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(&m);
+    return fmaxf(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+// Beyond this magnitude m k may overflow: exponents are then taken from the difference z - m alone.
+constexpr float kLarge = 1e30f;
+
+// A thread's running (m, sum of 2^((z - m) k)) over chunks.  With bf16 logits the exponent is one multiply-add (z k - m k:
+// m k's rounding, 2^-24 of it, is far below what the logits' own type resolves), with fp32 logits the difference first.
+template <typename T> struct Running {
+    static constexpr int N = 16 / (int)sizeof(T);
+    float m = neg_inf(), mk = 0.0f;
+    uint64_t acc = 0;                                    // two partial sums
+    float k;
+    __device__ __forceinline__ void add(const Pack<T, N>& c)
+    {
+        const float vm = chunk_max(c);
+        if (vm > m) {
+            const float f = term(m, vm, k);              // 0 for the first one
+            acc = mul2(acc, two(f, f));
+            m = vm;
+            mk = m * k;
+        }
+        if (fabsf(m) < kLarge) {
+            const uint64_t kk = two(k, k), off = sizeof(T) == 2 ? two(-mk, -mk) : two(-m, -m);
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i)
+                acc = add2(acc, ex2_2(sizeof(T) == 2 ? fma2(pair(c, i), kk, off) : mul2(add2(pair(c, i), off), kk)));
+        } else {
+            const float ref = m == neg_inf() ? 0.0f : m;
+            float x[N], s = 0.0f;
+            c.unpack(x);
+#pragma unroll
+            for (int e = 0; e < N; ++e) s += term(x[e], ref, k);
+            acc = add2(acc, two(s, 0.0f));
+        }
+    }
+    __device__ __forceinline__ float2 get() const
+    {
+        float x, y;
+        halves(acc, x, y);
+        return make_float2(m, x + y);
+    }
+};
 
 template <typename T, int CL, int NT>
 __global__ void __launch_bounds__(NT, NT == 512 ? 2 : 6) distill_fused_kernel(const FusedArgs f)
@@ -363,6 +462,7 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 2 : 6) distill_fused_kernel(co
     float* const zk = te + f.kp;                                                     // [2][kp] block 0: logits at the entries
     __shared__ float2 wstat[WARPS], cstat[2][CL];
     __shared__ float wmax[WARPS], wsum[WARPS], wloss[WARPS];
+    __shared__ int wvalid[WARPS];
     __shared__ uint64_t full[2], met[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = CL > 1 ? (int)cluster_rank() : 0;
@@ -492,38 +592,26 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 2 : 6) distill_fused_kernel(co
         if (waits) waits = mbar_wait(smem_addr(&full[b]), (it >> 1) & 1, a.status);
 
         // maximum and sum of the slice, each thread's own at first
-        float2 st = make_float2(neg_inf(), 0.0f);
+        Running<T> mine;
+        mine.k = a.scale2;
         if (w != 0.0f) {
-            auto add = [&](const float (&x)[N], float vm) {
-                if (vm > st.x) {
-                    st.y *= term(st.x, vm, a.scale2);                    // 0 for the first one
-                    st.x = vm;
-                }
-                const float ref = st.x == neg_inf() ? 0.0f : st.x;
-                float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-                for (int e = 0; e < N; e += 2) {
-                    s0 += term(x[e], ref, a.scale2);
-                    s1 += term(x[e + 1], ref, a.scale2);
-                }
-                st.y += s0 + s1;
-            };
-            for (int c = tid; c < chunks; c += NT) {
+            const int first = off > 0 ? 1 : 0, last = (off + len) / N;    // whole chunks
+#pragma unroll 2
+            for (int c = first + tid; c < last; c += NT) mine.add(Pack<T, N>::load(buf + c * N));
+            if (tid < 2 && (tid == 0 ? first > 0 : last < chunks && last >= first)) {     // the broken ones
+                const int c = tid == 0 ? 0 : last;
+                Pack<T, N> q = Pack<T, N>::load(buf + c * N);
                 float x[N];
-                Pack<T, N>::load(buf + c * N).unpack(x);
-                if (c == 0 || c == chunks - 1) {
+                q.unpack(x);
 #pragma unroll
-                    for (int e = 0; e < N; ++e) {
-                        const int i = c * N - off + e;
-                        if (i < 0 || i >= len) x[e] = neg_inf();
-                    }
+                for (int e = 0; e < N; ++e) {
+                    const int i = c * N - off + e;
+                    if (i < 0 || i >= len) x[e] = neg_inf();
                 }
-                float vm = x[0];
-#pragma unroll
-                for (int e = 1; e < N; ++e) vm = fmaxf(vm, x[e]);
-                add(x, vm);
+                mine.add(Pack<T, N>::pack(x));
             }
         }
+        float2 st = join_lanes<32>(mine.get(), a.scale2);
         float mt = neg_inf();
 #pragma unroll
         for (int q = 0; q < J; ++q) {
@@ -531,11 +619,9 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 2 : 6) distill_fused_kernel(co
             z[q] = id[q] >= 0 && i >= 0 && i < len ? elem(buf + off + i) : 0.0f;
             mt = fmaxf(mt, t[q]);
         }
+        if (warp < warps_k) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const float2 y = make_float2(__shfl_xor_sync(0xffffffffu, st.x, o), __shfl_xor_sync(0xffffffffu, st.y, o));
-            st = both(st, y, a.scale2);
-            mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+            for (int o = 16; o > 0; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
         }
         if (lane == 0) {
             wstat[warp] = st;
@@ -556,12 +642,7 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 2 : 6) distill_fused_kernel(co
             mt = wmax[0];
             for (int i = 1; i < warps_k; ++i) mt = fmaxf(mt, wmax[i]);
             if (warp == 0) {                                             // the slice's (m, s) to every block
-                st = lane < WARPS ? wstat[lane] : make_float2(neg_inf(), 0.0f);
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) {
-                    const float2 y = make_float2(__shfl_xor_sync(0xffffffffu, st.x, o), __shfl_xor_sync(0xffffffffu, st.y, o));
-                    st = both(st, y, a.scale2);
-                }
+                st = join_lanes<WARPS>(lane < WARPS ? wstat[lane] : make_float2(neg_inf(), 0.0f), a.scale2);
                 if constexpr (CL > 1) {
                     if (lane < CL) st_async(peer_addr(smem_addr(&cstat[set][rank]), lane), peer_addr(smem_addr(&met[set]), lane), st);
                 } else {
@@ -590,23 +671,29 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 2 : 6) distill_fused_kernel(co
             if (warp < warps_k) {
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) es += __shfl_xor_sync(0xffffffffu, es, o);
-                if (lane == 0) wsum[warp] = es;
+                valid = __reduce_add_sync(0xffffffffu, valid);
+                if (lane == 0) {
+                    wsum[warp] = es;
+                    wvalid[warp] = valid;
+                }
             }
+            __syncthreads();                                             // 2: the teacher's entries (and, alone, the sums)
             if constexpr (CL > 1) {
-                if (rank == 0) {
-                    const int all = __syncthreads_count(valid & 1) + 2 * __syncthreads_count(valid & 2);
-                    if (tid == 0) mbar_arrive_expect_tx(smem_addr(&met[set]), CL * (int)sizeof(float2) + all * 4);
-                } else if (tid == 0) {
-                    mbar_arrive_expect_tx(smem_addr(&met[set]), CL * (int)sizeof(float2));
+                if (tid == 0) {
+                    int all = 0;
+                    if (rank == 0)
+                        for (int i = 0; i < warps_k; ++i) all += wvalid[i];
+                    mbar_arrive_expect_tx(smem_addr(&met[set]), CL * (int)sizeof(float2) + all * 4);
                 }
                 if (waits) waits = mbar_wait(smem_addr(&met[set]), (ex >> 1) & 1, a.status);
             }
-            __syncthreads();                                             // 2: the teacher's entries (and, alone, the sums)
-            float2 tot = cstat[CL > 1 ? set : 0][0];
+            M = cstat[CL > 1 ? set : 0][0].x;
 #pragma unroll
-            for (int i = 1; i < CL; ++i) tot = both(tot, cstat[set][i], a.scale2);
-            M = tot.x;
-            S = M == neg_inf() ? __int_as_float(0x7fc00000) : tot.y;     // a row of -inf alone has no distribution
+            for (int i = 1; i < CL; ++i) M = fmaxf(M, cstat[set][i].x);
+            S = rescale(cstat[CL > 1 ? set : 0][0], M, a.scale2);
+#pragma unroll
+            for (int i = 1; i < CL; ++i) S += rescale(cstat[set][i], M, a.scale2);
+            if (M == neg_inf()) S = __int_as_float(0x7fc00000);          // a row of -inf alone has no distribution
             E = wsum[0];
             for (int i = 1; i < warps_k; ++i) E += wsum[i];
             c = w * a.temp;
@@ -631,39 +718,75 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 2 : 6) distill_fused_kernel(co
             }
             ++ex;
         }
-        // the gradient in the logits' place
-        for (int k = tid; k < chunks; k += NT) {
-            float x[N];
-            Pack<T, N>::load(buf + k * N).unpack(x);
+        // the gradient in the logits' place (broken chunks too: their elements outside the slice are not stored)
+        if (!counts) {
+            for (int i = tid; i < chunks; i += NT) Pack<T, N>::zero().store(buf + i * N);
+        } else if (sizeof(T) == 2 && fabsf(M) < kLarge && fabsf(cq) > 1.0f / kLarge && fabsf(cq) < kLarge) {
+            // c q = +-2^(z k + (log2 |c / S| - m k)): one multiply-add and one ex2 an element
+            const float shift = log2f(fabsf(cq)) - M * a.scale2;
+            const uint64_t kk = two(a.scale2, a.scale2), add = two(shift, shift);
+            const uint32_t sign = cq < 0.0f ? 0x80008000u : 0u;
+#pragma unroll 2
+            for (int i = tid; i < chunks; i += NT) {
+                const Pack<T, N> q = Pack<T, N>::load(buf + i * N);
+                float x[N];
 #pragma unroll
-            for (int e = 0; e < N; ++e) x[e] = counts ? cq * term(x[e], M, a.scale2) : 0.0f;
-            Pack<T, N>::pack(x).store(buf + k * N);
+                for (int e = 0; e < N / 2; ++e) halves(ex2_2(fma2(pair(q, e), kk, add)), x[2 * e], x[2 * e + 1]);
+                Pack<T, N> r = Pack<T, N>::pack(x);
+                r.q = make_uint4(r.q.x ^ sign, r.q.y ^ sign, r.q.z ^ sign, r.q.w ^ sign);
+                r.store(buf + i * N);
+            }
+        } else {
+            const uint64_t kk = two(a.scale2, a.scale2), mm = two(-M, -M), cc = two(cq, cq);
+#pragma unroll 2
+            for (int i = tid; i < chunks; i += NT) {
+                const Pack<T, N> q = Pack<T, N>::load(buf + i * N);
+                float x[N];
+#pragma unroll
+                for (int e = 0; e < N / 2; ++e) halves(mul2(ex2_2(mul2(add2(pair(q, e), mm), kk)), cc), x[2 * e], x[2 * e + 1]);
+                Pack<T, N>::pack(x).store(buf + i * N);
+            }
         }
-        // an entry of this slice that is the first with its id: the sum over the entries with this id
-        float p[J];
+        // does an id occur twice?  The block's threads share the comparisons: 2^k of them, each with all others' part
+        bool twice = false;
+        if (counts) {
+            const int parts = NT / f.kpow, part = tid / f.kpow;          // (entries beyond kpow: the thread's second one)
+#pragma unroll
+            for (int q = 0; q < J; ++q) {
+                const int j = (tid & (f.kpow - 1)) + q * f.kpow;
+                if (j < a.k && tid_[j] >= 0) {
+                    const int me = tid_[j];
+                    for (int o = part * 4; o < a.k; o += parts * 4) {
+                        const int4 v = *reinterpret_cast<const int4*>(tid_ + o);
+                        twice |= (v.x == me && o != j) | (v.y == me && o + 1 != j && o + 1 < a.k) |
+                                 (v.z == me && o + 2 != j && o + 2 < a.k) | (v.w == me && o + 3 != j && o + 3 < a.k);
+                    }
+                }
+                if (a.k <= f.kpow) break;
+            }
+        }
+        twice = __syncthreads_or(twice);                                 // 3: the slice is written
+        // the teacher's part: an entry of this slice that is the first with its id takes all of them
 #pragma unroll
         for (int q = 0; q < J; ++q) {
             const int j = tid + q * NT;
             const int64_t i = (int64_t)id[q] - v0;
-            p[q] = -1.0f;
             if (counts && id[q] >= 0 && i >= 0 && i < len) {
-                float sum = 0.0f;
+                float sum = te[j];
                 bool first = true;
-                for (int o = 0; o < a.k; ++o) {
-                    if (tid_[o] == id[q]) {
-                        first &= o >= j;
-                        sum += te[o];
+                if (twice) {
+                    sum = 0.0f;
+                    for (int o = 0; o < a.k; ++o) {
+                        if (tid_[o] == id[q]) {
+                            first &= o >= j;
+                            sum += te[o];
+                        }
                     }
                 }
-                if (first) p[q] = sum / E;
-            }
-        }
-        __syncthreads();                                                 // 3: the slice is written
-#pragma unroll
-        for (int q = 0; q < J; ++q) {
-            if (!(p[q] == -1.0f)) {
-                const float x[1] = {c * (term(z[q], M, a.scale2) / S - p[q])};
-                Pack<T, 1>::pack(x).store(buf + off + (id[q] - v0));
+                if (first) {
+                    const float x[1] = {c * (term(z[q], M, a.scale2) / S - sum / E)};
+                    Pack<T, 1>::pack(x).store(buf + off + i);
+                }
             }
         }
         if (tid == 0 && rank == 0) {
@@ -772,8 +895,10 @@ FusedPlan plan_of(const kan_distill_shape& s, const void* z, const void* dz)
     return P;
 }
 
-template <typename T, int CL, int NT> cudaError_t launch_fused(const FusedArgs& f, const FusedPlan& P, cudaStream_t st)
+template <typename T, int CL, int NT> cudaError_t launch_fused(FusedArgs f, const FusedPlan& P, cudaStream_t st)
 {
+    f.kpow = 4;
+    while (f.kpow < f.d.k && f.kpow < NT) f.kpow *= 2;
     // clusters that run at once, looked up again when the shared memory or the device differs from the last call's
     static std::atomic<uint64_t> known{0};
     auto kernel = distill_fused_kernel<T, CL, NT>;
