@@ -419,17 +419,19 @@ def _id_bytes(ids, name="ids"):
 def embed_forward(ids, weight, scale=1.0, y=None):
     """y[..., :] = scale * weight[ids[...], :]; ids int32 or int64 of any shape, weight [rows, dim].  An id outside the
     table gives a row of zeros and is reported by the device status (``_native.kan_sync_status``)."""
-    dtype, code, dev = weight.dtype, _code(weight), weight.get_device()
-    _check(weight, "weight")
-    if weight.dim() != 2:
-        raise ValueError("weight must be [rows, dim]")
+    dev, id_bytes = weight.get_device(), _id_bytes(ids)
+    if not (weight.dim() == 2 and dev >= 0 and weight.is_contiguous() and ids.get_device() == dev and ids.is_contiguous()):
+        _check(weight, "weight")
+        if weight.dim() != 2:
+            raise ValueError("weight must be [rows, dim]")
+        _need(ids, "ids", ids.dtype, ids.shape, dev)
     rows, dim = weight.shape
-    _need(ids, "ids", ids.dtype, ids.shape, dev)
-    s = N.make_embed_shape(ids.numel(), rows, dim, -1, scale, code, code, _id_bytes(ids))
+    code = _code(weight)
     if y is None:
         y = weight.new_empty((*ids.shape, dim))
     else:
-        _need(y, "y", dtype, (*ids.shape, dim), dev)
+        _need(y, "y", weight.dtype, (*ids.shape, dim), dev)
+    s = N.make_embed_shape(ids.numel(), rows, dim, -1, scale, code, code, id_bytes)
     with _on(dev):
         N.kan_embed_forward(s, ids.data_ptr(), weight.data_ptr(), y.data_ptr(), _raw_stream(dev))
     return y
@@ -536,12 +538,12 @@ def glr_forward(x, r, g, decay, h0=None, reset=None, keep=False, y=None, h_last=
     dev = x.get_device()
     B, T, C = x.shape
     if y is None:
-        y = x.new_empty((B, T, C))
+        y = torch.empty_like(x) if x.is_contiguous() else x.new_empty((B, T, C))
     else:
         _need(y, "y", x.dtype, (B, T, C), dev)
     _need(h0, "h0", torch.float32, (B, C), dev)
     if h_last is None:
-        h_last = decay.new_empty((B, C))
+        h_last = decay.new_empty((B, C)) if h0 is None else torch.empty_like(h0)
     elif h_last is not h0:
         _need(h_last, "h_last", torch.float32, (B, C), dev)
     kept = decay.new_empty((B, -(-T // N.KAN_GLR_STEPS), C)) if keep else None
