@@ -64,6 +64,7 @@ struct GlrArgs {
     double* part;                       // [B * cluster][C] partial sums for ddecay, or null
     int64_t B, T, C;
     int strips;                         // of 32 channels
+    int cluster;                        // blocks of a cluster (kernels of 8 warps)
     unsigned int* status;
 };
 
@@ -268,15 +269,15 @@ __device__ __forceinline__ void st_async(uint32_t to, uint32_t bar, float4 v)
 
 // Shared memory of the exchange, two sets used by turns: maps of the block's warps with their sums of y, maps of the
 // cluster's blocks with the mbarrier that counts them.
-template <int W, int CL> struct Meet {
-    float4 warp[2][W][32];           // p, k, b, y
-    float4 block[2][CL][32];         // p, k, b, -
+template <int W> struct Meet {
+    float4 warp[2][W][32];                             // p, k, b, y
+    float4 block[2][W > 1 ? kMaxCluster : 1][32];      // p, k, b, -
     uint64_t full[2];
 };
 
-template <int W, int CL> __device__ __forceinline__ void meet_init(Meet<W, CL>& s)
+template <int W> __device__ __forceinline__ void meet_init(Meet<W>& s, int cl)
 {
-    if constexpr (CL > 1) {
+    if (W > 1 && cl > 1) {
         if (threadIdx.x == 0) {
             mbar_init(smem_addr(&s.full[0]), 1);
             mbar_init(smem_addr(&s.full[1]), 1);
@@ -303,45 +304,43 @@ template <bool CUTS> __device__ __forceinline__ float pass(const float4 (*maps)[
 // (at_barrier runs right before it, past_barrier right after it): a set is written again only two spans later, when all warps have passed the
 // barrier in between, and a block's maps for that span are sent only after it has the whole cluster's of the span in
 // between.  A wait that gives up is recorded; the walk goes on (its results are void) and ends.
-template <int W, int CL, typename At, typename Past>
-__device__ __forceinline__ float exchange(Meet<W, CL>& s, int n, int wpos, int cpos, float y, float b, float& run, bool cuts,
+template <int W, typename At, typename Past>
+__device__ __forceinline__ float exchange(Meet<W>& s, int n, int cl, int wpos, int cpos, float y, float b, float& run, bool cuts,
                                           unsigned int* status, bool& waits, At at_barrier, Past past_barrier)
 {
     const int lane = threadIdx.x & 31, set = n & 1;
     const Map m = map_of(y, b);
     float in = run;
-    if constexpr (W * CL == 1) {
+    if constexpr (W == 1) {
         run = apply<true>(m, run);
     } else {
         s.warp[set][wpos][lane] = make_float4(m.p, m.k, b, y);
         at_barrier();
         __syncthreads();
-        if constexpr (CL > 1) {
-            if (wpos == 0) {
-                const float bt = cuts ? pass<true>(s.warp[set], 0, W, 0.0f) : pass<false>(s.warp[set], 0, W, 0.0f);
-                float yt = 0.0f;
+        if (cl > 1 && wpos == 0) {
+            const float bt = cuts ? pass<true>(s.warp[set], 0, W, 0.0f) : pass<false>(s.warp[set], 0, W, 0.0f);
+            float yt = 0.0f;
 #pragma unroll
-                for (int w = 0; w < W; ++w) {            // a reset cuts off a NaN before it
-                    const float l = s.warp[set][w][lane].w;
-                    yt = l == INFINITY ? l : yt + l;
-                }
-                const Map t = map_of(yt, bt);
-                const uint32_t bar = smem_addr(&s.full[set]), to = smem_addr(&s.block[set][cpos][lane]);
-                if (lane == 0) mbar_arrive_expect_tx(bar, CL * 32 * sizeof(float4));
-#pragma unroll
-                for (int c = 0; c < CL; ++c) st_async(peer_addr(to, c), peer_addr(bar, c), make_float4(t.p, t.k, t.b, 0.0f));
+            for (int w = 0; w < W; ++w) {            // a reset cuts off a NaN before it
+                const float l = s.warp[set][w][lane].w;
+                yt = l == INFINITY ? l : yt + l;
             }
+            const Map t = map_of(yt, bt);
+            const uint32_t bar = smem_addr(&s.full[set]), to = smem_addr(&s.block[set][cpos][lane]);
+            if (lane == 0) mbar_arrive_expect_tx(bar, cl * 32 * (uint32_t)sizeof(float4));
+#pragma unroll 4
+            for (int c = 0; c < cl; ++c) st_async(peer_addr(to, c), peer_addr(bar, c), make_float4(t.p, t.k, t.b, 0.0f));
         }
         past_barrier();
-        if constexpr (CL > 1) {
+        if (cl > 1) {
             if (waits) waits = mbar_wait(smem_addr(&s.full[set]), (n >> 1) & 1, status);
         }
         const float first = run;
         auto states = [&](auto careful) {
             constexpr bool CUTS = decltype(careful)::value;
-            if constexpr (CL > 1) {
+            if (cl > 1) {
                 in = pass<CUTS>(s.block[set], 0, cpos, first);
-                run = pass<CUTS>(s.block[set], cpos, CL, in);
+                run = pass<CUTS>(s.block[set], cpos, cl, in);
                 in = pass<CUTS>(s.warp[set], 0, wpos, in);
             } else {
                 in = pass<CUTS>(s.warp[set], 0, wpos, first);
@@ -483,16 +482,17 @@ template <typename T, bool STAGED, int S, int NA> struct Inputs {
         return r;
     }
 };
-// Forward: S steps a thread, W warps a block, CL blocks a cluster; STAGED: inputs through shared memory (W = 8), else
+// Forward: S steps a thread, W warps a block, a.cluster blocks a cluster; STAGED: inputs through shared memory (W = 8), else
 // into registers.
-template <typename T, bool STAGED, int S, int W, int CL>
+template <typename T, bool STAGED, int S, int W>
 __global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 1) glr_forward_kernel(const GlrArgs a)
 {
     constexpr int N = S > 1 ? 2 : 1;                     // steps side by side
     extern __shared__ __align__(128) char tiles[];       // STAGED: r, g, x
-    __shared__ Meet<W, CL> meet;
-    const Place at(a, CL);
-    constexpr int64_t SPAN = (int64_t)S * W * CL;
+    __shared__ Meet<W> meet;
+    const int side = W > 1 ? a.cluster : 1;              // blocks side by side in time
+    const Place at(a, side);
+    const int64_t SPAN = (int64_t)S * W * side;
     const int64_t mine = (int64_t)at.rank * W * S, first = mine + at.warp * S;   // the block's and the thread's first step
     const int64_t state = at.b * a.C + at.c;
     const T* X = reinterpret_cast<const T*>(a.x) + at.b * a.xb;
@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 1) glr_forward_kernel(con
         }
         in.load(base, a.T, live, set);
     };
-    meet_init(meet);
+    meet_init(meet, side);
     bool waits = true;
     fetch(0, 0);
     zb = zb_next;
@@ -569,7 +569,7 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 1) glr_forward_kernel(con
                 if (i < live) B = fmaf(fa[i], B, bb[i]);
             }
         }
-        float h = exchange<W, CL>(meet, n, at.warp, at.rank, len, B, run, a.reset != nullptr, a.status, waits,
+        float h = exchange<W>(meet, n, side, at.warp, at.rank, len, B, run, a.reset != nullptr, a.status, waits,
             [&] {
                 if constexpr (STAGED) copies_wait();
             },
@@ -606,14 +606,15 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 1) glr_forward_kernel(con
 }
 
 // Backward: the same split, walked from the end of the sequence.
-template <typename T, bool STAGED, int W, int CL>
+template <typename T, bool STAGED, int W>
 __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_backward_kernel(const GlrArgs a)
 {
     constexpr int S = kSteps, N = 2;                     // a thread's steps begin at a kept state
     extern __shared__ __align__(128) char tiles[];       // STAGED: r, g, x, dy
-    __shared__ Meet<W, CL> meet;
-    const Place at(a, CL);
-    constexpr int64_t SPAN = (int64_t)S * W * CL;
+    __shared__ Meet<W> meet;
+    const int side = W > 1 ? a.cluster : 1;              // blocks side by side in time
+    const Place at(a, side);
+    const int64_t SPAN = (int64_t)S * W * side;
     const int64_t mine = (int64_t)at.rank * W * S, first = mine + at.warp * S;
     const int64_t state = at.b * a.C + at.c, end = (a.T - 1) / SPAN * SPAN;      // end: the last span's first step
     const T* X = reinterpret_cast<const T*>(a.x) + at.b * a.xb;
@@ -646,7 +647,7 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_backward_kernel(co
         K -= SPAN / kSteps * a.C;
         in.load(base, a.T, live, set);
     };
-    meet_init(meet);
+    meet_init(meet, side);
     bool waits = true;
     fetch(end, 0);
     zb = zb_next, hb = hb_next;
@@ -712,7 +713,7 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_backward_kernel(co
         }
         if (!STAGED && base > 0) fetch(base - SPAN, 0);
         zb = zb_next, hb = hb_next;
-        float flow = exchange<W, CL>(meet, n, W - 1 - at.warp, CL - 1 - at.rank, len, B, run, a.reset != nullptr, a.status, waits,
+        float flow = exchange<W>(meet, n, side, W - 1 - at.warp, side - 1 - at.rank, len, B, run, a.reset != nullptr, a.status, waits,
             [&] {
                 if constexpr (STAGED) copies_wait();
             },
@@ -761,7 +762,7 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_backward_kernel(co
         if (at.warp == 0 && at.on) {
             double v = 0.0;
             for (int w = 0; w < W; ++w) v += red[w][lane];
-            a.part[(at.b * CL + at.rank) * a.C + at.c] = v;
+            a.part[(at.b * side + at.rank) * a.C + at.c] = v;
         }
     }
 }
@@ -844,40 +845,36 @@ template <typename K> cudaError_t launch(K kernel, int warps, int cluster, size_
     return e;
 }
 
-// The kernels of one direction and operand type: blocks of 8 warps in clusters of 1 to 16, and a block of one warp for
-// sequences of at most 8 steps (and, forward, for a single one).
+// The kernel of one direction and operand type: blocks of 8 warps in clusters of 1 to 16.
 template <typename T, bool STAGED, bool BWD> struct Kernels {
     static constexpr size_t kSmem = STAGED ? 2 * (BWD ? 4 : 3) * Tile<T>::kBytes : 0;
-    static void (*of(int cluster))(const GlrArgs)
+    static void (*kernel())(const GlrArgs)
     {
-        if constexpr (BWD)
-            return cluster == 1 ? glr_backward_kernel<T, STAGED, 8, 1> : cluster == 2 ? glr_backward_kernel<T, STAGED, 8, 2>
-                 : cluster == 4 ? glr_backward_kernel<T, STAGED, 8, 4> : cluster == 8 ? glr_backward_kernel<T, STAGED, 8, 8>
-                 : glr_backward_kernel<T, STAGED, 8, 16>;
-        else
-            return cluster == 1 ? glr_forward_kernel<T, STAGED, kSteps, 8, 1> : cluster == 2 ? glr_forward_kernel<T, STAGED, kSteps, 8, 2>
-                 : cluster == 4 ? glr_forward_kernel<T, STAGED, kSteps, 8, 4> : cluster == 8 ? glr_forward_kernel<T, STAGED, kSteps, 8, 8>
-                 : glr_forward_kernel<T, STAGED, kSteps, 8, 16>;
+        if constexpr (BWD) return glr_backward_kernel<T, STAGED, 8>;
+        else return glr_forward_kernel<T, STAGED, kSteps, 8>;
     }
-    // Blocks of a cluster lie side by side in time.  The size for which the SMs are done first: a wave of blocks takes
-    // its spans times the blocks that share an SM (one alone hides little of its latencies: it counts for two), and a
-    // span a little more with each block whose maps are walked.
+    // Blocks of a cluster lie side by side in time.  Measured (cycles): a block starts in 5000; a span takes a block alone
+    // on its SM 2800 (backward 3700), more of them kIssue each, and 110 for each block whose map is walked.  The size for
+    // which the waves of blocks are done first.
+    static constexpr int64_t kIssue = BWD ? (STAGED ? 2700 : 3100) : (STAGED ? 1500 : 2200), kAlone = BWD ? 3700 : 2800;
     static int cluster_for(const GlrArgs& a)
     {
-        static std::atomic<int> known[5][64];
+        static std::atomic<int> known[kMaxCluster][64];
         const int64_t units = a.B * a.strips, sms = 148;
         int best = 0;
         int64_t cost = -1;
-        for (int i = 0; i < 5; ++i) {
-            const int cl = 1 << i;
-            const int64_t at_once = resident(of(cl), 8, cl, kSmem, known[i]);
+        for (int cl = 1; cl <= kMaxCluster; cl += cl < 8 ? 1 : 8) {
+            if (cl > 1 && (int64_t)8 * kSteps * (cl - 1) >= a.T) break;              // (more blocks than the sequence has steps for)
+            const int64_t at_once = resident(kernel(), 8, cl, kSmem, known[cl - 1]);
             if (at_once < 1) {
                 if (cl > 8) break;
                 return 0;
             }
-            auto shared = [&](int64_t clusters) { return clusters ? std::max<int64_t>(2, (clusters * cl + sms - 1) / sms) : 0; };
-            const int64_t rounds = units / at_once * shared(at_once) + shared(units % at_once);
-            const int64_t c = rounds * ((a.T + 8 * kSteps * cl - 1) / (8 * kSteps * cl)) * (16 + cl);
+            const int64_t spans = (a.T + 8 * kSteps * cl - 1) / (8 * kSteps * cl);
+            auto wave = [&](int64_t clusters) {
+                return clusters ? 5000 + spans * (std::max(kAlone, kIssue * ((clusters * cl + sms - 1) / sms)) + 110 * cl) : 0;
+            };
+            const int64_t c = units / at_once * wave(at_once) + wave(units % at_once);
             if (cost < 0 || c < cost) {
                 cost = c;
                 best = cl;
@@ -885,17 +882,18 @@ template <typename T, bool STAGED, bool BWD> struct Kernels {
         }
         return best;
     }
-    static cudaError_t run(GlrArgs& a, int& cluster, cudaStream_t st)
+    static cudaError_t run(GlrArgs& a, cudaStream_t st)
     {
-        cluster = cluster_for(a);
-        return cluster ? launch(of(cluster), 8, cluster, kSmem, a, st) : cudaErrorInvalidValue;
+        a.cluster = cluster_for(a);
+        return a.cluster ? launch(kernel(), 8, a.cluster, kSmem, a, st) : cudaErrorInvalidValue;
     }
 };
+// A block of one warp for sequences of at most 8 steps (forward, for a single one too).
 template <typename T, bool BWD> cudaError_t run_short(const GlrArgs& a, cudaStream_t st)
 {
-    if constexpr (BWD) return launch(glr_backward_kernel<T, false, 1, 1>, 1, 1, 0, a, st);
-    else if (a.T == 1) return launch(glr_forward_kernel<T, false, 1, 1, 1>, 1, 1, 0, a, st);
-    else return launch(glr_forward_kernel<T, false, kSteps, 1, 1>, 1, 1, 0, a, st);
+    if constexpr (BWD) return launch(glr_backward_kernel<T, false, 1>, 1, 1, 0, a, st);
+    else if (a.T == 1) return launch(glr_forward_kernel<T, false, 1, 1>, 1, 1, 0, a, st);
+    else return launch(glr_forward_kernel<T, false, kSteps, 1>, 1, 1, 0, a, st);
 }
 
 // Inputs go through shared memory where their rows begin on 16 bytes.
@@ -909,16 +907,16 @@ bool staged_ok(const kan_glr_shape& s, const GlrArgs& a)
     return strides % 16 == 0 && in % 16 == 0;
 }
 
-template <typename T, bool BWD> cudaError_t run_type(const kan_glr_shape& s, GlrArgs& a, int& cluster, cudaStream_t st)
+template <typename T, bool BWD> cudaError_t run_type(const kan_glr_shape& s, GlrArgs& a, cudaStream_t st)
 {
     a.strips = (int)((s.channels + 31) / 32);
-    cluster = 1;
+    a.cluster = 1;
     if (a.T <= kSteps) return run_short<T, BWD>(a, st);
-    return staged_ok(s, a) ? Kernels<T, true, BWD>::run(a, cluster, st) : Kernels<T, false, BWD>::run(a, cluster, st);
+    return staged_ok(s, a) ? Kernels<T, true, BWD>::run(a, st) : Kernels<T, false, BWD>::run(a, st);
 }
-template <bool BWD> cudaError_t run(const kan_glr_shape& s, GlrArgs& a, int& cluster, cudaStream_t st)
+template <bool BWD> cudaError_t run(const kan_glr_shape& s, GlrArgs& a, cudaStream_t st)
 {
-    return s.dtype == KAN_F32 ? run_type<float, BWD>(s, a, cluster, st) : run_type<__nv_bfloat16, BWD>(s, a, cluster, st);
+    return s.dtype == KAN_F32 ? run_type<float, BWD>(s, a, st) : run_type<__nv_bfloat16, BWD>(s, a, st);
 }
 
 void common_args(const kan_glr_shape& s, GlrArgs& a)
@@ -977,8 +975,7 @@ kan_status kan_glr_forward(const kan_glr_shape* s, const void* x, const void* r,
     common_args(*s, a);
     a.x = x, a.r = r, a.g = g, a.decay = decay, a.reset = reset, a.h0 = h0;
     a.y = y, a.h_last = h_last, a.kept = kept;
-    int cluster;
-    e = run<false>(*s, a, cluster, cs);
+    e = run<false>(*s, a, cs);
     return e == cudaSuccess ? KAN_OK : gl_fail(KAN_ERR_CUDA, cudaGetErrorString(e));
 }
 
@@ -1010,10 +1007,9 @@ kan_status kan_glr_backward(const kan_glr_shape* s, const void* x, const void* r
             return gl_fail(KAN_ERR_WORKSPACE, "workspace too small");
         a.part = reinterpret_cast<double*>(workspace);
     }
-    int cluster;
-    e = run<true>(*s, a, cluster, cs);
+    e = run<true>(*s, a, cs);
     if (e == cudaSuccess && ddecay) {
-        glr_decay_kernel<<<(unsigned)((s->channels + 127) / 128), 128, 0, cs>>>(a.part, s->batch * cluster, s->channels, decay, ddecay);
+        glr_decay_kernel<<<(unsigned)((s->channels + 127) / 128), 128, 0, cs>>>(a.part, s->batch * a.cluster, s->channels, decay, ddecay);
         count_launch();
         e = cudaGetLastError();
     }
