@@ -1,0 +1,224 @@
+"""The sequence operators together, as a training step and a serving loop use them: token ids through the embedding, KAN
+layers and the gated linear recurrence to logits, the distillation loss, and every parameter's gradient, against the same
+chain in fp64; the refusals of the torch calls on CUDA tensors.
+
+Bar of the chain, normwise per tensor.  A KAN layer's fp32 results are within
+1e-5 (the bar of the layer's own tests).  An error of its input comes out
+multiplied by at most |phi'| / |phi| of a cubic spline of spacing h = 2 / 8,
+2 / h = 8.  Two layers follow one another (the others' errors are far
+smaller), forward and backward: 1e-5 (1 + 8) (1 + 8) = 8e-4, taken as 1e-3.
+"""
+import pytest
+import torch
+
+from kolmogorov_arnold_network_b200 import _native as N
+from kolmogorov_arnold_network_b200 import layer as L
+
+import ref_sequence as ref
+
+pytestmark = pytest.mark.gpu
+
+BAR = 1e-3
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+
+
+def kan64(x, coef, G=8, lo=-1.0, hi=1.0):
+    """The cubic B-spline layer in fp64 by the Cox-de Boor recursion (differentiable)."""
+    h = (hi - lo) / G
+    t = lo + (torch.arange(G + 7, dtype=torch.float64) - 3) * h
+    x = x[..., None]
+    b = ((x >= t[:-1]) & (x < t[1:])).double()
+    for k in range(1, 4):
+        b = (x - t[:-k - 1]) / (k * h) * b[..., :-1] + (t[k + 1:] - x) / (k * h) * b[..., 1:]
+    return torch.einsum("...im,jim->...j", b, coef.double())
+
+
+class Model(torch.nn.Module):
+    def __init__(self, vocab, width, dtype=torch.float32):
+        super().__init__()
+        kw = dict(dtype=dtype, device="cuda")
+        self.embed = L.TokenEmbedding(vocab, width, scale=0.5 * width ** 0.5, **kw)
+        self.x, self.r, self.g = (L.KANLayer(width, width, coef_std=0.3, **kw) for _ in range(3))
+        self.mix = L.GatedLinearRecurrence(width, longest=50.0, device="cuda")
+        self.out = L.KANLayer(width, vocab, coef_std=0.3, **kw)
+        self.loss = L.TopLogitDistillation(2.0)
+
+    def logits(self, ids, reset=None, h0=None):
+        e = self.embed(ids)
+        y, h = self.mix(self.x(e), self.r(e), self.g(e), h0, reset)
+        return self.out(y), h
+
+
+def batch(vocab, seed=0, B=3, T=40, K=6):
+    g = torch.Generator().manual_seed(seed)
+    ids = torch.randint(0, vocab, (B, T), generator=g)
+    reset = torch.rand(B, T, generator=g) < 0.05
+    at = torch.randint(-2, vocab, (B, T, K), generator=g)
+    teacher = torch.randn(B, T, K, generator=g) * 2
+    weight = (torch.rand(B, T, generator=g) < 0.8).float()
+    return ids, reset, at, teacher, weight
+
+
+def near(got, want, bar=BAR):
+    got, want = got.detach().cpu().double(), want.detach()
+    assert float((got - want).norm()) <= bar * float(want.norm()), float((got - want).norm() / want.norm())
+
+
+def test_training_step():
+    torch.manual_seed(1)
+    vocab, width = 150, 32
+    m = Model(vocab, width)
+    ids, reset, at, teacher, weight = batch(vocab)
+    logits, h = m.logits(ids.cuda(), reset.cuda())
+    loss = m.loss(logits, at.cuda(), teacher.cuda(), weight.cuda())
+    loss.backward()
+    p = {k: v.detach().cpu().double().requires_grad_() for k, v in m.named_parameters()}
+    e = p["embed.weight"][ids] * m.embed.scale
+    y, h64 = ref.glr(kan64(e, p["x.coef"]), kan64(e, p["r.coef"]), kan64(e, p["g.coef"]), p["mix.decay"], None, reset)
+    z = kan64(y, p["out.coef"])
+    loss64 = ref.distill(z.reshape(-1, vocab), at.reshape(-1, 6), teacher.reshape(-1, 6), 2.0, weight.reshape(-1)).sum()
+    loss64.backward()
+    near(logits, z)
+    near(h, h64)
+    assert abs(float(loss.detach()) - float(loss64.detach())) <= BAR * float(loss64.detach())
+    for k, v in m.named_parameters():
+        near(v.grad, p[k].grad)
+    # the loss and the logits' gradient in one pass, going on from the logits
+    m.zero_grad()
+    logits, _ = m.logits(ids.cuda(), reset.cuda())
+    flat = logits.reshape(-1, vocab)
+    rows, dz = L.distill_loss_grad(flat.detach(), at.reshape(-1, 6).cuda(), teacher.reshape(-1, 6).cuda(), 2.0, weight.reshape(-1).cuda())
+    flat.backward(dz)
+    assert abs(float(rows.sum()) - float(loss64.detach())) <= BAR * float(loss64.detach())
+    for k, v in m.named_parameters():
+        near(v.grad, p[k].grad)
+    assert N.kan_sync_status(None) == 0
+
+
+def test_bf16_step_runs():
+    m = Model(136, 64, torch.bfloat16)
+    ids, reset, at, teacher, weight = batch(136, seed=3)
+    logits, _ = m.logits(ids.cuda(), reset.cuda())
+    m.loss(logits, at.cuda(), teacher.cuda(), weight.cuda()).backward()
+    for k, v in m.named_parameters():
+        assert v.grad is not None and v.grad.dtype == v.dtype and v.grad.shape == v.shape, k
+        assert bool(v.grad.isfinite().all()) and bool((v.grad != 0).any()), k
+
+
+def test_prompt_then_tokens():
+    """Serving: a prompt's last state, then one token after another, against the whole sequence at once."""
+    torch.manual_seed(2)
+    m = Model(150, 32)
+    ids = torch.randint(0, 150, (5, 24), generator=torch.Generator().manual_seed(4)).cuda()
+    with torch.no_grad():
+        whole, h_whole = m.logits(ids)
+        parts, h = m.logits(ids[:, :15])
+        parts = [parts]
+        h = h.clone()
+        for t in range(15, 24):
+            e = m.embed(ids[:, t])
+            y = m.mix.step(m.x(e), m.r(e), m.g(e), h)
+            parts.append(m.out(y)[:, None])
+    # the same fp32 arithmetic, composed at other places: within the recurrence's and the layer's own bars
+    near(torch.cat(parts, 1), whole.cpu().double())
+    near(h, h_whole.cpu().double(), 1e-5)
+
+
+def test_refusals():
+    c = dict(device="cuda")
+    ids, W = torch.zeros(4, dtype=torch.int64), torch.zeros(6, 8, **c)
+    with pytest.raises(ValueError, match="ids"):
+        L.embed_forward(ids, W)
+    with pytest.raises(TypeError, match="int32 or int64"):
+        L.embed_forward(ids.cuda().float(), W)
+    with pytest.raises(ValueError, match="contiguous"):
+        L.embed_forward(ids.cuda(), W.t())
+    with pytest.raises(ValueError, match="rows, dim"):
+        L.embed_forward(ids.cuda(), W[0])
+    with pytest.raises(TypeError, match="dtype"):
+        L.embed_forward(ids.cuda(), W.double())
+    with pytest.raises(ValueError, match="shape"):
+        L.embed_forward(ids.cuda(), W, y=torch.zeros(3, 8, **c))
+    with pytest.raises(ValueError, match="dY"):
+        L.embed_backward(ids.cuda(), torch.zeros(3, 8, **c), 6)
+    with pytest.raises(TypeError, match="grad_dtype"):
+        L.embed_backward(ids.cuda(), torch.zeros(4, 8, **c), 6, grad_dtype=torch.float64)
+    with pytest.raises(N.KanError, match="padding_idx"):
+        L.embed_backward(ids.cuda(), torch.zeros(4, 8, **c), 6, padding_idx=6)
+    with pytest.raises(N.KanError, match="workspace"):
+        L.embed_backward(ids.cuda(), torch.zeros(4, 8, **c), 6, ws=torch.zeros(16, dtype=torch.uint8, **c))
+    x, d = torch.zeros(2, 5, 8, **c), torch.zeros(8, **c)
+    with pytest.raises(ValueError, match="r has shape"):
+        L.glr_forward(x, x[:, :4], x, d)
+    with pytest.raises(TypeError, match="g has dtype"):
+        L.glr_forward(x, x, x.bfloat16(), d)
+    with pytest.raises(ValueError, match="contiguous"):
+        L.glr_forward(x.transpose(1, 2), x.transpose(1, 2), x.transpose(1, 2), torch.zeros(5, **c))
+    with pytest.raises(TypeError, match="decay"):
+        L.glr_forward(x, x, x, d.double())
+    with pytest.raises(ValueError, match="decay"):
+        L.glr_forward(x, x, x, d[:7])
+    with pytest.raises(TypeError, match="reset"):
+        L.glr_forward(x, x, x, d, reset=torch.zeros(2, 5, **c))
+    with pytest.raises(ValueError, match="h0"):
+        L.glr_forward(x, x, x, d, h0=torch.zeros(2, 7, **c))
+    with pytest.raises(ValueError, match="h0"):
+        L.glr_forward(x, x, x, d, h0=torch.zeros(2, 8))
+    _, _, kept = L.glr_forward(x, x, x, d, keep=True)
+    with pytest.raises(ValueError, match="kept"):
+        L.glr_backward(x, x, x, d, kept[:1], x)
+    with pytest.raises(ValueError, match="dY"):
+        L.glr_backward(x, x, x, d, kept, x[:, :3])
+    z, at, t = torch.zeros(3, 20, **c), torch.zeros(3, 4, dtype=torch.int64, **c), torch.zeros(3, 4, **c)
+    with pytest.raises(ValueError, match="ids"):
+        L.distill_forward(z, at[:2], t)
+    with pytest.raises(ValueError, match="teacher"):
+        L.distill_forward(z, at, t[:, :3])
+    with pytest.raises(TypeError, match="teacher"):
+        L.distill_forward(z, at, t.bfloat16())
+    with pytest.raises(ValueError, match="weight"):
+        L.distill_forward(z, at, t, weight=torch.zeros(2, **c))
+    with pytest.raises(ValueError, match="contiguous"):
+        L.distill_forward(torch.zeros(20, 3, **c).t(), at, t)
+    with pytest.raises(ValueError, match="overlap"):
+        L.distill_forward(z[:1].expand(3, 20), at, t)
+    with pytest.raises(N.KanError, match="1024"):
+        L.distill_forward(z, at[:, :1].expand(3, 1025).contiguous(), t[:, :1].expand(3, 1025).contiguous())
+    with pytest.raises(N.KanError, match="temperature"):
+        L.distill_forward(z, at, t, 0.0)
+    with pytest.raises(ValueError, match="dlogits"):
+        L.distill_loss_grad(z, at, t, dlogits=torch.zeros(3, 21, **c))
+
+
+def test_other_streams_and_two_calls_at_once():
+    """Calls on two streams side by side share nothing: each result as on its own."""
+    torch.manual_seed(5)
+    sets = []
+    for k in range(2):
+        x, r, g, dy = (torch.randn(4, 600, 64, device="cuda").bfloat16() for _ in range(4))
+        ids = torch.randint(0, 300, (3000,), device="cuda")
+        de = torch.randn(3000, 48, device="cuda")
+        z, at, t = torch.randn(64, 9001, device="cuda"), torch.randint(0, 9001, (64, 8), device="cuda"), torch.randn(64, 8, device="cuda")
+        sets.append((x, r, g, torch.randn(64, device="cuda") - 2, dy, ids, de, z, at, t))
+
+    def work(x, r, g, d, dy, ids, de, z, at, t):
+        y, h, kept = L.glr_forward(x, r, g, d, keep=True)
+        return [y, h, *L.glr_backward(x, r, g, d, kept, dy)[:4], L.embed_backward(ids, de, 300), *L.distill_loss_grad(z, at, t)]
+
+    alone = [work(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    both = []
+    for _ in range(3):
+        both.clear()
+        for s, st in zip(sets, streams):
+            with torch.cuda.stream(st):
+                both.append(work(*s))
+        torch.cuda.synchronize()
+        for a, b in zip(alone, both):
+            assert all(torch.equal(u, v) for u, v in zip(a, b))
