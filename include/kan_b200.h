@@ -433,7 +433,7 @@ typedef struct {
     int64_t ld, ld_grad;  /* row strides of z and dz (elements) */
     int32_t entries;      /* teacher entries per row, 1..1024 */
     int32_t id_bytes;     /* 4 or 8 */
-    float temperature;    /* > 0, finite */
+    float temperature;    /* 1e-6..1e6 */
     int32_t dtype;        /* kan_dtype of z, dz */
 } kan_distill_shape;
 

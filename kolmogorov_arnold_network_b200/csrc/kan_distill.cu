@@ -162,28 +162,37 @@ __device__ __forceinline__ float chunk_max(const Pack<__nv_bfloat16, 8>& c)
     return fmaxf(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
-// Beyond this magnitude m k may overflow: exponents are then taken from the difference z - m alone.
+// Above this magnitude (an infinity too) exponents are taken one by one, from the difference z - m.
 constexpr float kLarge = 1e30f;
+// bf16 logits: up to this |m k| an exponent is one multiply-add, z k - q with q = m k rounded, and what all terms got too
+// much by that rounding (2^-5 in the exponent at most) goes out of their sum at the end.
+constexpr float kLargeExp = 1 << 20;
+// Gradients in bf16: up to this |m k| its rounding and that of the sum it enters, 2^-18 in the exponent each, are as small
+// as the other fp32 roundings.
+constexpr float kLargeOut = 128.0f;
 
-// A thread's running (m, sum of 2^((z - m) k)) over chunks.  With bf16 logits the exponent is one multiply-add (z k - m k:
-// m k's rounding, 2^-24 of it, is far below what the logits' own type resolves), with fp32 logits the difference first.
+// A thread's running (m, sum of 2^((z - m) k)) over chunks; within, the sum is relative to 2^q (bf16) or to m (fp32).
 template <typename T> struct Running {
     static constexpr int N = 16 / (int)sizeof(T);
-    float m = neg_inf(), mk = 0.0f;
+    float m = neg_inf(), mk = neg_inf();                 // mk: m k rounded
     uint64_t acc = 0;                                    // two partial sums
     float k;
+    __device__ __forceinline__ bool quick() const { return sizeof(T) == 2 ? fabsf(mk) < kLargeExp : fabsf(m) < kLarge; }
+    // what makes the sum relative to m: 2^(q - m k)
+    __device__ __forceinline__ float to_m() const { return sizeof(T) == 2 && quick() ? ex2(-fmaf(m, k, -mk)) : 1.0f; }
     template <int U> __device__ __forceinline__ void add(const Pack<T, N> (&c)[U])
     {
         float vm = chunk_max(c[0]);
 #pragma unroll
         for (int u = 1; u < U; ++u) vm = fmaxf(vm, chunk_max(c[u]));
         if (vm > m) {
-            const float f = term(m, vm, k);              // 0 for the first one
-            acc = mul2(acc, two(f, f));
+            float f = to_m() * term(m, vm, k);           // 0 for the first one
             m = vm;
             mk = m * k;
+            if (sizeof(T) == 2 && quick()) f *= ex2(fmaf(m, k, -mk));
+            acc = mul2(acc, two(f, f));
         }
-        if (fabsf(m) < kLarge) {
+        if (quick()) {
             const uint64_t kk = two(k, k), off = sizeof(T) == 2 ? two(-mk, -mk) : two(-m, -m);
             uint64_t part[U] = {};
 #pragma unroll
@@ -210,7 +219,7 @@ template <typename T> struct Running {
     {
         float x, y;
         halves(acc, x, y);
-        return make_float2(m, x + y);
+        return make_float2(m, (x + y) * to_m());
     }
 };
 
@@ -455,7 +464,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(const DistArgs a
                         if (i + u * NT < to) store_last<T, N>(to_ + (int64_t)(i + u * NT) * N, fn(q[u]));
                 }
             };
-            if (sizeof(T) == 2 && fabsf(M) < kLarge && fabsf(cq) > 1.0f / kLarge && fabsf(cq) < kLarge) {
+            if (sizeof(T) == 2 && fabsf(M * a.scale2) < kLargeOut && fabsf(cq) > 1.0f / kLarge && fabsf(cq) < kLarge) {
                 // c q = +-2^(z k + (log2 |c / S| - m k)): one multiply-add and one ex2 an element
                 const float shift = log2f(fabsf(cq)) - M * a.scale2;
                 const uint64_t kk = two(a.scale2, a.scale2), add = two(shift, shift);
@@ -552,6 +561,8 @@ kan_status validate(const kan_distill_shape* s)
     if (s->id_bytes != 4 && s->id_bytes != 8) return di_fail(KAN_ERR_INVALID_ARG, "id_bytes must be 4 or 8");
     if (!(s->temperature > 0.0f) || !(s->temperature - s->temperature == 0.0f))
         return di_fail(KAN_ERR_INVALID_ARG, "temperature must be positive and finite");
+    if (s->temperature < 1e-6f || s->temperature > 1e6f)                 // (T^2, 1 / T and their products stay in range)
+        return di_fail(KAN_ERR_UNSUPPORTED, "temperature outside 1e-6..1e6");
     if (s->entries > kMaxK) return di_fail(KAN_ERR_UNSUPPORTED, "more than 1024 teacher entries per row");
     if (s->rows > ((int64_t)1 << 31) - 1 || s->vocab > ((int64_t)1 << 30)) return di_fail(KAN_ERR_UNSUPPORTED, "sizes too large");
     return KAN_OK;

@@ -319,3 +319,17 @@ def test_two_captured_graphs():
         gr.replay()
         torch.cuda.synchronize()
         check(*out, (z, ids, t, 1.0, w))
+
+
+@pytest.mark.parametrize("temp", [1e-6, 1e-3, 0.03, 40.0, 1e6])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_extreme_temperatures(dt, temp):
+    """Cold: exponents of thousands (within `bounds` an element counts by its own probability, however large z / T is);
+    hot: nearly uniform.  The reference takes the temperature as the library does, in fp32."""
+    temp = float(torch.tensor(temp))
+    for n, vocab, k in ((6, 700, 5), (3, 40003, 9)):
+        args = draw(n, vocab, k, dt, seed=17)
+        args = (args[0], args[1], args[2], temp, args[3])
+        loss, dz, loss2, dz2 = run(*args)
+        check(loss, dz, args)
+        check(loss2, dz2, args)

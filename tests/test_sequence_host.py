@@ -161,3 +161,9 @@ def test_distill_python_refusals():
         L.TopLogitDistillation(0.0)
     with pytest.raises(ValueError, match="reduction"):
         L.TopLogitDistillation(1.0, "mean")
+
+
+@pytest.mark.parametrize("t", [1e-7, 1e-30, 2e6, 3e38])
+def test_distill_temperature_range(lib, t):
+    assert distill_calls(lib, ctypes.byref(distill(temperature=t))) == (2,) * 3
+    assert "1e-6..1e6" in lib.kan_last_error().decode()
