@@ -672,6 +672,7 @@ kan_status kan_distill_backward(const kan_distill_shape* s, const void* z, const
     if (!z || !ids || !teacher || !stats || !dz) return di_fail(KAN_ERR_INVALID_ARG, "a null pointer");
     if (misaligned(*s, {z, dz}, ids, {teacher, weight, dloss}) || reinterpret_cast<uintptr_t>(stats) % 8)
         return di_fail(KAN_ERR_UNSUPPORTED, "operands must be aligned to their elements, stats to 8 bytes");
+    if (z == dz && s->ld != s->ld_grad) return di_fail(KAN_ERR_INVALID_ARG, "dz in place of z needs its row stride");
     DistArgs a = args_of(*s, z, ids, teacher, weight);
     a.stats = reinterpret_cast<float2*>(const_cast<float*>(stats));
     a.dloss = dloss;
@@ -688,6 +689,7 @@ kan_status kan_distill_loss_grad(const kan_distill_shape* s, const void* z, cons
     if (!z || !ids || !teacher || !loss || !stats || !dz) return di_fail(KAN_ERR_INVALID_ARG, "a null pointer");
     if (misaligned(*s, {z, dz}, ids, {teacher, weight, loss}) || reinterpret_cast<uintptr_t>(stats) % 8)
         return di_fail(KAN_ERR_UNSUPPORTED, "operands must be aligned to their elements, stats to 8 bytes");
+    if (z == dz && s->ld != s->ld_grad) return di_fail(KAN_ERR_INVALID_ARG, "dz in place of z needs its row stride");
     DistArgs a = args_of(*s, z, ids, teacher, weight);
     a.loss = loss;
     a.stats = reinterpret_cast<float2*>(stats);

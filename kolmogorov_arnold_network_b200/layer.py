@@ -697,7 +697,8 @@ def distill_loss_grad(logits, ids, teacher, temperature=1.0, weight=None, dlogit
 class _DistillFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, ids, teacher, temperature, weight):
-        logits = logits if logits.stride(-1) == 1 else logits.contiguous()
+        if logits.stride(1) != 1 or (logits.shape[0] > 1 and logits.stride(0) < logits.shape[1]):    # (repeated rows too)
+            logits = logits.contiguous()
         loss, stats = distill_forward(logits, ids, teacher, temperature, weight)
         ctx.save_for_backward(logits, ids, teacher, stats, weight)
         ctx.temperature = temperature
@@ -718,8 +719,8 @@ class TopLogitDistillation(torch.nn.Module):
 
     def __init__(self, temperature=1.0, reduction="sum"):
         super().__init__()
-        if not temperature > 0 or not math.isfinite(temperature):
-            raise ValueError("temperature must be positive and finite")
+        if not 1e-6 <= temperature <= 1e6:
+            raise ValueError("temperature must lie in 1e-6..1e6")
         if reduction not in ("sum", "none"):
             raise ValueError("reduction must be 'sum' or 'none'")
         self.temperature, self.reduction = float(temperature), reduction

@@ -333,3 +333,15 @@ def test_extreme_temperatures(dt, temp):
         loss, dz, loss2, dz2 = run(*args)
         check(loss, dz, args)
         check(loss2, dz2, args)
+
+
+def test_module_repeated_rows():
+    """Logits broadcast over rows: every row counts, their gradients meet in the one row."""
+    z, ids, t, w = draw(4, 300, 5, "f32", seed=9)
+    leaf = z[:1].cuda().requires_grad_()
+    L.TopLogitDistillation(2.0)(leaf.expand(4, 300), ids.cuda(), t.cuda(), w.cuda()).backward()
+    rows = z[:1].expand(4, 300).contiguous()
+    _, wd = reference(rows, ids, t, 2.0, w)
+    _, bd = bounds(rows, ids, t, 2.0, w)
+    bar = (kappa(300) + 4) * U32 * bd.sum(0) + 1e-37                      # four rows added in fp32
+    assert bool(((leaf.grad[0].cpu().double() - wd.sum(0)).abs() <= bar).all())

@@ -167,3 +167,9 @@ def test_distill_python_refusals():
 def test_distill_temperature_range(lib, t):
     assert distill_calls(lib, ctypes.byref(distill(temperature=t))) == (2,) * 3
     assert "1e-6..1e6" in lib.kan_last_error().decode()
+
+
+def test_distill_in_place_needs_one_stride(lib):
+    s = ctypes.byref(distill(ld=120))
+    assert distill_calls(lib, s)[1:] == (1, 1)
+    assert "stride" in lib.kan_last_error().decode()
