@@ -376,7 +376,7 @@ KAN_API kan_status kan_embed_backward(const kan_embed_shape* s, const void* ids,
  * [batch, channels] float32; reset [batch, time] bytes, or NULL.
  * kept [batch, ceil(time / KAN_GLR_STEPS), channels] float32: the states that
  * the forward keeps for the backward (NULL: none).  Operands need the
- * alignment of their elements only; any channels.
+ * alignment of their elements only; up to 2^20 channels.
  * ------------------------------------------------------------------------ */
 #define KAN_GLR_STEPS 8
 
@@ -446,8 +446,8 @@ KAN_API kan_status kan_distill_backward(const kan_distill_shape* s, const void* 
                                         const float* weight, const float* stats, const float* dloss, void* dz,
                                         void* stream);
 
-/* Both at once, for a training step whose loss is the sum of loss[] (dloss = 1): the logits are read once where a row
- * fits the shared memory of a cluster. */
+/* Both at once, for a training step whose loss is the sum of loss[] (dloss = 1): the logits come from HBM once, the second
+ * reading of a row from L2. */
 KAN_API kan_status kan_distill_loss_grad(const kan_distill_shape* s, const void* z, const void* ids,
                                          const float* teacher, const float* weight, float* loss, float* stats, void* dz,
                                          void* stream);

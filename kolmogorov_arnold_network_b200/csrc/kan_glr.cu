@@ -45,7 +45,7 @@ namespace {
 constexpr int kSteps = 8;         // steps per thread, and the spacing of the kept states
 
 constexpr int kMaxCluster = 16;   // blocks of a cluster
-constexpr int64_t kMaxStride = 1 << 20;   // elements from a step to the next: a span of 512 steps stays within 32 bits of bytes
+constexpr int64_t kMaxChannels = 1 << 20, kMaxStride = (int64_t)1 << 40;     // (strides of steps, in elements)
 
 struct GlrArgs {
     const void *x, *r, *g;
@@ -792,9 +792,9 @@ kan_status validate(const kan_glr_shape* s)
     for (int64_t v : st)
         if (v < 0) return gl_fail(KAN_ERR_INVALID_ARG, "negative stride");
     for (int i = 1; i < 6; i += 2)
-        if (st[i] > kMaxStride) return gl_fail(KAN_ERR_UNSUPPORTED, "a stride of steps above 2^20 elements");
-    if (s->channels > kMaxStride || s->time > ((int64_t)1 << 40) || s->batch > ((int64_t)1 << 31) ||
-        s->batch * ((s->channels + 31) / 32) > ((int64_t)1 << 27))
+        if (st[i] > kMaxStride) return gl_fail(KAN_ERR_UNSUPPORTED, "a stride of steps above 2^40 elements");
+    if (s->channels > kMaxChannels || s->time > ((int64_t)1 << 40) || s->batch > ((int64_t)1 << 31) ||
+        s->batch * ((s->channels + 31) / 32) >= ((int64_t)1 << 27))
         return gl_fail(KAN_ERR_UNSUPPORTED, "sizes too large");
     return KAN_OK;
 }

@@ -308,3 +308,16 @@ def test_two_captured_graphs():
     torch.cuda.synchronize()
     for gr, d, dev, out in graphs:
         check(out, reference(d), bounds_of(d))
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_steps_far_apart(dt):
+    """Time-major inputs of a large batch: more than a million elements from a step to the next."""
+    d = draw(2, 21, 32, dt, seed=12)
+    far = dict(d)
+    for k in "xrg":
+        buf = torch.zeros(21, (1 << 20) + 48, dtype=d[k].dtype, device="cuda")
+        view = buf.as_strided((2, 21, 32), (32, (1 << 20) + 48, 1))
+        view.copy_(d[k])
+        far[k] = view
+    check(run(far), reference(d), bounds_of(d))

@@ -173,3 +173,8 @@ def test_distill_in_place_needs_one_stride(lib):
     s = ctypes.byref(distill(ld=120))
     assert distill_calls(lib, s)[1:] == (1, 1)
     assert "stride" in lib.kan_last_error().decode()
+
+
+@pytest.mark.parametrize("kw", [dict(x_strides=(32, 1 << 41)), dict(channels=(1 << 20) + 1), dict(batch=1 << 27)])
+def test_glr_limits(lib, kw):
+    assert glr_calls(lib, ctypes.byref(glr(**kw))) == (2, 2)
