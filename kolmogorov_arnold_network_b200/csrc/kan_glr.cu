@@ -287,6 +287,13 @@ template <int W> __device__ __forceinline__ void meet_init(Meet<W>& s, int cl)
     }
 }
 
+// A thread whose wait gave up stays until the cluster's other threads have ended: they may still send to its block.  (Threads
+// that have ended count as arrived.)
+__device__ __forceinline__ void meet_end(bool waits)
+{
+    if (!waits) asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
 // The state past the maps from <= i < to.
 template <bool CUTS> __device__ __forceinline__ float pass(const float4 (*maps)[32], int from, int to, float h)
 {
@@ -333,7 +340,7 @@ __device__ __forceinline__ float exchange(Meet<W>& s, int n, int cl, int wpos, i
         }
         past_barrier();
         if (cl > 1) {
-            if (waits) waits = mbar_wait(smem_addr(&s.full[set]), (n >> 1) & 1, status);
+            if (waits) waits = mbar_wait_cluster(smem_addr(&s.full[set]), (n >> 1) & 1, status);
         }
         const float first = run;
         auto states = [&](auto careful) {
@@ -603,6 +610,7 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 1) glr_forward_kernel(con
         Y += SPAN * a.C;
     }
     if (a.h_last && at.on && at.rank == 0 && at.warp == 0) a.h_last[state] = run;
+    if constexpr (W > 1) meet_end(waits);
 }
 
 // Backward: the same split, walked from the end of the sequence.
@@ -765,6 +773,7 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_backward_kernel(co
             a.part[(at.b * side + at.rank) * a.C + at.c] = v;
         }
     }
+    if constexpr (W > 1) meet_end(waits);
 }
 
 // ddecay from the partial sums of dL L, in their order.

@@ -8,6 +8,10 @@ multiplied by at most |phi'| / |phi| of a cubic spline of spacing h = 2 / 8,
 2 / h = 8.  Two layers follow one another (the others' errors are far
 smaller), forward and backward: 1e-5 (1 + 8) (1 + 8) = 8e-4, taken as 1e-3.
 """
+import pathlib
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -222,3 +226,64 @@ def test_other_streams_and_two_calls_at_once():
         torch.cuda.synchronize()
         for a, b in zip(alone, both):
             assert all(torch.equal(u, v) for u, v in zip(a, b))
+
+
+FIRST = """
+import torch
+from kolmogorov_arnold_network_b200 import _native as N, layer as L
+torch.manual_seed(0)
+x, r, g, dy = (torch.randn(2, 700, 64, device="cuda") for _ in range(4))
+d, ids = torch.randn(64, device="cuda"), torch.randint(0, 99, (9000,), device="cuda")
+de = torch.randn(9000, 64, device="cuda")
+z, at, t = torch.randn(7, 70001, device="cuda"), torch.randint(0, 70001, (7, 8), device="cuda"), torch.randn(7, 8, device="cuda")
+def work():
+    y, h, kept = L.glr_forward(x, r, g, d, keep=True)
+    return [y, h, *L.glr_backward(x, r, g, d, kept, dy), L.embed_forward(ids, de[:99]), L.embed_backward(ids, de, 99),
+            *L.distill_loss_grad(z, at, t)]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = work()
+for _ in range(2):
+    graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(out, work()))
+assert N.kan_sync_status(None) == 0
+print("as eager")
+"""
+
+
+def test_first_calls_of_a_process_captured():
+    """What the library looks up at its first call (kernels, their attributes, the device's limits) can be looked up while a
+    graph is being captured."""
+    root = pathlib.Path(__file__).resolve().parent.parent
+    got = subprocess.run([sys.executable, "-c", FIRST], cwd=root, capture_output=True, text=True, timeout=300)
+    assert got.returncode == 0 and "as eager" in got.stdout, got.stderr[-2000:]
+
+
+def test_backward_captured_beside_an_eager_graph():
+    """A training step's backward in a captured graph, by the torch calls (no autograd state is touched), while an eager
+    graph of the same table and decay is alive and used afterwards."""
+    torch.manual_seed(7)
+    emb, mix = L.TokenEmbedding(50, 32, device="cuda"), L.GatedLinearRecurrence(32, device="cuda")
+    ids = torch.randint(0, 50, (2, 90), device="cuda")
+    e = emb(ids)
+    y, _ = mix(e, e, e)                                                   # the eager graph
+    dy = torch.randn_like(y)
+
+    def step():
+        x = L.embed_forward(ids, emb.weight.detach(), emb.scale)
+        _, _, kept = L.glr_forward(x, x, x, mix.decay.detach(), keep=True)
+        dx, dr, dg, dd, _ = L.glr_backward(x, x, x, mix.decay.detach(), kept, dy)
+        return L.embed_backward(ids, dx + dr + dg, 50, emb.scale), dd
+
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dw, dd = step()
+    graph.replay()
+    y.backward(dy)
+    torch.cuda.synchronize()
+    assert torch.equal(dd, mix.decay.grad)
+    # the three gradients meet in another order in autograd: two roundings of fp32 each way
+    near(dw, emb.weight.grad.cpu().double(), 1e-6)
