@@ -239,7 +239,7 @@ template <typename T, int NT, int CL, Mode MODE>
 __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(const DistArgs a)
 {
     using R = RowSplit<T>;
-    constexpr int N = R::N, WARPS = NT / 32, J = NT == 128 ? 2 : kMaxK / NT;      // at most J entries a thread
+    constexpr int N = R::N, WARPS = NT / 32, J = NT < 256 ? 2 : kMaxK / NT;       // at most J entries a thread
     constexpr int U = 6;                                                 // vectors that a thread takes at once
     __shared__ __align__(16) int32_t tid_[MODE == kLoss ? 1 : J * NT];                 // ids of the entries, -1: none
     __shared__ float te[MODE == kLoss ? 1 : J * NT];                     // exp((t - max) / T)
@@ -618,14 +618,30 @@ template <typename T, int NT, int CL, Mode MODE> cudaError_t launch(DistArgs a, 
     return e;
 }
 
-// Blocks per row: as many as keep the rows in flight below half of L2 (where the row is read twice), and as many as fill the
-// SMs where there are few rows; short rows go to small blocks.
+// Threads per row.  A row's reductions and barriers take a time of their own, so that the more rows an SM has in flight the
+// better (small blocks), until a thread's share of a row grows long, and with the gradient as long as the rows in flight stay
+// below half of L2 (large blocks, clusters).  Measured, rows of bf16 logits, loss and gradient, us with 32 | 64 | 128 | 256
+// threads: 16384 x 1000 26 | 50 | 77 | 136, 16384 x 4000 77 | 89 | 114 | 196, 8192 x 8000 68 | 64 | 80 | 105,
+// 8192 x 16000 134 | 114 | 113 | 149, 8192 x 24000 205 | 182 | 158 | 184, 8192 x 50257 429 | 419 | 367 | 326; the loss alone:
+// 16384 x 1000 15 | 30 | 45 | 88, 8192 x 24000 72 | 69 | 75 | 90, 8192 x 50257 140 | 137 | 138 | 156.  With few rows (at most
+// as many as run at once) wider blocks: 600 x 4000 8.3 | 7.9 | 7.3 | 11.4.
+// Blocks of 256 per row: as many as keep the rows in flight below half of L2 (2048 x 200000: 334 us with four, 399 with one),
+// and as many as fill the SMs where there are few rows (16 x 50257: 8.6 us against 11.9 with one).
+constexpr int64_t kThreadsAtOnce = 148 * 1024, kHalfL2 = (int64_t)63 << 20;
 template <typename T, Mode MODE> cudaError_t run_type(const DistArgs& a, cudaStream_t st)
 {
     const int64_t bytes = a.vocab * (int64_t)sizeof(T);
-    if (bytes <= 16 << 10 && a.k <= 256) return launch<T, 128, 1, MODE>(a, st);
+    int nt = MODE == kLoss ? (bytes <= 16 << 10 ? 32 : 64) : bytes <= 8 << 10 ? 32 : bytes <= 24 << 10 ? 64 : 128;
+    while (2 * nt < a.k || (nt < 128 && a.n * nt * 2 <= kThreadsAtOnce)) nt *= 2;
+    if (nt == 128 && bytes * (kThreadsAtOnce / 128) > kHalfL2) nt = 256;
+    switch (nt) {
+    case 32: return launch<T, 32, 1, MODE>(a, st);
+    case 64: return launch<T, 64, 1, MODE>(a, st);
+    case 128: return launch<T, 128, 1, MODE>(a, st);
+    }
+    constexpr int64_t kBlocks = kThreadsAtOnce / 256;
     int cl = 1;
-    while (cl < 8 && ((MODE == kBoth && 592 / cl * bytes > (int64_t)63 << 20) || a.n * cl * 2 <= 592)) cl *= 2;
+    while (cl < 8 && ((MODE == kBoth && kBlocks / cl * bytes > kHalfL2) || a.n * cl * 2 <= kBlocks)) cl *= 2;
     if (bytes / cl < 8 << 10) cl = 1;
     switch (cl) {
     case 1: return launch<T, 256, 1, MODE>(a, st);
