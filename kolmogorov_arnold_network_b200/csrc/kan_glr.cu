@@ -271,13 +271,13 @@ __device__ __forceinline__ void st_async(uint32_t to, uint32_t bar, float4 v)
 // cluster's blocks with the mbarrier that counts them.
 template <int W> struct Meet {
     float4 warp[2][W][32];                             // p, k, b, y
-    float4 block[2][W > 1 ? kMaxCluster : 1][32];      // p, k, b, -
+    float4 block[2][W == 8 ? kMaxCluster : 1][32];     // p, k, b, -
     uint64_t full[2];
 };
 
 template <int W> __device__ __forceinline__ void meet_init(Meet<W>& s, int cl)
 {
-    if (W > 1 && cl > 1) {
+    if (W == 8 && cl > 1) {
         if (threadIdx.x == 0) {
             mbar_init(smem_addr(&s.full[0]), 1);
             mbar_init(smem_addr(&s.full[1]), 1);
@@ -324,7 +324,7 @@ __device__ __forceinline__ float exchange(Meet<W>& s, int n, int cl, int wpos, i
         s.warp[set][wpos][lane] = make_float4(m.p, m.k, b, y);
         at_barrier();
         __syncthreads();
-        if (cl > 1 && wpos == 0) {
+        if (W == 8 && cl > 1 && wpos == 0) {
             const float bt = cuts ? pass<true>(s.warp[set], 0, W, 0.0f) : pass<false>(s.warp[set], 0, W, 0.0f);
             float yt = 0.0f;
 #pragma unroll
@@ -339,13 +339,13 @@ __device__ __forceinline__ float exchange(Meet<W>& s, int n, int cl, int wpos, i
             for (int c = 0; c < cl; ++c) st_async(peer_addr(to, c), peer_addr(bar, c), make_float4(t.p, t.k, t.b, 0.0f));
         }
         past_barrier();
-        if (cl > 1) {
+        if (W == 8 && cl > 1) {
             if (waits) waits = mbar_wait_cluster(smem_addr(&s.full[set]), (n >> 1) & 1, status);
         }
         const float first = run;
         auto states = [&](auto careful) {
             constexpr bool CUTS = decltype(careful)::value;
-            if (cl > 1) {
+            if (W == 8 && cl > 1) {
                 in = pass<CUTS>(s.block[set], 0, cpos, first);
                 run = pass<CUTS>(s.block[set], cpos, cl, in);
                 in = pass<CUTS>(s.warp[set], 0, wpos, in);
@@ -492,12 +492,12 @@ template <typename T, bool STAGED, int S, int NA> struct Inputs {
 // Forward: S steps a thread, W warps a block, a.cluster blocks a cluster; STAGED: inputs through shared memory (W = 8), else
 // into registers.
 template <typename T, bool STAGED, int S, int W>
-__global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 1) glr_forward_kernel(const GlrArgs a)
+__global__ void __launch_bounds__(32 * W, 24 / W) glr_forward_kernel(const GlrArgs a)
 {
     constexpr int N = S > 1 ? 2 : 1;                     // steps side by side
     extern __shared__ __align__(128) char tiles[];       // STAGED: r, g, x
     __shared__ Meet<W> meet;
-    const int side = W > 1 ? a.cluster : 1;              // blocks side by side in time
+    const int side = W == 8 ? a.cluster : 1;             // blocks side by side in time
     const Place at(a, side);
     const int64_t SPAN = (int64_t)S * W * side;
     const int64_t mine = (int64_t)at.rank * W * S, first = mine + at.warp * S;   // the block's and the thread's first step
@@ -610,17 +610,17 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 3 : 1) glr_forward_kernel(con
         Y += SPAN * a.C;
     }
     if (a.h_last && at.on && at.rank == 0 && at.warp == 0) a.h_last[state] = run;
-    if constexpr (W > 1) meet_end(waits);
+    if constexpr (W == 8) meet_end(waits);
 }
 
 // Backward: the same split, walked from the end of the sequence.
-template <typename T, bool STAGED, int W>
-__global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_backward_kernel(const GlrArgs a)
+template <typename T, bool STAGED, int S, int W>
+__global__ void __launch_bounds__(32 * W, 16 / W) glr_backward_kernel(const GlrArgs a)
 {
-    constexpr int S = kSteps, N = 2;                     // a thread's steps begin at a kept state
+    constexpr int N = S > 1 ? 2 : 1;                     // steps side by side (a thread's begin at a kept state)
     extern __shared__ __align__(128) char tiles[];       // STAGED: r, g, x, dy
     __shared__ Meet<W> meet;
-    const int side = W > 1 ? a.cluster : 1;              // blocks side by side in time
+    const int side = W == 8 ? a.cluster : 1;             // blocks side by side in time
     const Place at(a, side);
     const int64_t SPAN = (int64_t)S * W * side;
     const int64_t mine = (int64_t)at.rank * W * S, first = mine + at.warp * S;
@@ -773,21 +773,32 @@ __global__ void __launch_bounds__(32 * W, W == 8 ? 2 : 1) glr_backward_kernel(co
             a.part[(at.b * side + at.rank) * a.C + at.c] = v;
         }
     }
-    if constexpr (W > 1) meet_end(waits);
+    if constexpr (W == 8) meet_end(waits);
 }
 
-// ddecay from the partial sums of dL L, in their order.
-__global__ void glr_decay_kernel(const double* __restrict__ part, int64_t n, int64_t C, const float* __restrict__ decay,
-                                 float* __restrict__ ddecay)
+// ddecay from the partial sums of dL L: a block takes 16 channels, its threads' sums of every blockDim.y-th partial meet as
+// a tree (a fixed order; 4096 x 768 partials in 1/20 of what one thread a channel takes).
+constexpr int kDecayChannels = 16, kDecayRows = 64;
+__global__ void __launch_bounds__(kDecayChannels * kDecayRows) glr_decay_kernel(const double* __restrict__ part, int64_t n, int64_t C,
+                                                                                const float* __restrict__ decay,
+                                                                                float* __restrict__ ddecay)
 {
-    const int64_t c = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (c >= C) return;
+    __shared__ double red[kDecayRows][kDecayChannels];
+    const int64_t c = (int64_t)blockIdx.x * kDecayChannels + threadIdx.x;
     double v = 0.0;
-    for (int64_t i = 0; i < n; ++i) v += part[i * C + c];
+    if (c < C)
+#pragma unroll 4
+        for (int64_t i = threadIdx.y; i < n; i += blockDim.y) v += part[i * C + c];
+    red[threadIdx.y][threadIdx.x] = v;
+    for (int half = blockDim.y / 2; half > 0; half /= 2) {
+        __syncthreads();
+        if ((int)threadIdx.y < half) red[threadIdx.y][threadIdx.x] += red[threadIdx.y + half][threadIdx.x];
+    }
+    if (c >= C || threadIdx.y != 0) return;
     const float d = decay[c];
     // sigmoid(d) / softplus(d), which goes to 1 as d falls
     const float ratio = d > -15.0f ? 1.0f / ((1.0f + expf(-d)) * softplus_of(d)) : 1.0f;
-    ddecay[c] = (float)(v * (double)ratio);
+    ddecay[c] = (float)(red[0][threadIdx.x] * (double)ratio);
 }
 
 kan_status gl_fail(kan_status st, const char* msg) { return set_last_error(st, msg); }
@@ -859,31 +870,41 @@ template <typename T, bool STAGED, bool BWD> struct Kernels {
     static constexpr size_t kSmem = STAGED ? 2 * (BWD ? 4 : 3) * Tile<T>::kBytes : 0;
     static void (*kernel())(const GlrArgs)
     {
-        if constexpr (BWD) return glr_backward_kernel<T, STAGED, 8>;
+        if constexpr (BWD) return glr_backward_kernel<T, STAGED, kSteps, 8>;
         else return glr_forward_kernel<T, STAGED, kSteps, 8>;
     }
-    // Blocks of a cluster lie side by side in time.  Measured (cycles): a block starts in 5000; a span takes a block alone
-    // on its SM 2800 (backward 3700), more of them kIssue each, and 110 for each block whose map is walked.  The size for
-    // which the waves of blocks are done first.
-    static constexpr int64_t kIssue = BWD ? (STAGED ? 2700 : 3100) : (STAGED ? 1500 : 2200), kAlone = BWD ? 3700 : 2800;
+    // Blocks of a cluster lie side by side in time: more of them make fewer spans, but each span's exchange longer and the
+    // clusters that run at once fewer.  The size for which the waves of clusters are done first, by what a block's start and
+    // a span were measured to take (cycles): blocks that share an SM take kIssue of it each, one takes kAlone at least,
+    // every block whose map is walked adds kWalk.  From 1 x 2048 x 768 and 32 x 512 x 768 to 16 x 4096 x 1024 and
+    // 1 x 65536 x 1000 it finds the best size (1, 2, 3, 5 and 8 are), where a fixed size of 2 takes up to 2.7, of 8 up to 2
+    // times as long.
+    static constexpr int64_t kStart = 5000, kAlone = BWD ? (STAGED ? 3110 : 3890) : (STAGED ? 2570 : 2820),
+                             kIssue = BWD ? (STAGED ? 2330 : 2670) : (STAGED ? 1240 : 1360),
+                             kWalk = BWD ? (STAGED ? 80 : 110) : (STAGED ? 190 : 210);
+    // Shared memory with which an SM holds one block, two, as many as it can (by registers 3, backward 2)
+    static constexpr size_t kRoom[3] = {130 * 1024, 70 * 1024, kSmem};
     static int cluster_for(const GlrArgs& a)
     {
-        static std::atomic<int> known[kMaxCluster][64];
-        const int64_t units = a.B * a.strips, sms = 148;
+        static std::atomic<int> known[kMaxCluster][3][64];
+        const int64_t units = a.B * a.strips;
         int best = 0;
         int64_t cost = -1;
         for (int cl = 1; cl <= kMaxCluster; cl += cl < 8 ? 1 : 8) {
             if (cl > 1 && (int64_t)8 * kSteps * (cl - 1) >= a.T) break;              // (more blocks than the sequence has steps for)
-            const int64_t at_once = resident(kernel(), 8, cl, kSmem, known[cl - 1]);
-            if (at_once < 1) {
+            int64_t hold[3];                             // clusters at once with so many blocks an SM
+            for (int k = 0; k < 3; ++k) hold[k] = resident(kernel(), 8, cl, kRoom[k], known[cl - 1][k]);
+            if (std::min({hold[0], hold[1], hold[2]}) < 1) {
                 if (cl > 8) break;
                 return 0;
             }
             const int64_t spans = (a.T + 8 * kSteps * cl - 1) / (8 * kSteps * cl);
             auto wave = [&](int64_t clusters) {
-                return clusters ? 5000 + spans * (std::max(kAlone, kIssue * ((clusters * cl + sms - 1) / sms)) + 110 * cl) : 0;
+                if (!clusters) return (int64_t)0;
+                const int64_t share = clusters <= hold[0] ? 1 : clusters <= hold[1] ? 2 : 3;
+                return kStart + spans * (std::max(kAlone, kIssue * share) + kWalk * cl);
             };
-            const int64_t c = units / at_once * wave(at_once) + wave(units % at_once);
+            const int64_t c = units / hold[2] * wave(hold[2]) + wave(units % hold[2]);
             if (cost < 0 || c < cost) {
                 cost = c;
                 best = cl;
@@ -897,12 +918,11 @@ template <typename T, bool STAGED, bool BWD> struct Kernels {
         return a.cluster ? launch(kernel(), 8, a.cluster, kSmem, a, st) : cudaErrorInvalidValue;
     }
 };
-// A block of one warp for sequences of at most 8 steps (forward, for a single one too).
-template <typename T, bool BWD> cudaError_t run_short(const GlrArgs& a, cudaStream_t st)
+// Short sequences: a block of as many warps as hold their steps (one step: a warp whose threads take that one).
+template <typename T, bool BWD, int S, int W> cudaError_t run_short(const GlrArgs& a, cudaStream_t st)
 {
-    if constexpr (BWD) return launch(glr_backward_kernel<T, false, 1>, 1, 1, 0, a, st);
-    else if (a.T == 1) return launch(glr_forward_kernel<T, false, 1, 1>, 1, 1, 0, a, st);
-    else return launch(glr_forward_kernel<T, false, kSteps, 1>, 1, 1, 0, a, st);
+    if constexpr (BWD) return launch(glr_backward_kernel<T, false, S, W>, W, 1, 0, a, st);
+    else return launch(glr_forward_kernel<T, false, S, W>, W, 1, 0, a, st);
 }
 
 // Inputs go through shared memory where their rows begin on 16 bytes.
@@ -920,7 +940,10 @@ template <typename T, bool BWD> cudaError_t run_type(const kan_glr_shape& s, Glr
 {
     a.strips = (int)((s.channels + 31) / 32);
     a.cluster = 1;
-    if (a.T <= kSteps) return run_short<T, BWD>(a, st);
+    if (a.T == 1) return run_short<T, BWD, 1, 1>(a, st);
+    if (a.T <= kSteps) return run_short<T, BWD, kSteps, 1>(a, st);
+    if (a.T <= 2 * kSteps) return run_short<T, BWD, kSteps, 2>(a, st);
+    if (a.T <= 4 * kSteps) return run_short<T, BWD, kSteps, 4>(a, st);
     return staged_ok(s, a) ? Kernels<T, true, BWD>::run(a, st) : Kernels<T, false, BWD>::run(a, st);
 }
 template <bool BWD> cudaError_t run(const kan_glr_shape& s, GlrArgs& a, cudaStream_t st)
@@ -1018,7 +1041,11 @@ kan_status kan_glr_backward(const kan_glr_shape* s, const void* x, const void* r
     }
     e = run<true>(*s, a, cs);
     if (e == cudaSuccess && ddecay) {
-        glr_decay_kernel<<<(unsigned)((s->channels + 127) / 128), 128, 0, cs>>>(a.part, s->batch * a.cluster, s->channels, decay, ddecay);
+        const int64_t n = s->batch * a.cluster;
+        int rows = 1;                                    // of threads, a power of two
+        while (rows < kDecayRows && rows < n) rows *= 2;
+        glr_decay_kernel<<<(unsigned)((s->channels + kDecayChannels - 1) / kDecayChannels), dim3(kDecayChannels, rows), 0, cs>>>(
+            a.part, n, s->channels, decay, ddecay);
         count_launch();
         e = cudaGetLastError();
     }
