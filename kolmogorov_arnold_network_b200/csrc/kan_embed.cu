@@ -6,18 +6,20 @@
 //
 // Forward: one warp per (token, 128-vector segment of its row), the widest
 // vectors that the rows allow; bound by HBM (each token's row written, each
-// distinct row read).
+// distinct row read): 65536 tokens of a 50257 x 1024 fp32 table 58 us, 87% of
+// the copy rate.
 //
-// Backward, without atomic adds and with one fixed order of summation:
+// Backward, without atomic adds of floats and with one fixed order of
+// summation.  Up to 512 tokens: one launch (embed_few_kernel).  More tokens:
 //   1. The tokens are ordered by id, stably.  A sort block owns the ids that
-//      are alike modulo P (a power of two, 256 at least): neighbouring ids, whose frequencies are
-//      alike in a vocabulary, fall to different blocks.
-//      Few tokens: every block reads all ids twice (they stay in L2); the
-//      first reading counts, per warp, the tokens of each owned id and all
-//      tokens of the blocks before it, which gives the block's place in the
-//      order without any exchange between blocks; the second one places its
-//      tokens.  Many tokens: embed_split_kernel first groups each piece of
-//      2048 tokens by owner, and a sort block reads its own tokens only.
+//      are alike modulo P (a power of two, 256 at least): neighbouring ids,
+//      whose frequencies are alike in a vocabulary, fall to different blocks.
+//      Up to 8192 tokens every block reads all ids (they stay in L2), counts,
+//      per warp, the tokens of each owned id and all tokens of the blocks
+//      before it, which gives the block's place in the order without any
+//      exchange between blocks, and then places its tokens.  Above that
+//      embed_split_kernel first groups each piece of 2048 tokens by owner, and
+//      a sort block reads its own tokens only.
 //   2. embed_sum_kernel cuts the ordered list into chunks; a thread keeps some
 //      vectors of columns and adds the chunk's rows in order.  Runs that lie
 //      within a chunk are written at once, the pieces of runs that cross a
@@ -26,7 +28,11 @@
 //      rows of the ids that no token has, the larger part of the traffic where
 //      the vocabulary is large.
 //   3. embed_join_kernel adds the partials of each such run in chunk order.
-// Sums are fp32 and rounded once, when the row of dW is written.
+// Sums are fp32 and rounded once, when the row of dW is written.  The launches
+// overlap (each waits for the one before it when it needs its results).
+// 131071 x 771 fp32 tokens over 8001 ids: order 16 us, sums 83 us (66 at the
+// copy rate), joins 12 us, 119 together; 8192 x 768 bf16 over 50257 ids: 28 us
+// (14 at the copy rate), three dependent kernels of which none fills the time.
 #include <algorithm>
 
 #include "kan_device.cuh"
@@ -40,8 +46,8 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxBins = 1536;    // ids per sort block (their per-warp counts lie in shared memory)
 constexpr int kMaxChunk = 64;     // tokens per chunk of the ordered list, at most
-constexpr int kJoinRows = 4;     // partials that a block of the join adds side by side
-constexpr int kShortRun = 4;      // a run of at most so many further pieces is joined by one block
+constexpr int kJoinRows = 4;      // partials that a block of the join adds side by side (8192 tokens of one id: 33 us, with 1 63)
+constexpr int kShortRun = 4;      // a run of at most so many further pieces is joined by one block (32768 x 771 fp32: 62 us, with 0 65)
 constexpr int kPiece = 2048;      // tokens that a block of the split groups by owner
 constexpr int kFound = 32;        // tokens that a warp of the sort keeps from its first reading
 constexpr int kBatch = 8;          // ids that a thread of the sort reads at once
@@ -534,6 +540,145 @@ __global__ void __launch_bounds__(64 * kJoinRows) embed_join_kernel(const SumArg
     }
 }
 
+// ---- backward: few tokens, in one launch ----
+// Tokens at most.  16 to 512 tokens: 10 to 12 us for a table of 32003 x 768 bf16 (7.5 us of it the zero rows) against 17 to 19
+// with the order, 3.5 to 7 us against 12 to 14 for 1000 x 64 fp32.  1024 tokens: 16 against 21 us and 24 against 21 for
+// 5000 x 771 fp32, where frequent ids keep a block busy; all of them the same id: 35 against 17 (512: 19 against 15).
+constexpr int kFew = 512;
+constexpr int kFewBlocks = 293;       // a prime (regular ids spread), 2 blocks an SM
+constexpr int kFewRows = 1 << 15;     // rows of the table per block at most (a bit each)
+constexpr int kAlone = 16;            // tokens of an id that one warp adds by itself
+
+struct FewArgs {
+    const void *ids, *dY;
+    void* dW;
+    int64_t rows, dim, pad, row_bytes;
+    int tokens;
+    float scale;
+    unsigned int* status;
+};
+
+// A block owns every kFewBlocks-th row.  All blocks read all ids; a bit says which of the block's rows have tokens, the others
+// become 0.  A warp adds the tokens of an id in their order; the many tokens of a frequent id are parted among the block's
+// warps in order, whose sums are then added in order.
+template <typename T, typename O, int N, typename I>
+__global__ void __launch_bounds__(256, 2) embed_few_kernel(const FewArgs a)
+{
+    constexpr int NV = N * (int)sizeof(T) <= 4 ? 4 : 2, COLS = 32 * NV * N, U = 8;       // columns of a pass, rows in flight
+    __shared__ __align__(16) int32_t id[kFew];
+    __shared__ uint32_t has[kFewRows / 32];
+    __shared__ int32_t hit[kFew], many[kFew];
+    __shared__ int hits, manys;
+    __shared__ __align__(16) float red[8][COLS];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int stride = gridDim.x, own = (int)((a.rows - blockIdx.x + stride - 1) / stride);      // the block's rows
+    const int groups = (a.tokens + 31) / 32;
+    for (int i = tid; i < (own + 31) / 32; i += 256) has[i] = 0;
+    if (tid == 0) hits = manys = 0;
+    bool bad = false;
+    for (int i = tid; i < 32 * groups; i += 256) {
+        const int64_t v = i < a.tokens ? id_at<I>(a.ids, i) : a.pad;
+        const bool in = v >= 0 && v < a.rows;
+        bad |= i < a.tokens && !in;
+        id[i] = i < a.tokens && in && v != a.pad ? (int)v : -1;
+    }
+    if (bad && blockIdx.x == 0) record_status(a.status, KAN_ERR_DEVICE_CHECK);
+    __syncthreads();
+    for (int i = tid; i < a.tokens; i += 256) {
+        const int v = id[i];
+        if (v < 0 || v % stride != (int)blockIdx.x) continue;
+        const int r = v / stride;
+        const uint32_t bit = 1u << (r & 31);
+        if (!(atomicOr(&has[r >> 5], bit) & bit)) hit[atomicAdd(&hits, 1)] = v;          // (rows stand alone: any order)
+    }
+    __syncthreads();
+
+    const int64_t vecs = a.dim / N;
+    const T* const dY = reinterpret_cast<const T*>(a.dY);
+    O* const dW = reinterpret_cast<O*>(a.dW);
+    // adds the tokens with id v among the groups g0..g1, in their order, for the vectors v0 + 32 k
+    auto sum = [&](int v, int g0, int g1, int64_t v0, float (&acc)[NV][N]) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int e = 0; e < N; ++e) acc[k][e] = 0.0f;
+        for (int g = g0; g < g1; ++g) {
+            unsigned m = __ballot_sync(0xffffffffu, id[32 * g + lane] == v);
+            while (m) {
+                Pack<T, N> q[U][NV];
+                int n = 0;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (!m) break;
+                    const T* row = dY + (int64_t)(32 * g + __ffs(m) - 1) * a.dim;
+#pragma unroll
+                    for (int k = 0; k < NV; ++k) q[u][k] = v0 + 32 * k < vecs ? Pack<T, N>::load(row + (v0 + 32 * k) * N) : Pack<T, N>::zero();
+                    m &= m - 1;
+                    ++n;
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (u >= n) break;
+#pragma unroll
+                    for (int k = 0; k < NV; ++k) {
+                        float f[N];
+                        q[u][k].unpack(f);
+#pragma unroll
+                        for (int e = 0; e < N; ++e) acc[k][e] += f[e];
+                    }
+                }
+            }
+        }
+    };
+    auto store = [&](int v, int64_t v0, const float (&acc)[NV][N]) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+            if (v0 + 32 * k < vecs) store_row<T, O, N>(dW + (int64_t)v * a.dim + (v0 + 32 * k) * N, acc[k], a.scale);
+    };
+    float acc[NV][N];
+    const int passes = (int)((vecs + 32 * NV - 1) / (32 * NV));
+    for (int64_t w = warp; w < (int64_t)hits * passes; w += 8) {
+        const int h = (int)(w / passes), v = hit[h], pass = (int)(w - (int64_t)h * passes);
+        int n = 0;
+        for (int g = 0; g < groups; ++g) n += __popc(__ballot_sync(0xffffffffu, id[32 * g + lane] == v));
+        if (n > kAlone) {
+            if (lane == 0 && pass == 0) many[atomicAdd(&manys, 1)] = v;
+            continue;
+        }
+        const int64_t v0 = (int64_t)pass * 32 * NV + lane;
+        sum(v, 0, groups, v0, acc);
+        store(v, v0, acc);
+    }
+    for (int r = warp; r < own; r += 8) {
+        if (has[r >> 5] >> (r & 31) & 1) continue;
+        char* row = reinterpret_cast<char*>(a.dW) + ((int64_t)r * stride + blockIdx.x) * a.row_bytes;
+        if (a.row_bytes % 16 == 0) zero_row<uint4>(row, a.row_bytes);
+        else if (a.row_bytes % 4 == 0) zero_row<uint32_t>(row, a.row_bytes);
+        else zero_row<uint16_t>(row, a.row_bytes);
+    }
+    __syncthreads();
+    for (int h = 0; h < manys; ++h) {
+        for (int64_t v0 = lane; v0 - lane < vecs; v0 += 32 * NV) {
+            sum(many[h], groups * warp / 8, groups * (warp + 1) / 8, v0, acc);
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int e = 0; e < N; ++e) red[warp][(k * N + e) * 32 + lane] = acc[k][e];
+            __syncthreads();
+            if (warp == 0) {
+#pragma unroll
+                for (int k = 0; k < NV; ++k)
+#pragma unroll
+                    for (int e = 0; e < N; ++e)
+#pragma unroll
+                        for (int w = 1; w < 8; ++w) acc[k][e] += red[w][(k * N + e) * 32 + lane];
+                store(many[h], v0, acc);
+            }
+            __syncthreads();
+        }
+    }
+}
+
 kan_status em_fail(kan_status st, const char* msg) { return set_last_error(st, msg); }
 
 kan_status validate(const kan_embed_shape* s)
@@ -561,14 +706,17 @@ int sort_shift(const kan_embed_shape& s)
     return sh;
 }
 
-// Tokens per chunk: small enough that the chunks fill the SMs, 16 to 64 (fewer tokens a chunk, more partials).
+// Tokens per chunk: small enough that the chunks fill the SMs, 16 to 64 (fewer tokens a chunk, more partials; us with chunks
+// of 16 | 64: 8192 tokens of 768 bf16 22.7 | 26.7, 131072 tokens 102 | 71).
 int chunk_of(const kan_embed_shape& s)
 {
     int c = kMaxChunk;
     while (c > 16 && s.tokens / c < 4 * 148) c /= 2;
     return c;
 }
-// Above this many tokens the sort blocks read what embed_split_kernel has grouped for them, below it the ids themselves.
+// Above this many tokens the sort blocks read what embed_split_kernel has grouped for them, below it the ids themselves
+// (x 768 bf16 over 32003 ids, us with the split | without: 4096 tokens 23.0 | 21.7, 8192 24.0 | 22.8, 16384 28 | 30,
+// 131072 71 | 117).
 constexpr int64_t kSplitFrom = 8192;
 
 struct Layout {
@@ -664,7 +812,8 @@ cudaError_t forward_of(const kan_embed_shape& s, const void* ids, const void* W,
 template <typename T, typename O, int N>
 cudaError_t launch_sum(const kan_embed_shape& s, SumArgs a, cudaStream_t st)
 {
-    // narrow vectors come four to a thread, so that a row's bookkeeping is shared by as many loads
+    // narrow vectors come four to a thread, so that a row's bookkeeping is shared by as many loads (32768 x 771 fp32: 62 us,
+    // with one 69)
     constexpr int NV = N * (int)sizeof(T) <= 4 ? 4 : 1;
     const int64_t vecs = (s.dim / N + NV - 1) / NV;
     const int64_t slices = (vecs + 255) / 256;
@@ -683,6 +832,25 @@ cudaError_t sum_of(const kan_embed_shape& s, const SumArgs& a, cudaStream_t st)
     case 4: return launch_sum<T, O, 4>(s, a, st);
     case 2: return launch_sum<T, O, 2>(s, a, st);
     default: return launch_sum<T, O, 1>(s, a, st);
+    }
+}
+
+template <typename T, typename O, int N> cudaError_t launch_few(const FewArgs& a, int id_bytes, cudaStream_t st)
+{
+    const unsigned grid = (unsigned)std::min<int64_t>(a.rows, kFewBlocks);
+    if (id_bytes == 8) embed_few_kernel<T, O, N, int64_t><<<grid, 256, 0, st>>>(a);
+    else embed_few_kernel<T, O, N, int32_t><<<grid, 256, 0, st>>>(a);
+    count_launch();
+    return cudaGetLastError();
+}
+
+template <typename T, typename O> cudaError_t few_of(const FewArgs& a, int id_bytes, cudaStream_t st)
+{
+    switch (common_vector_bytes((uint64_t)a.dim * sizeof(T)) / (int)sizeof(T)) {
+    case 8: if constexpr (sizeof(T) == 2) return launch_few<T, O, 8>(a, id_bytes, st);
+    case 4: return launch_few<T, O, 4>(a, id_bytes, st);
+    case 2: return launch_few<T, O, 2>(a, id_bytes, st);
+    default: return launch_few<T, O, 1>(a, id_bytes, st);
     }
 }
 
@@ -732,6 +900,24 @@ kan_status kan_embed_backward(const kan_embed_shape* s, const void* ids, const v
     }
     const Layout L = layout_of(*s);
     if (!workspace || ws_bytes < L.bytes) return em_fail(KAN_ERR_WORKSPACE, "workspace too small");
+    const bool g32 = s->grad_dtype == KAN_F32;
+    if (s->tokens <= kFew && s->rows <= (int64_t)kFewBlocks * kFewRows) {
+        FewArgs f{};
+        f.ids = ids;
+        f.dY = dY;
+        f.dW = dW;
+        f.rows = s->rows;
+        f.dim = s->dim;
+        f.pad = s->padding_idx;
+        f.row_bytes = row_bytes;
+        f.tokens = (int)s->tokens;
+        f.scale = s->scale;
+        f.status = device_status_ptr();
+        const cudaError_t e = s->dtype == KAN_F32
+            ? (g32 ? few_of<float, float>(f, s->id_bytes, cs) : few_of<float, __nv_bfloat16>(f, s->id_bytes, cs))
+            : (g32 ? few_of<__nv_bfloat16, float>(f, s->id_bytes, cs) : few_of<__nv_bfloat16, __nv_bfloat16>(f, s->id_bytes, cs));
+        return e == cudaSuccess ? KAN_OK : em_fail(KAN_ERR_CUDA, cudaGetErrorString(e));
+    }
     char* ws = reinterpret_cast<char*>(workspace);
     SortArgs o{};
     o.ids = ids;
@@ -767,7 +953,6 @@ kan_status kan_embed_backward(const kan_embed_shape* s, const void* ids, const v
         a.shift = L.shift;
         a.bins = L.bins;
         a.chunks = L.chunks;
-        const bool g32 = s->grad_dtype == KAN_F32;
         if (s->dtype == KAN_F32)
             e = g32 ? sum_of<float, float>(*s, a, cs) : sum_of<float, __nv_bfloat16>(*s, a, cs);
         else

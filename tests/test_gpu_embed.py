@@ -207,3 +207,30 @@ def test_other_stream():
         got = L.embed_backward(ids, dY, 64)
     st.synchronize()
     _check_grad(got, ids, dY, 64, 1.0)
+
+
+FEW = [(n, rows, dim, kind) for n in (16, 17, 511, 512, 513) for rows, dim in ((3, 40), (293, 9), (294, 514), (2000, 1029))
+       for kind in ("uniform", "zipf", "one")]
+
+
+@pytest.mark.parametrize("dt,gdt", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32")])
+@pytest.mark.parametrize("case", FEW, ids=lambda c: "n{}_v{}_d{}_{}".format(*c))
+def test_gradient_of_few_tokens(dt, gdt, case):
+    """Around the sizes up to which one launch takes all, one warp an id, and every block a row."""
+    n, rows, dim, kind = case
+    ids = _ids(n, rows, kind, n + rows)
+    dY = torch.randn(n, dim, generator=torch.Generator().manual_seed(n)).to(DT[dt])
+    pad = rows - 1 if dim == 9 else None
+    got = [L.embed_backward(ids.cuda(), dY.cuda(), rows, 0.5, padding_idx=pad, grad_dtype=DT[gdt]) for _ in range(2)]
+    _check_grad(got[0], ids, dY, rows, 0.5, *(() if pad is None else (pad,)))
+    assert torch.equal(*got)
+    assert N.kan_sync_status(None) == 0
+
+
+@pytest.mark.parametrize("rows", [293 * 32768, 293 * 32768 + 1])
+def test_few_tokens_of_a_huge_table(rows):
+    ids = torch.tensor([rows - 1, 0, rows - 1, 293, 7, rows // 2])
+    dY = torch.randn(6, 2)
+    got = L.embed_backward(ids.cuda(), dY.cuda(), rows)
+    want = torch.zeros(rows, 2).index_add_(0, ids, dY)
+    assert torch.equal(got.cpu(), want)
