@@ -178,3 +178,25 @@ def test_distill_in_place_needs_one_stride(lib):
 @pytest.mark.parametrize("kw", [dict(x_strides=(32, 1 << 41)), dict(channels=(1 << 20) + 1), dict(batch=1 << 27)])
 def test_glr_limits(lib, kw):
     assert glr_calls(lib, ctypes.byref(glr(**kw))) == (2, 2)
+
+
+def test_bench_figures_do_not_hang_on_the_sequence_sources(tmp_path, monkeypatch):
+    """The benchmark's ncu figures are of the layer kernels: their hash passes over the sequence operators' sources, which
+    no other source includes."""
+    import pathlib
+
+    import bench
+    csrc = pathlib.Path(bench.ROOT) / "kolmogorov_arnold_network_b200" / "csrc"
+    for f in csrc.iterdir():
+        if f.name not in bench.SEQUENCE_SOURCES:
+            text = f.read_text()
+            assert not any(f'"{n}"' in text for n in bench.SEQUENCE_SOURCES), f.name
+    here = tmp_path / "kolmogorov_arnold_network_b200" / "csrc"
+    here.mkdir(parents=True)
+    (here / "kan_tc.cu").write_text("a")
+    monkeypatch.setattr(bench, "ROOT", str(tmp_path))
+    before = bench.csrc_hash()
+    (here / "kan_glr.cu").write_text("b")
+    assert bench.csrc_hash() == before
+    (here / "kan_tc.cu").write_text("c")
+    assert bench.csrc_hash() != before
