@@ -345,3 +345,20 @@ def test_module_repeated_rows():
     _, bd = bounds(rows, ids, t, 2.0, w)
     bar = (kappa(300) + 4) * U32 * bd.sum(0) + 1e-37                      # four rows added in fp32
     assert bool(((leaf.grad[0].cpu().double() - wd.sum(0)).abs() <= bar).all())
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("n,vocab,k", [(5000, 100, 64), (5000, 101, 65), (3000, 4099, 128), (3000, 4098, 129), (2400, 6001, 3),
+                                       (1300, 13001, 20), (1200, 260, 300), (1190, 9000, 257)])
+def test_many_rows(dt, n, vocab, k):
+    """More rows than run at once: the narrow blocks (32 to 128 threads a row), at the entries where they end."""
+    z, ids, t, w = draw(n, vocab, k, dt, seed=n + k, repeat=True)
+    loss, dz, loss2, dz2 = run(z, ids, t, 1.5, w)
+    at = torch.randperm(n, generator=torch.Generator().manual_seed(1))[:40].sort().values
+    args = (z[at], ids[at], t[at], 1.5, w[at])
+    check(loss.cpu()[at], dz.cpu()[at], args)
+    check(loss2.cpu()[at], dz2.cpu()[at], args)
+    assert bool(dz.isfinite().all()) and bool(dz2.isfinite().all())
+    # every row: its gradient sums to 0, up to the rounding of each element
+    total = dz2.double().sum(1).abs().cpu()
+    assert bool((total <= (torch.finfo(dz2.dtype).eps / 2 + kappa(vocab) * U32) * dz2.double().abs().sum(1).cpu() + kappa(vocab) * U32 * 3 * w + 1e-37).all())

@@ -321,3 +321,37 @@ def test_steps_far_apart(dt):
         view.copy_(d[k])
         far[k] = view
     check(run(far), reference(d), bounds_of(d))
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("case", [(1, 777, 32), (1, 1030, 40), (1, 2500, 16), (2, 1030, 104), (5, 777, 384), (6, 777, 416), (7, 777, 449),
+                                  (10, 777, 384), (3, 1030, 801), (16, 200, 512), (600, 70, 24)], ids=lambda c: "b{}_t{}_c{}".format(*c))
+def test_blocks_side_by_side(dt, case):
+    """As many sequences and channels as make the number of blocks side by side in time 1 to 7, 8 and 16; some channels of some
+    sequences against the reference (they do not touch one another)."""
+    d = draw(*case, dt, seed=case[0] + case[1], reset="some")
+    B, T, C = case
+    rows, cols = sorted({0, B // 2, B - 1}), sorted({0, 1, C // 2, C - 2, C - 1})
+    part = {k: None if v is None else v[rows][..., cols] if v.dim() == 3 or k in ("h0", "dh_last") else v[rows] if k == "reset" else v[cols]
+            for k, v in d.items()}
+    got = run(d)
+    got = {k: v[rows][..., cols] if k != "ddecay" else v for k, v in got.items() if k != "ddecay" or len(rows) == B}
+    if "ddecay" in got:
+        got["ddecay"] = got["ddecay"][cols]
+    want = {k: v for k, v in reference(part).items() if k in got}
+    check(got, want, bounds_of(part))
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [2, 8, 15, 16, 17, 31, 32, 33, 63, 64, 65])
+def test_short_sequences(dt, T):
+    for C, reset in ((40, None), (33, "some")):
+        d = draw(3, T, C, dt, seed=T, reset=reset)
+        check(run(d), reference(d), bounds_of(d))
+
+
+def test_sum_of_many_sequences():
+    """ddecay over more partial sums than a block has threads for."""
+    for B, T in ((300, 1), (130, 9), (1, 5)):
+        d = draw(B, T, 19, "f32", seed=B)
+        check(run(d), reference(d), bounds_of(d))
