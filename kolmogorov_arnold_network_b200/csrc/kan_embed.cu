@@ -18,7 +18,7 @@
 //      per warp, the tokens of each owned id and all tokens of the blocks
 //      before it, which gives the block's place in the order without any
 //      exchange between blocks, and then places its tokens.  Above that
-//      embed_split_kernel first groups each piece of 2048 tokens by owner, and
+//      embed_split_kernel first groups pieces of 1024 tokens or more by owner, and
 //      a sort block reads its own tokens only.
 //   2. embed_sum_kernel cuts the ordered list into chunks; a thread keeps some
 //      vectors of columns and adds the chunk's rows in order.  Runs that lie
@@ -48,7 +48,6 @@ constexpr int kMaxBins = 1536;    // ids per sort block (their per-warp counts l
 constexpr int kMaxChunk = 64;     // tokens per chunk of the ordered list, at most
 constexpr int kJoinRows = 4;      // partials that a block of the join adds side by side (8192 tokens of one id: 33 us, with 1 63)
 constexpr int kShortRun = 4;      // a run of at most so many further pieces is joined by one block (32768 x 771 fp32: 62 us, with 0 65)
-constexpr int kPiece = 2048;      // tokens that a block of the split groups by owner
 constexpr int kFound = 32;        // tokens that a warp of the sort keeps from its first reading
 constexpr int kBatch = 8;          // ids that a thread of the sort reads at once
 constexpr int kSplitShift = 8;    // owners of the split: 256 (more sort blocks share an owner's tokens)
@@ -115,14 +114,15 @@ struct SortArgs {
     int shift;           // log2 P
     int bins;            // ids per block
     int pieces;          // 0: the blocks read the ids themselves
+    int piece;           // tokens of a piece
     unsigned int* status;
 };
 
 // Groups a piece of tokens by owner (id % 256), stably: counts per warp and owner, their running sums, then each token
 // to its place.
-template <typename I> __global__ void __launch_bounds__(kSortThreads) embed_split_kernel(const SortArgs a)
+template <typename I, int PER> __global__ void __launch_bounds__(kSortThreads) embed_split_kernel(const SortArgs a)
 {
-    constexpr int P = 1 << kSplitShift, PER = kPiece / kSortThreads;
+    constexpr int P = 1 << kSplitShift, kPiece = PER * kSortThreads;
     __shared__ int32_t cnt[kSortWarps][P];
     __shared__ int32_t wsum[8];
     let_next_start();
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const SortArgs
             for (int k = 0; k < 32 && q0 + k < t1; ++k) {
                 const int f = __shfl_sync(0xffffffffu, from, k), l = __shfl_sync(0xffffffffu, to, k);
                 for (int j = f + lane; j < l; j += 32) {
-                    const int id = a.grouped[(q0 + k) * kPiece + j].y;
+                    const int id = a.grouped[(q0 + k) * a.piece + j].y;
                     const int o = sort_block(id, a.shift);
                     below += o < p;
                     if (o == p) atomicAdd(&mine[id >> a.shift], 1);   // an integer count: no order
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const SortArgs
             for (int k = 0; k < 32 && q0 + k < t1; ++k) {
                 const int f = __shfl_sync(0xffffffffu, from, k), l = __shfl_sync(0xffffffffu, to, k);
                 for (int j0 = f; j0 < l; j0 += 32) {
-                    const int2 g = j0 + lane < l ? a.grouped[(q0 + k) * kPiece + j0 + lane] : make_int2(0, -1);
+                    const int2 g = j0 + lane < l ? a.grouped[(q0 + k) * a.piece + j0 + lane] : make_int2(0, -1);
                     place(g.y >= 0 && sort_block(g.y, a.shift) == p, g.x, g.y);
                 }
             }
@@ -715,14 +715,19 @@ int chunk_of(const kan_embed_shape& s)
     return c;
 }
 // Above this many tokens the sort blocks read what embed_split_kernel has grouped for them, below it the ids themselves
-// (x 768 bf16 over 32003 ids, us with the split | without: 4096 tokens 23.0 | 21.7, 8192 24.0 | 22.8, 16384 28 | 30,
-// 131072 71 | 117).
-constexpr int64_t kSplitFrom = 8192;
+// (x 768 bf16 over 32003 ids, us with the split | without: 4096 tokens 21.6 | 21.6, 8192 22.6 | 22.7, of one id 46 | 33;
+// 16384 26 | 30, 131072 71 | 118).
+constexpr int64_t kSplitFrom = 8192, kPieceFrom = 65536;
+
+// Tokens that a block of the split groups: small pieces fill the SMs, large ones give the sort blocks longer stretches to read
+// (us with 1024 | 2048: 16384 tokens of 256 bf16 over 5000 ids 20.4 | 22.6, 98304 over 32003 36.2 | 36.3, 262144 of 64 over
+// 50257 62 | 58).
+int piece_of(const kan_embed_shape& s) { return s.tokens <= kPieceFrom ? kSortThreads : 2 * kSortThreads; }
 
 struct Layout {
     size_t perm, key, count, present, grouped, start, part, bytes;
     int64_t chunks, pieces, part_dim;
-    int chunk, shift, bins;
+    int chunk, piece, shift, bins;
 };
 
 Layout layout_of(const kan_embed_shape& s)
@@ -731,7 +736,8 @@ Layout layout_of(const kan_embed_shape& s)
     Layout L{};
     L.chunk = chunk_of(s);
     L.chunks = (s.tokens + L.chunk - 1) / L.chunk;
-    L.pieces = s.tokens > kSplitFrom ? (s.tokens + kPiece - 1) / kPiece : 0;
+    L.piece = piece_of(s);
+    L.pieces = s.tokens > kSplitFrom ? (s.tokens + L.piece - 1) / L.piece : 0;
     L.shift = sort_shift(s);
     L.bins = (int)(((s.rows - 1) >> L.shift) + 1);
     L.perm = 0;
@@ -772,7 +778,8 @@ template <typename I> cudaError_t launch_sort(const SortArgs& o, cudaStream_t st
     if (o.pieces) {
         e = cudaFuncSetAttribute(embed_sort_kernel<I, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
-        embed_split_kernel<I><<<(unsigned)o.pieces, kSortThreads, 0, st>>>(o);
+        if (o.piece == kSortThreads) embed_split_kernel<I, 1><<<(unsigned)o.pieces, kSortThreads, 0, st>>>(o);
+        else embed_split_kernel<I, 2><<<(unsigned)o.pieces, kSortThreads, 0, st>>>(o);
         count_launch();
         e = cudaGetLastError();
         return e == cudaSuccess ? launch_after(embed_sort_kernel<I, true>, grid, kSortThreads, smem, o, st) : e;
@@ -933,6 +940,7 @@ kan_status kan_embed_backward(const kan_embed_shape* s, const void* ids, const v
     o.shift = L.shift;
     o.bins = L.bins;
     o.pieces = (int)L.pieces;
+    o.piece = L.piece;
     o.status = device_status_ptr();
     cudaError_t e = s->id_bytes == 8 ? launch_sort<int64_t>(o, cs) : launch_sort<int32_t>(o, cs);
     if (e == cudaSuccess) {
