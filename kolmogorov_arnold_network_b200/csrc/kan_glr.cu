@@ -596,21 +596,20 @@ __global__ void __launch_bounds__(32 * W, 24 / W) glr_forward_kernel(const GlrAr
             K += SPAN / kSteps * a.C;
         }
         if (at.on) {
-            T* y = Y;
+            const uint32_t step_bytes = (uint32_t)a.C * (uint32_t)sizeof(T);
+            auto row = [&](int i) { return reinterpret_cast<T*>(reinterpret_cast<char*>(Y) + (uint64_t)step_bytes * (uint32_t)i); };
             if (live == S && !cuts) {
 #pragma unroll
                 for (int i = 0; i < S; ++i) {
                     h = fmaf(fa[i], h, bb[i]);
-                    put(y, h);
-                    y += a.C;
+                    put(row(i), h);
                 }
             } else {
 #pragma unroll
                 for (int i = 0; i < S; ++i) {
                     if (cuts >> i & 1) h = 0.0f;
                     h = fmaf(fa[i], h, bb[i]);
-                    if (i < live) put(y, h);
-                    y += a.C;
+                    if (i < live) put(row(i), h);
                 }
             }
         }
@@ -771,6 +770,8 @@ __global__ void __launch_bounds__(32 * W, 16 / W) glr_backward_kernel(const GlrA
     }
     if (a.dh0 && at.on && at.rank == 0 && at.warp == 0) a.dh0[state] = run;
     if (a.part) {
+        // glr_decay_kernel may be set up (not behind the many small blocks of short sequences: 4096 single tokens 64 -> 115 us)
+        if constexpr (W == 8) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         __shared__ double red[W][32];
         red[at.warp][lane] = acc;
         __syncthreads();
@@ -791,6 +792,7 @@ __global__ void __launch_bounds__(kDecayChannels * kDecayRows) glr_decay_kernel(
                                                                                 float* __restrict__ ddecay)
 {
     __shared__ double red[kDecayRows][kDecayChannels];
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // the backward kernel has ended
     const int64_t c = (int64_t)blockIdx.x * kDecayChannels + threadIdx.x;
     double v = 0.0;
     if (c < C)
@@ -1053,10 +1055,17 @@ kan_status kan_glr_backward(const kan_glr_shape* s, const void* x, const void* r
         const int64_t n = s->batch * a.cluster;
         int rows = 1;                                    // of threads, a power of two
         while (rows < kDecayRows && rows < n) rows *= 2;
-        glr_decay_kernel<<<(unsigned)((s->channels + kDecayChannels - 1) / kDecayChannels), dim3(kDecayChannels, rows), 0, cs>>>(
-            a.part, n, s->channels, decay, ddecay);
-        count_launch();
-        e = cudaGetLastError();
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((unsigned)((s->channels + kDecayChannels - 1) / kDecayChannels));
+        cfg.blockDim = dim3(kDecayChannels, rows);
+        cfg.stream = cs;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        e = cudaLaunchKernelEx(&cfg, glr_decay_kernel, static_cast<const double*>(a.part), n, s->channels, decay, ddecay);
+        if (e == cudaSuccess) count_launch();
     }
     return e == cudaSuccess ? KAN_OK : gl_fail(KAN_ERR_CUDA, cudaGetErrorString(e));
 }
