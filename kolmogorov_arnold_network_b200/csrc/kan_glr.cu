@@ -36,7 +36,7 @@
 // Bound by instructions and their latency, not by HBM: about 70 an element
 // forward and 100 to 110 backward (four and five of them ex2, rcp or rsqrt on
 // the quarter-rate unit, 50% busy), 2.2 to 2.8 issued a cycle.  8 x 1024 x 768
-// bf16: forward 24 us, backward 42 us (8 and 14 at the copy rate);
+// bf16: forward 24 us, backward 41 us (8 and 14 at the copy rate);
 // 1 x 65536 x 1000 fp32: 280 and 363 us (165 and 285 at the copy rate).
 #include <algorithm>
 #include <atomic>
@@ -51,6 +51,8 @@ namespace {
 constexpr int kSteps = 8;         // steps per thread, and the spacing of the kept states
 
 constexpr int kMaxCluster = 16;   // blocks of a cluster
+constexpr int kUnits = 4;         // sequences' strips that a block of the kernels of one warp takes (4096 x 1 x 768 forward:
+                                  // 32 us, with 8 34, with one 52)
 constexpr int64_t kMaxChannels = 1 << 20, kMaxStride = (int64_t)1 << 40;     // (strides of steps, in elements)
 
 struct GlrArgs {
@@ -367,16 +369,20 @@ __device__ __forceinline__ float exchange(Meet<W>& s, int n, int cl, int wpos, i
     return in;
 }
 
-// Where a thread stands: its block's unit is (sequence b, strip of 32 channels).
+// Where a thread stands: its block's unit is (sequence b, strip of 32 channels); a block of kUnits units has a warp for each.
 struct Place {
     int warp, rank;
     bool on;                         // its channel exists
     int64_t b, c, c0, read;          // c0: the strip's first channel; read: the channel that is read (c, or 0 beyond the last)
-    __device__ __forceinline__ Place(const GlrArgs& a, int cl)
+    __device__ __forceinline__ Place(const GlrArgs& a, int cl, int units)
     {
         warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0);
         rank = cl > 1 ? (int)cluster_rank() : 0;
-        const int unit = blockIdx.x / cl;
+        int unit = blockIdx.x / cl;
+        if (units > 1) {
+            unit = blockIdx.x * units + warp;
+            warp = 0;
+        }
         b = unit / a.strips;
         c0 = (unit - b * a.strips) * 32;
         c = c0 + (threadIdx.x & 31);
@@ -499,13 +505,14 @@ template <typename T, bool STAGED, int S, int NA> struct Inputs {
 // Forward: S steps a thread, W warps a block, a.cluster blocks a cluster; STAGED: inputs through shared memory (W = 8), else
 // into registers.
 template <typename T, bool STAGED, int S, int W>
-__global__ void __launch_bounds__(32 * W, 24 / W) glr_forward_kernel(const GlrArgs a)
+__global__ void __launch_bounds__(W == 1 ? 32 * kUnits : 32 * W, 24 / (W == 1 ? kUnits : W)) glr_forward_kernel(const GlrArgs a)
 {
     constexpr int N = S > 1 ? 2 : 1;                     // steps side by side
     extern __shared__ __align__(128) char tiles[];       // STAGED: r, g, x
     __shared__ Meet<W> meet;
     const int side = W == 8 ? a.cluster : 1;             // blocks side by side in time
-    const Place at(a, side);
+    const Place at(a, side, W == 1 ? kUnits : 1);
+    if (W == 1 && at.b >= a.B) return;
     const int64_t SPAN = (int64_t)S * W * side;
     const int64_t mine = (int64_t)at.rank * W * S, first = mine + at.warp * S;   // the block's and the thread's first step
     const int64_t state = at.b * a.C + at.c;
@@ -621,13 +628,14 @@ __global__ void __launch_bounds__(32 * W, 24 / W) glr_forward_kernel(const GlrAr
 
 // Backward: the same split, walked from the end of the sequence.
 template <typename T, bool STAGED, int S, int W>
-__global__ void __launch_bounds__(32 * W, 16 / W) glr_backward_kernel(const GlrArgs a)
+__global__ void __launch_bounds__(W == 1 ? 32 * kUnits : 32 * W, 16 / (W == 1 ? kUnits : W)) glr_backward_kernel(const GlrArgs a)
 {
     constexpr int N = S > 1 ? 2 : 1;                     // steps side by side (a thread's begin at a kept state)
     extern __shared__ __align__(128) char tiles[];       // STAGED: r, g, x, dy
     __shared__ Meet<W> meet;
     const int side = W == 8 ? a.cluster : 1;             // blocks side by side in time
-    const Place at(a, side);
+    const Place at(a, side, W == 1 ? kUnits : 1);
+    if (W == 1 && at.b >= a.B) return;
     const int64_t SPAN = (int64_t)S * W * side;
     const int64_t mine = (int64_t)at.rank * W * S, first = mine + at.warp * S;
     const int64_t state = at.b * a.C + at.c, end = (a.T - 1) / SPAN * SPAN;      // end: the last span's first step
@@ -772,14 +780,16 @@ __global__ void __launch_bounds__(32 * W, 16 / W) glr_backward_kernel(const GlrA
     if (a.part) {
         // glr_decay_kernel may be set up (not behind the many small blocks of short sequences: 4096 single tokens 64 -> 115 us)
         if constexpr (W == 8) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-        __shared__ double red[W][32];
-        red[at.warp][lane] = acc;
-        __syncthreads();
-        if (at.warp == 0 && at.on) {
-            double v = 0.0;
-            for (int w = 0; w < W; ++w) v += red[w][lane];
-            a.part[(at.b * side + at.rank) * a.C + at.c] = v;
+        if constexpr (W > 1) {
+            __shared__ double red[W][32];
+            red[at.warp][lane] = acc;
+            __syncthreads();
+            if (at.warp == 0) {
+                acc = 0.0;
+                for (int w = 0; w < W; ++w) acc += red[w][lane];
+            }
         }
+        if (at.warp == 0 && at.on) a.part[(at.b * side + at.rank) * a.C + at.c] = acc;
     }
     if constexpr (W == 8) meet_end(waits);
 }
@@ -859,8 +869,8 @@ template <typename K> int resident(K kernel, int warps, int cluster, size_t smem
 template <typename K> cudaError_t launch(K kernel, int warps, int cluster, size_t smem, const GlrArgs& a, cudaStream_t st)
 {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(a.B * a.strips * cluster));
-    cfg.blockDim = dim3(32 * warps);
+    cfg.gridDim = dim3((unsigned)(warps == 1 ? (a.B * a.strips + kUnits - 1) / kUnits : a.B * a.strips * cluster));
+    cfg.blockDim = dim3(32 * (warps == 1 ? kUnits : warps));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute at[1];
