@@ -938,7 +938,7 @@ template <typename T, bool STAGED, bool BWD> struct Kernels {
     }
 };
 // Short sequences: a block of as many warps as hold their steps (one step: a warp whose threads take that one).  256 x 16 x 768
-// bf16 forward | backward: 12 | 22 us, with blocks of 8 warps 51 | 95; 64 x 1 x 768: 2.2 | 5 us against 14 | 27.
+// bf16 forward | backward: 12 | 22 us, with blocks of 8 warps 51 | 95; 64 x 1 x 768: 2.0 | 4.7 us against 14 | 27.
 template <typename T, bool BWD, int S, int W> cudaError_t run_short(const GlrArgs& a, cudaStream_t st)
 {
     if constexpr (BWD) return launch(glr_backward_kernel<T, false, S, W>, W, 1, 0, a, st);

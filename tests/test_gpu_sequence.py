@@ -29,6 +29,8 @@ BAR = 1e-3
 def _gpu():
     if not torch.cuda.is_available():
         pytest.skip("no CUDA device")
+    yield
+    torch.cuda.empty_cache()                                              # (some tests here hold tens of GB)
 
 
 def kan64(x, coef, G=8, lo=-1.0, hi=1.0):
@@ -287,3 +289,55 @@ def test_backward_captured_beside_an_eager_graph():
     assert torch.equal(dd, mix.decay.grad)
     # the three gradients meet in another order in autograd: two roundings of fp32 each way
     near(dw, emb.weight.grad.cpu().double(), 1e-6)
+
+
+@pytest.mark.parametrize("few", [True, False])
+def test_embedding_offsets_beyond_32_bits(few):
+    """A table of more than 2^31 elements: rows at both ends and around the border."""
+    rows, dim = (1 << 21) + 77, 1024
+    n = 40 if few else 9000
+    W = torch.zeros(rows, dim, dtype=torch.bfloat16, device="cuda")
+    ids = torch.tensor([0, rows - 1, (1 << 21) - 1, 1 << 21, rows - 1] * (n // 5), device="cuda")
+    W[ids.unique()] = torch.randn(4, dim, device="cuda").bfloat16()
+    assert torch.equal(L.embed_forward(ids, W), W[ids])
+    dY = torch.randint(-2, 3, (n, dim), device="cuda").bfloat16()
+    got = L.embed_backward(ids, dY, rows, grad_dtype=torch.bfloat16, out=W)     # small whole numbers: every sum is exact in fp32
+    for v in ids.unique().tolist():
+        assert torch.equal(got[v], dY[ids == v].float().sum(0).bfloat16())
+    assert int((got != 0).any(1).sum()) == 4
+    assert N.kan_sync_status(None) == 0
+
+
+def test_recurrence_offsets_beyond_32_bits():
+    """A sequence of more than 2^31 elements against its last part, started from the state before it."""
+    T, C, cut = (1 << 21) + 100, 1024, (1 << 21) - 8 * 52
+    torch.manual_seed(3)
+    x = torch.randn(1, T, C, dtype=torch.bfloat16, device="cuda")
+    d = torch.randn(C, device="cuda")
+    y, h, kept = L.glr_forward(x, x, x, d, keep=True)
+    # (the state that enters step `cut`, which is kept: cut is a multiple of 8)
+    y2, h2, kept2 = L.glr_forward(x[:, cut:], x[:, cut:], x[:, cut:], d, h0=kept[:, cut // 8].contiguous(), keep=True)
+    near(h, h2.cpu().double(), 1e-5)
+    near(y[:, cut:], y2.cpu().double(), 2 ** -7)
+    dy = torch.zeros_like(x)
+    dy[:, cut:] = x[:, cut:]
+    dx, dr, dg, _, _ = L.glr_backward(x, x, x, d, kept, dy, need=(True, True, True, True, False))
+    ex, er, eg, _, _ = L.glr_backward(x[:, cut:], x[:, cut:], x[:, cut:], d, kept2, dy[:, cut:], need=(True, True, True, True, False))
+    for a, b in ((dx, ex), (dr, er), (dg, eg)):
+        near(a[:, cut:], b.cpu().double(), 2 ** -7)
+    assert N.kan_sync_status(None) == 0
+
+
+def test_distillation_offsets_beyond_32_bits():
+    """Logits of more than 2^31 elements: the last rows against the same rows alone, in place."""
+    n, vocab = 33000, 65600
+    z = torch.empty(n, vocab, dtype=torch.bfloat16, device="cuda")
+    z.normal_(generator=torch.Generator(device="cuda").manual_seed(2))
+    at, t = torch.randint(0, vocab, (n, 5), device="cuda"), torch.randn(n, 5, device="cuda")
+    last = z[-7:].clone()
+    rows, want = L.distill_loss_grad(last, at[-7:].contiguous(), t[-7:].contiguous(), 2.0)
+    loss, dz = L.distill_loss_grad(z, at, t, 2.0, dlogits=z)
+    assert dz is z
+    near(loss[-7:], rows.cpu().double(), 1e-6)
+    near(dz[-7:], want.cpu().double(), 2 ** -7)                           # (blocks of another size: the last bits of the sums)
+    assert N.kan_sync_status(None) == 0
